@@ -12,14 +12,19 @@ Functions mirror the C ABI in ``include/moe_expand.h``:
     moe_act_quant, moe_gather, moe_expand_to_masked_slab,
     moe_grouped_gemm_fp8_masked, moe_act_quant_masked, moe_masked_slab_to_expand,
     moe_grouped_gemm_bf16, moe_silu_mul_bf16,
-    moe_expand_capacity, moe_expand_workspace_bytes, moe_status_string
+    moe_grouped_dgrad_bf16, moe_grouped_wgrad_bf16, moe_silu_mul_bf16_backward,
+    moe_gather_backward, moe_adamw,
+    moe_expand_capacity, moe_expand_workspace_bytes,
+    moe_grouped_wgrad_workspace_bytes, moe_status_string
 
 plus :class:`ExpandedMoE`, which allocates the buffers once for a given
 receive-buffer size and runs the five calls of a layer in order, and
 :class:`StandardMoE`, the same for the standard (non-EP) path: bf16 token
 rows in, top-k weights and the routed scaling factor applied in the gather,
-:class:`MaskedMoE`, the decode path on a fixed-height masked slab, and
-:class:`StandardBf16MoE`, the standard path with bf16 weights.
+:class:`MaskedMoE`, the decode path on a fixed-height masked slab,
+:class:`StandardBf16MoE`, the standard path with bf16 weights, and
+:class:`TrainableBf16MoE`, that path with its backward pass and an AdamW step
+(:class:`AdamWTensors` lists the tensors of one).
 """
 
 import ctypes
@@ -35,6 +40,9 @@ MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH, MOE_ERR_SCRATCH = 4, 5, 
 MOE_NOALLOC_SCRATCH_BYTES = 4 << 20
 MOE_SCALE_F32, MOE_SCALE_UE8M0, MOE_SCALE_NONE, MOE_SCALE_MXFP8 = 0, 1, 2, 3
 MOE_FLAG_CAPACITY_OVERFLOW, MOE_FLAG_EXPERT_ID_RANGE, MOE_FLAG_SLAB_OVERFLOW = 1, 2, 4
+MOE_GRAD_BF16, MOE_GRAD_F32 = 0, 1
+MOE_STATE_F32, MOE_STATE_FP8 = 0, 1
+MOE_STATE_GROUP = 128
 FMT = {"f32": MOE_SCALE_F32, "ue8m0": MOE_SCALE_UE8M0, "none": MOE_SCALE_NONE,
        "mxfp8": MOE_SCALE_MXFP8}
 
@@ -42,6 +50,8 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+
+_D = ctypes.c_double
 
 _SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -64,6 +74,14 @@ _SIGNATURES = {
     "moe_masked_slab_to_expand": (_I, [_P, _P, _I, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P]),
     "moe_grouped_gemm_bf16": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P]),
     "moe_silu_mul_bf16": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _P, _P]),
+    "moe_grouped_dgrad_bf16": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P]),
+    "moe_grouped_wgrad_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
+    "moe_grouped_wgrad_bf16": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _P, _P, _SZ,
+                                    _P]),
+    "moe_silu_mul_bf16_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P]),
+    "moe_gather_backward": (_I, [_P, _P, _P, _P, ctypes.c_float, _P, _I, _I64, _I, _I, _I64,
+                                 _P, _P, _P]),
+    "moe_adamw": (_I, [_P, _I, _P, _P, _P, _D, _D, _D, _D, _P]),
 }
 
 _lib = None
@@ -277,6 +295,169 @@ def moe_silu_mul_bf16(gate_up, m_indices, psum, status, num_experts, align, out,
     _check("moe_silu_mul_bf16", code)
 
 
+def _need(fn, name, t, dtype, shape):
+    """t is a contiguous GPU tensor of the current device, of this dtype and
+    shape (the library sees plain pointers and cannot tell)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in (dtype if isinstance(dtype, tuple)
+                                                         else (dtype,)):
+        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)}, "
+                         f"got {t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
+
+
+def _need_layout(fn, psum, status, num_experts, m_indices=None, capacity=0):
+    import torch
+    _need(fn, "psum", psum, torch.int32, (num_experts,))
+    _need(fn, "status", status, torch.int32, (2,))
+    if m_indices is not None:
+        _need(fn, "m_indices", m_indices, torch.int32, (capacity,))
+
+
+def moe_grouped_dgrad_bf16(dy, w, psum, status, align, dx, stream=None):
+    """dy [capacity, n] bf16, w [E, n, k] bf16 -> dx [capacity, k] bf16 (live rows)."""
+    import torch
+    fn, bf = "moe_grouped_dgrad_bf16", torch.bfloat16
+    (capacity, n), (E, _, k) = dy.shape, w.shape
+    _need(fn, "dy", dy, bf, (capacity, n))
+    _need(fn, "w", w, bf, (E, n, k))
+    _need(fn, "dx", dx, bf, (capacity, k))
+    _need_layout(fn, psum, status, E)
+    code = lib().moe_grouped_dgrad_bf16(_ptr(dy), _ptr(w), _ptr(psum), _ptr(status), capacity,
+                                        n, k, E, align, _ptr(dx), _stream(stream))
+    _check(fn, code)
+
+
+def moe_grouped_wgrad_workspace_bytes(capacity, n, k, num_experts) -> int:
+    return int(lib().moe_grouped_wgrad_workspace_bytes(capacity, n, k, num_experts))
+
+
+def moe_grouped_wgrad_bf16(dy, x, psum, status, align, dw, workspace=None, accumulate=False,
+                           stream=None):
+    """dy [capacity, n] bf16, x [capacity, k] bf16 -> dw [E, n, k] bf16 or fp32,
+    added to what it holds with accumulate.  workspace: a uint8 tensor of at
+    least moe_grouped_wgrad_workspace_bytes (None where that is 0)."""
+    import torch
+    fn, bf = "moe_grouped_wgrad_bf16", torch.bfloat16
+    (capacity, n), k, E = dy.shape, x.shape[1], dw.shape[0]
+    _need(fn, "dy", dy, bf, (capacity, n))
+    _need(fn, "x", x, bf, (capacity, k))
+    _need(fn, "dw", dw, (bf, torch.float32), (E, n, k))
+    _need_layout(fn, psum, status, E)
+    size = 0
+    if workspace is not None:
+        _need(fn, "workspace", workspace, torch.uint8, (workspace.numel(),))
+        size = workspace.numel()
+    code = lib().moe_grouped_wgrad_bf16(
+        _ptr(dy), _ptr(x), _ptr(psum), _ptr(status), capacity, n, k, E, align,
+        MOE_GRAD_BF16 if dw.dtype == bf else MOE_GRAD_F32, int(bool(accumulate)), _ptr(dw),
+        _ptr(workspace), size, _stream(stream))
+    _check(fn, code)
+
+
+def moe_silu_mul_bf16_backward(gate_up, dy, m_indices, psum, status, num_experts, align,
+                               d_gate_up, stream=None):
+    """gate_up [capacity, 2I] bf16, dy [capacity, I] bf16 -> d_gate_up [capacity, 2I]
+    bf16 (live rows; may be gate_up itself)."""
+    import torch
+    fn, bf = "moe_silu_mul_bf16_backward", torch.bfloat16
+    capacity, inter = dy.shape
+    _need(fn, "gate_up", gate_up, bf, (capacity, 2 * inter))
+    _need(fn, "dy", dy, bf, (capacity, inter))
+    _need(fn, "d_gate_up", d_gate_up, bf, (capacity, 2 * inter))
+    _need_layout(fn, psum, status, num_experts, m_indices, capacity)
+    code = lib().moe_silu_mul_bf16_backward(
+        _ptr(gate_up), _ptr(dy), _ptr(m_indices), _ptr(psum), _ptr(status), capacity, inter,
+        num_experts, align, _ptr(d_gate_up), _stream(stream))
+    _check(fn, code)
+
+
+def moe_gather_backward(dout, expert_out, src2dst, topk_weights, psum_recv_per_rank,
+                        d_expert_out, d_topk_weights, stream=None, routed_scaling_factor=1.0):
+    """dout [rows, H] bf16, expert_out [capacity, H] bf16 -> d_expert_out [capacity, H]
+    bf16 (rows named by src2dst) and d_topk_weights [rows, topk] fp32; the
+    latter (and then expert_out) may be None."""
+    import torch
+    fn, bf = "moe_gather_backward", torch.bfloat16
+    (rows, topk), (capacity, hidden) = src2dst.shape, d_expert_out.shape
+    _need(fn, "dout", dout, bf, (rows, hidden))
+    _need(fn, "src2dst", src2dst, torch.int32, (rows, topk))
+    _need(fn, "d_expert_out", d_expert_out, bf, (capacity, hidden))
+    if expert_out is not None:
+        _need(fn, "expert_out", expert_out, bf, (capacity, hidden))
+    for name, t in (("topk_weights", topk_weights), ("d_topk_weights", d_topk_weights)):
+        if t is not None:
+            _need(fn, name, t, torch.float32, (rows, topk))
+    if psum_recv_per_rank is not None:
+        _need(fn, "psum_recv_per_rank", psum_recv_per_rank, torch.int32,
+              (psum_recv_per_rank.numel(),))
+    code = lib().moe_gather_backward(
+        _ptr(dout), _ptr(expert_out), _ptr(src2dst), _ptr(topk_weights),
+        float(routed_scaling_factor), _ptr(psum_recv_per_rank),
+        0 if psum_recv_per_rank is None else psum_recv_per_rank.numel(), rows, hidden, topk,
+        capacity, _ptr(d_expert_out), _ptr(d_topk_weights), _stream(stream))
+    _check(fn, code)
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("master", _P), ("grad", _P), ("m", _P), ("v", _P), ("param", _P),
+                ("m_scale", _P), ("v_scale", _P), ("numel", _I64), ("grad_fmt", _I),
+                ("state_fmt", _I)]
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, listed once and used at every step.
+
+    entries: (master, grad, m, v, param, m_scale, v_scale) each.  master
+    fp32; grad bf16 or fp32; param a bf16 copy of master, or None; m and v
+    fp32 with scales None, or 8-bit codes (torch.float8_e4m3fn or uint8) with
+    fp32 scales, one per group of MOE_STATE_GROUP values.  All contiguous, of
+    one size.  The list keeps the tensors alive."""
+
+    def __init__(self, entries):
+        import torch
+        fn, f32, bf = "AdamWTensors", torch.float32, torch.bfloat16
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        self.entries = [tuple(e) for e in entries]
+        self.array = (_AdamWTensor * max(len(self.entries), 1))()
+        for i, (master, grad, m, v, param, ms, vs) in enumerate(self.entries):
+            shape, n = master.shape, master.numel()
+            fp8 = ms is not None
+            _need(fn, f"master {i}", master, f32, shape)
+            _need(fn, f"grad {i}", grad, (bf, f32), shape)
+            for name, t, sc in (("m", m, ms), ("v", v, vs)):
+                _need(fn, f"{name} {i}", t, codes if fp8 else f32, shape)
+                if fp8:
+                    _need(fn, f"{name}_scale {i}", sc, f32,
+                          (-(-n // MOE_STATE_GROUP),))
+                elif sc is not None:
+                    raise ValueError(f"{fn}: tensor {i} has one state with a scale only")
+            if param is not None:
+                _need(fn, f"param {i}", param, bf, shape)
+            self.array[i] = _AdamWTensor(
+                _ptr(master), _ptr(grad), _ptr(m), _ptr(v), _ptr(param), _ptr(ms), _ptr(vs), n,
+                MOE_GRAD_BF16 if grad.dtype == bf else MOE_GRAD_F32,
+                MOE_STATE_FP8 if fp8 else MOE_STATE_F32)
+
+
+def moe_adamw(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+              grad_scale=None, stream=None):
+    """One AdamW step over an :class:`AdamWTensors`.  step int64 [1] (the number
+    of this step, from 1), lr and grad_scale fp32 [1], all on the GPU."""
+    import torch
+    fn = "moe_adamw"
+    _need(fn, "step", step, torch.int64, (1,))
+    _need(fn, "lr", lr, torch.float32, (1,))
+    if grad_scale is not None:
+        _need(fn, "grad_scale", grad_scale, torch.float32, (1,))
+    code = lib().moe_adamw(tensors.array, len(tensors.entries), _ptr(step), _ptr(lr),
+                           _ptr(grad_scale), beta1, beta2, eps, weight_decay, _stream(stream))
+    _check(fn, code)
+
+
 class ExpandedMoE:
     """Buffers for one receive-buffer size, and the layer's five calls.
 
@@ -484,3 +665,84 @@ class StandardBf16MoE:
         self.experts(stream)
         self.gather(topk_weights, psum_recv_per_rank, out, stream)
         return out
+
+
+class TrainableBf16MoE(StandardBf16MoE):
+    """The bf16-weight path with its backward pass and an AdamW step.
+
+    __call__ is the forward pass; it leaves the expanded rows, the gate_up
+    rows, SiLU*up and the down rows in the object's buffers, and backward()
+    reads them.  w13 and w2 are the bf16 copies that update() rewrites from
+    the fp32 masters master13 and master2.  grad: 'f32' or 'bf16' weight
+    gradients (dw13, dw2); state: 'f32' or 'fp8' optimiser states."""
+
+    def __init__(self, rows, topk, w13, w2, align=128, routed_scaling_factor=1.0,
+                 grad="f32", state="f32", lr=1e-4, device="cuda"):
+        import torch
+        super().__init__(rows, topk, w13, w2, align, routed_scaling_factor, device)
+        if grad not in ("f32", "bf16") or state not in ("f32", "fp8"):
+            raise ValueError("TrainableBf16MoE: grad is 'f32' or 'bf16', state 'f32' or 'fp8'")
+        cap, bf, f32 = self.capacity, torch.bfloat16, torch.float32
+        # d of the down rows, and, once those have been used, of the expanded rows
+        self.d_rows = torch.empty((cap, self.H), dtype=bf, device=device)
+        self.d_y = torch.empty((cap, self.I), dtype=bf, device=device)
+        self.d_gate_up = torch.empty((cap, 2 * self.I), dtype=bf, device=device)
+        gdt = f32 if grad == "f32" else bf
+        self.dw13 = torch.zeros(w13.shape, dtype=gdt, device=device)
+        self.dw2 = torch.zeros(w2.shape, dtype=gdt, device=device)
+        need = max(moe_grouped_wgrad_workspace_bytes(cap, 2 * self.I, self.H, self.E),
+                   moe_grouped_wgrad_workspace_bytes(cap, self.H, self.I, self.E))
+        self.wgrad_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        self.master13, self.master2 = w13.float(), w2.float()
+        self.step = torch.zeros(1, dtype=torch.int64, device=device)
+        self.lr = torch.full((1,), float(lr), dtype=f32, device=device)
+        self.states, entries = [], []
+        for master, dw, w in ((self.master13, self.dw13, w13), (self.master2, self.dw2, w2)):
+            sdt = f32 if state == "f32" else torch.float8_e4m3fn
+            m, v = (torch.zeros(w.shape, dtype=f32, device=device).to(sdt) for _ in range(2))
+            groups = -(-w.numel() // MOE_STATE_GROUP)
+            ms, vs = (None if state == "f32" else
+                      torch.zeros(groups, dtype=f32, device=device) for _ in range(2))
+            self.states.append((m, v, ms, vs))
+            entries.append((master, dw, m, v, w, ms, vs))
+        self.tensors = AdamWTensors(entries)
+
+    def backward(self, dout, topk_weights, psum_recv_per_rank=None, dx=None,
+                 d_topk_weights=None, accumulate=False, stream=None):
+        """Gradients of the last forward call (its topk_weights and
+        psum_recv_per_rank): returns (dx [rows, H] bf16, d_topk_weights
+        [rows, topk] fp32) and leaves the weights' in dw13 and dw2, added to
+        what they hold with accumulate."""
+        import torch
+        if dx is None:
+            dx = torch.empty((self.rows, self.H), dtype=torch.bfloat16, device=dout.device)
+        if d_topk_weights is None:
+            d_topk_weights = torch.empty((self.rows, self.topk), dtype=torch.float32,
+                                         device=dout.device)
+        lay = (self.psum, self.status, self.align)
+        moe_gather_backward(dout, self.down, self.src2dst, topk_weights, psum_recv_per_rank,
+                            self.d_rows, d_topk_weights, stream,
+                            routed_scaling_factor=self.routed_scaling_factor)
+        moe_grouped_wgrad_bf16(self.d_rows, self.y, *lay, self.dw2, self.wgrad_workspace,
+                               accumulate, stream)
+        moe_grouped_dgrad_bf16(self.d_rows, self.w2, *lay, self.d_y, stream)
+        moe_silu_mul_bf16_backward(self.gate_up, self.d_y, self.m_indices, self.psum,
+                                   self.status, self.E, self.align, self.d_gate_up, stream)
+        moe_grouped_wgrad_bf16(self.d_gate_up, self.ex, *lay, self.dw13, self.wgrad_workspace,
+                               accumulate, stream)
+        moe_grouped_dgrad_bf16(self.d_gate_up, self.w13, *lay, self.d_rows, stream)
+        moe_gather(self.d_rows, self.src2dst, None, psum_recv_per_rank, dx, stream)
+        return dx, d_topk_weights
+
+    def update(self, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=None,
+               stream=None):
+        """One AdamW step on both weights with the gradients in dw13 and dw2 and
+        the learning rate in the lr tensor; counts step up first."""
+        import torch
+        if stream is None:
+            self.step.add_(1)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(int(stream))):
+                self.step.add_(1)
+        moe_adamw(self.tensors, self.step, self.lr, beta1, beta2, eps, weight_decay, grad_scale,
+                  stream)

@@ -1,0 +1,320 @@
+// moe_adamw: one AdamW step with decoupled weight decay over many tensors,
+// with fp32 or 8-bit states.
+//
+//   g = grad * grad_scale
+//   m = m * b1 + g * (1 - b1),   v = v * b2 + g^2 * (1 - b2)
+//   master -= lr * (m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps) + wd * master)
+//
+// 8-bit states: groups of 128 consecutive values as E4M3 codes and an fp32
+// scale.  The second moment is kept as its root r = sqrt(v): the codes cover
+// 448 / 2^-9 = 2.3e5 between the largest and the smallest value of a group,
+// for r that is 5e10 in v.  The codes are decided in fp32 with every
+// operation rounded in the order above (no contraction), so they are the ones
+// that the same sequence of elementwise fp32 operations gives.
+//
+// HBM-bound: everything is read once and written once.  A workgroup takes a
+// chunk of one tensor; the list of tensors travels in the kernel's arguments
+// (nothing is copied to the device), up to kMaxTensors per launch.  Each lane
+// owns 8 consecutive values, so a group of 128 is 16 lanes and its maximum is
+// four exchanges.
+#include "common.hpp"
+
+// Each operation rounded by itself: plain operators under this pragma (the
+// header's __fmul_rn and __fadd_rn may still be joined into one fma).
+#pragma clang fp contract(off)
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;                              // values per lane and pass
+constexpr int kPasses = 4;
+constexpr int kChunk = kThreads * kVec * kPasses;    // values per workgroup
+constexpr int kMaxTensors = 32;                      // per launch (kernel arguments: 4 KB)
+constexpr float kFp8Max = 448.f, kCodeMin = 0x1p-9f, kAmaxFloor = 0x1p-100f;
+static_assert(MOE_STATE_GROUP == 128 && kChunk % MOE_STATE_GROUP == 0, "groups fill chunks");
+
+struct Batch {
+  moe_adamw_tensor t[kMaxTensors];
+  int64_t first[kMaxTensors + 1];  // first workgroup of each tensor
+  int count;
+};
+static_assert(sizeof(Batch) <= 3584, "kernel argument size");
+
+struct Hyper {
+  double beta1, beta2;
+  float b1, one_b1, b2, one_b2, eps, wd;
+};
+
+// b^t in fp64 by repeated squaring (t >= 1 is the step's number).
+__device__ __forceinline__ double pow_int(double b, int64_t t) {
+  double r = 1.0;
+  for (uint64_t n = t > 0 ? (uint64_t)t : 0; n; n >>= 1) {
+    if (n & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+struct Step {
+  float c1, c2, lr, gs;
+};
+
+__device__ __forceinline__ void update(const Hyper& h, const Step& st, float grad, float& p,
+                                       float& m, float& v) {
+  const float g = grad * st.gs;
+  m = m * h.b1 + g * h.one_b1;
+  v = v * h.b2 + (g * g) * h.one_b2;
+  const float u = (m / st.c1) / (sqrtf(v / st.c2) + h.eps);
+  p = p - (u + p * h.wd) * st.lr;
+}
+
+// Largest magnitude of the 16 lanes that hold a group, not below the floor.
+__device__ __forceinline__ float group_amax(const float (&x)[kVec]) {
+  float a = kAmaxFloor;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) a = fmaxf(a, fabsf(x[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor(a, o, kWave));
+  return a;
+}
+
+// Codes of x and their group's scale.
+template <bool kPositive>
+__device__ __forceinline__ uint2 encode(const float (&x)[kVec], float& scale) {
+  const float amax = group_amax(x);
+  scale = amax * (1.f / kFp8Max);
+  const float inv = (1.f / amax) * kFp8Max;
+  float q[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    q[i] = x[i] * inv;
+    if (kPositive && x[i] > 0.f) q[i] = fmaxf(q[i], kCodeMin);
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+__device__ __forceinline__ void decode(uint2 c, float scale, float (&x)[kVec]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
+  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+  const f2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
+  const f2 e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+  const float y[kVec] = {a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) x[i] = y[i] * scale;
+}
+
+// n (1..kVec) consecutive values at p + i; whole vectors where n == kVec (the
+// base is 16-byte aligned and i a multiple of kVec).
+__device__ __forceinline__ void load_f32(const float* p, int64_t i, int n, float (&x)[kVec]) {
+  if (n == kVec) {
+    const float4 a = *reinterpret_cast<const float4*>(p + i);
+    const float4 b = *reinterpret_cast<const float4*>(p + i + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = j < n ? p[i + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void store_f32(float* p, int64_t i, int n, const float (&x)[kVec]) {
+  if (n == kVec) {
+    *reinterpret_cast<float4*>(p + i) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + i + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (j < n) p[i + j] = x[j];
+  }
+}
+__device__ __forceinline__ void load_bf16(const uint16_t* p, int64_t i, int n, float (&x)[kVec]) {
+  if (n == kVec) {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(a[j] << 16);
+      x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = j < n ? bf16_to_f32(p[i + j]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store_bf16(uint16_t* p, int64_t i, int n, const float (&x)[kVec]) {
+  if (n == kVec) {
+    u32x4 a;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      a[j] = (uint32_t)f32_to_bf16_rne(x[2 * j]) | ((uint32_t)f32_to_bf16_rne(x[2 * j + 1]) << 16);
+    *reinterpret_cast<u32x4*>(p + i) = a;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (j < n) p[i + j] = f32_to_bf16_rne(x[j]);
+  }
+}
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t i, int n) {
+  if (n == kVec) return *reinterpret_cast<const uint2*>(p + i);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < kVec; ++j)
+    if (j < n) w[j / 4] |= (uint32_t)p[i + j] << (8 * (j % 4));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int n, uint2 c) {
+  if (n == kVec) {
+    *reinterpret_cast<uint2*>(p + i) = c;
+  } else {
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (j < n) p[i + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+  }
+}
+
+template <bool kGradF32, bool kFp8>
+__device__ __forceinline__ void run_chunk(const moe_adamw_tensor& t, int64_t base,
+                                          const Hyper& h, const Step& st) {
+#pragma unroll 1
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int64_t i = base + (int64_t)(pass * kThreads + threadIdx.x) * kVec;
+    // Lanes past the end keep 0s and take part in their group's maximum.
+    const int n = (int)max((int64_t)0, min((int64_t)kVec, t.numel - i));
+    float g[kVec] = {}, p[kVec] = {}, m[kVec] = {}, v[kVec] = {};
+    if (n > 0) {
+      if (kGradF32) load_f32((const float*)t.grad, i, n, g);
+      else load_bf16((const uint16_t*)t.grad, i, n, g);
+      load_f32(t.master, i, n, p);
+      if constexpr (kFp8) {
+        const uint2 cm = load_codes((const uint8_t*)t.m, i, n);
+        const uint2 cv = load_codes((const uint8_t*)t.v, i, n);
+        decode(cm, t.m_scale[i / MOE_STATE_GROUP], m);
+        decode(cv, t.v_scale[i / MOE_STATE_GROUP], v);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = v[j] * v[j];
+      } else {
+        load_f32((const float*)t.m, i, n, m);
+        load_f32((const float*)t.v, i, n, v);
+      }
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) update(h, st, g[j], p[j], m[j], v[j]);
+      store_f32(t.master, i, n, p);
+      if (t.param) store_bf16((uint16_t*)t.param, i, n, p);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = sqrtf(v[j]);
+      if (n < kVec) {  // values past the end have been updated too: back to 0
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (j >= n) m[j] = 0.f, v[j] = 0.f;
+      }
+      float sm, sv;
+      const uint2 cm = encode<false>(m, sm), cv = encode<true>(v, sv);
+      if (n > 0) {
+        store_codes((uint8_t*)t.m, i, n, cm);
+        store_codes((uint8_t*)t.v, i, n, cv);
+        if ((threadIdx.x & 15) == 0) {
+          t.m_scale[i / MOE_STATE_GROUP] = sm;
+          t.v_scale[i / MOE_STATE_GROUP] = sv;
+        }
+      }
+    } else if (n > 0) {
+      store_f32((float*)t.m, i, n, m);
+      store_f32((float*)t.v, i, n, v);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch b, const Hyper h,
+                                                         const int64_t* __restrict__ step,
+                                                         const float* __restrict__ lr,
+                                                         const float* __restrict__ grad_scale) {
+  int q = 0;
+  while (q + 1 < b.count && (int64_t)blockIdx.x >= b.first[q + 1]) ++q;  // uniform
+  const moe_adamw_tensor& t = b.t[q];
+  const int64_t base = ((int64_t)blockIdx.x - b.first[q]) * kChunk;
+  const int64_t n = *step;
+  const Step st = {(float)(1.0 - pow_int(h.beta1, n)), (float)(1.0 - pow_int(h.beta2, n)), *lr,
+                   grad_scale ? *grad_scale : 1.f};
+  if (t.state_fmt == MOE_STATE_FP8) {
+    if (t.grad_fmt == MOE_GRAD_F32) run_chunk<true, true>(t, base, h, st);
+    else run_chunk<false, true>(t, base, h, st);
+  } else {
+    if (t.grad_fmt == MOE_GRAD_F32) run_chunk<true, false>(t, base, h, st);
+    else run_chunk<false, false>(t, base, h, st);
+  }
+}
+
+// One tensor's arguments; MOE_OK also for an empty one.
+moe_status check_tensor(const moe_adamw_tensor& t) {
+  if (t.numel < 0 || t.numel > (1LL << 40)) return MOE_ERR_SHAPE;
+  if ((t.grad_fmt != MOE_GRAD_BF16 && t.grad_fmt != MOE_GRAD_F32) ||
+      (t.state_fmt != MOE_STATE_F32 && t.state_fmt != MOE_STATE_FP8))
+    return MOE_ERR_UNSUPPORTED;
+  if (t.numel == 0) return MOE_OK;
+  if (!t.master || !t.grad || !t.m || !t.v) return MOE_ERR_NULL;
+  if (t.state_fmt == MOE_STATE_FP8 && (!t.m_scale || !t.v_scale)) return MOE_ERR_NULL;
+  if (((uintptr_t)t.master % 16) || ((uintptr_t)t.grad % 16) || ((uintptr_t)t.m % 16) ||
+      ((uintptr_t)t.v % 16) || ((uintptr_t)t.param % 16))
+    return MOE_ERR_ALIGNMENT;
+  if (t.state_fmt == MOE_STATE_FP8 && (((uintptr_t)t.m_scale % 4) || ((uintptr_t)t.v_scale % 4)))
+    return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors,
+                                const int64_t* step, const float* lr, const float* grad_scale,
+                                double beta1, double beta2, double eps, double weight_decay,
+                                void* stream) {
+  if (num_tensors < 0) return MOE_ERR_SHAPE;
+  // Written so that NaN fails too.
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+      !(eps >= 0.0 && eps <= 3.4e38) || !(weight_decay >= 0.0 && weight_decay <= 3.4e38))
+    return MOE_ERR_SHAPE;
+  if (!step || !lr || (num_tensors > 0 && !tensors)) return MOE_ERR_NULL;
+  if (((uintptr_t)step % 8) || ((uintptr_t)lr % 4) || ((uintptr_t)grad_scale % 4))
+    return MOE_ERR_ALIGNMENT;
+  for (int i = 0; i < num_tensors; ++i) {
+    const moe_status s = check_tensor(tensors[i]);
+    if (s != MOE_OK) return s;
+    const uintptr_t a = (uintptr_t)tensors[i].master, an = (uintptr_t)tensors[i].numel * 4;
+    for (int j = 0; j < i; ++j) {  // two updates of one value would race
+      const uintptr_t c = (uintptr_t)tensors[j].master, cn = (uintptr_t)tensors[j].numel * 4;
+      if (an && cn && a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
+    }
+  }
+  const Hyper h = {beta1, beta2, (float)beta1, (float)(1.0 - beta1), (float)beta2,
+                   (float)(1.0 - beta2), (float)eps, (float)weight_decay};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  for (int i = 0; i < num_tensors;) {
+    Batch b;
+    b.count = 0;
+    b.first[0] = 0;
+    int64_t blocks = 0;
+    constexpr int64_t kMaxBlocks = 1LL << 30;  // one tensor has at most 2^27
+    for (; i < num_tensors && b.count < kMaxTensors; ++i) {
+      const int64_t n = (tensors[i].numel + kChunk - 1) / kChunk;
+      if (n == 0) continue;
+      if (b.count > 0 && blocks + n > kMaxBlocks) break;
+      b.t[b.count] = tensors[i];
+      blocks += n;
+      b.first[++b.count] = blocks;
+    }
+    if (b.count == 0) break;
+    hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, b, h, step, lr,
+                       grad_scale);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
+  }
+  return MOE_OK;
+}

@@ -36,6 +36,23 @@
  *                                weights
  *   moe_gather                   combine with weight 1
  *
+ * Training the bf16 path: after the forward calls (moe_expand_layout_bf16,
+ * moe_grouped_gemm_bf16, moe_silu_mul_bf16, moe_grouped_gemm_bf16,
+ * moe_gather, whose intermediate buffers the caller keeps), in call order:
+ *   moe_gather_backward          d out -> d of the down rows and of the
+ *                                top-k weights
+ *   moe_grouped_wgrad_bf16       d w2 from the down rows' d and SiLU*up
+ *   moe_grouped_dgrad_bf16       d of SiLU*up
+ *   moe_silu_mul_bf16_backward   d of the gate_up rows
+ *   moe_grouped_wgrad_bf16       d w13 from them and the expanded rows
+ *   moe_grouped_dgrad_bf16       d of the expanded rows
+ *   moe_gather                   (weights NULL, factor 1) d of the tokens
+ *   moe_adamw                    AdamW over all the weights at once
+ * None of these reads or writes alignment pad rows or rows past the total,
+ * so they may hold anything.  A captured sequence may be replayed on new
+ * routings: every row count, the step number and the learning rate are read
+ * on the device.
+ *
  * Sources, by page and section:
  *  [P1] SGLang pull request 37261, "feat(deepep_v2): expanded (do_expand=True)
  *       prefill dispatch for DeepEP-V2": Modifications/Core (row labels from
@@ -131,6 +148,17 @@ typedef enum {
                                most 256 experts), moe_act_quant (no fold)  */
 } moe_scale_fmt;
 
+typedef enum {
+  MOE_GRAD_BF16 = 0,        /* gradients in bf16                          */
+  MOE_GRAD_F32 = 1          /* gradients in fp32                          */
+} moe_grad_fmt;
+
+typedef enum {
+  MOE_STATE_F32 = 0,        /* optimiser states in fp32                   */
+  MOE_STATE_FP8 = 1         /* optimiser states as fp8 codes with an fp32
+                               scale per group of MOE_STATE_GROUP values  */
+} moe_state_fmt;
+
 /* Bits of status[1] written by moe_expand_layout. */
 #define MOE_FLAG_CAPACITY_OVERFLOW 1 /* total rows > capacity: rows at or past
                                         the capacity were dropped (their slots
@@ -146,6 +174,7 @@ typedef enum {
 #define MOE_MAX_TOPK 32
 #define MOE_MIN_ALIGN 16
 #define MOE_MAX_ALIGN 1024
+#define MOE_STATE_GROUP 128
 /* Size of moe_expand_layout_noalloc's static per-GPU scratch: calls with
  * moe_expand_workspace_bytes(rows, topk, num_experts) above it are refused
  * (roughly rows * num_experts <= 15 million). */
@@ -449,6 +478,137 @@ moe_status moe_masked_slab_to_expand(
     const void* slab_out, const int32_t* masked_m, int max_m, const int32_t* psum,
     const int32_t* status, const int32_t* m_indices, const float* row_weight,
     int64_t capacity, int hidden, int num_experts, int align, void* out, void* stream);
+
+/*
+ * Input gradient of moe_grouped_gemm_bf16: for every live expanded row m of
+ * expert e (m < psum[e], m < min(status[0], capacity))
+ *   dx[m, t] = bf16( sum_j dy[m, j] * w[e, j, t] )
+ * accumulated in fp32.  n and k are those of the forward call: dy is the
+ * gradient of its output.
+ *   dy   [capacity, n] bf16, w [num_experts, n, k] bf16 as in the forward
+ *        call (not transposed), psum, status as there
+ *   dx   [capacity, k] bf16; rows that are not live are not written
+ * Rows of dy that are not live do not enter any result.
+ * Sizes, alignment and errors as moe_grouped_gemm_bf16 (n % 128 == 0,
+ * k % 64 == 0, and n / 64, k / 64 <= 511).
+ */
+moe_status moe_grouped_dgrad_bf16(
+    const void* dy, const void* w, const int32_t* psum, const int32_t* status,
+    int64_t capacity, int n, int k, int num_experts, int align, void* dx,
+    void* stream);
+
+/*
+ * Host, pure.  Bytes of device workspace moe_grouped_wgrad_bf16 needs (0 for
+ * most sizes: only few, long reductions are split over workgroups and joined
+ * through it).  Returns 0 on bad input.
+ */
+size_t moe_grouped_wgrad_workspace_bytes(int64_t capacity, int n, int k, int num_experts);
+
+/*
+ * Weight gradient of moe_grouped_gemm_bf16: for every expert e
+ *   dw[e, j, t] = sum over the live rows m of e of dy[m, j] * x[m, t]
+ * accumulated in fp32 (the order of the sum depends on the sizes and the
+ * rows of e only: equal calls give equal bits) and rounded once to `fmt`.
+ * accumulate != 0: the sum is added to dw's value in fp32 first (dw holds
+ * the gradients of earlier calls).  An expert without live rows gets 0, or
+ * keeps its values when accumulating.
+ *   dy   [capacity, n] bf16, x [capacity, k] bf16 (the forward call's a)
+ *   dw   [num_experts, n, k] in `fmt`
+ * Rows that are not live do not enter any result, whatever they hold.
+ * workspace: device, >= moe_grouped_wgrad_workspace_bytes(...) bytes,
+ * 256-byte aligned, no initialisation needed; may be NULL when that is 0.
+ * Calls that may overlap need a workspace each.
+ * Sizes and errors as moe_grouped_dgrad_bf16; a short workspace is
+ * MOE_ERR_WORKSPACE.  Buffers 16-byte aligned.
+ */
+moe_status moe_grouped_wgrad_bf16(
+    const void* dy, const void* x, const int32_t* psum, const int32_t* status,
+    int64_t capacity, int n, int k, int num_experts, int align, moe_grad_fmt fmt,
+    int accumulate, void* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of moe_silu_mul_bf16, for every live expanded row:
+ *   gate_up    [capacity, 2*inter] bf16: g = first half, u = second, as given
+ *              to the forward call
+ *   dy         [capacity, inter] bf16
+ *   d_gate_up  [capacity, 2*inter] bf16: with s = 1 / (1 + exp(-g)) in fp32
+ *              d g = dy * u * (s * (1 + g * (1 - s))),  d u = dy * (g * s),
+ *              each rounded once to bf16
+ * Rows that are not live are not written.  d_gate_up may be gate_up itself
+ * (each value is read before its place is written).
+ * Sizes and errors as moe_silu_mul_bf16.
+ */
+moe_status moe_silu_mul_bf16_backward(
+    const void* gate_up, const void* dy, const int32_t* m_indices, const int32_t* psum,
+    const int32_t* status, int64_t capacity, int inter, int num_experts, int align,
+    void* d_gate_up, void* stream);
+
+/*
+ * Gradient of moe_gather (out[r] = f * sum_k c[r,k] * expert_out[src2dst[r,k]]):
+ *   dout            [rows, hidden] bf16
+ *   expert_out, src2dst, topk_weights, routed_scaling_factor,
+ *   psum_recv_per_rank, num_src_ranks  as given to the forward call;
+ *                   src2dst names each expanded row at most once, as
+ *                   moe_expand_layout writes it
+ *   d_expert_out    [capacity, hidden] bf16: for each live slot (r, k),
+ *                   r < R_v, row src2dst[r,k] = bf16( (f * c[r,k]) * dout[r] ),
+ *                   c = 1 when topk_weights is NULL; other rows are not written
+ *   d_topk_weights  [rows, topk] fp32: f * sum_h dout[r,h] *
+ *                   expert_out[src2dst[r,k], h], summed in fp32; 0 for the
+ *                   slots of valid rows that are not live; rows >= R_v are
+ *                   not written.  May be NULL (expert_out is then not read
+ *                   and may be NULL too).
+ * Sizes and errors as moe_gather.
+ */
+moe_status moe_gather_backward(
+    const void* dout, const void* expert_out, const int32_t* src2dst,
+    const float* topk_weights, float routed_scaling_factor,
+    const int32_t* psum_recv_per_rank, int num_src_ranks, int64_t rows, int hidden,
+    int topk, int64_t capacity, void* d_expert_out, float* d_topk_weights, void* stream);
+
+/* One tensor of moe_adamw (device pointers, 16-byte aligned; grad in the
+ * given format; all hold numel values in the same order). */
+typedef struct {
+  float* master;            /* fp32 parameters, updated                     */
+  const void* grad;         /* gradient, bf16 or fp32                       */
+  void* m;                  /* first moment: fp32, or fp8 codes             */
+  void* v;                  /* second moment: fp32, or fp8 codes of its root */
+  void* param;              /* bf16 copy of the updated master, or NULL     */
+  float* m_scale;           /* MOE_STATE_FP8: [ceil(numel/128)] fp32        */
+  float* v_scale;           /* MOE_STATE_FP8: [ceil(numel/128)] fp32        */
+  int64_t numel;
+  moe_grad_fmt grad_fmt;
+  moe_state_fmt state_fmt;
+} moe_adamw_tensor;
+
+/*
+ * One AdamW step over num_tensors tensors (host array, read before the call
+ * returns), with decoupled weight decay.  With t = *step (the number of this
+ * step, from 1), in fp32, each operation rounded:
+ *   g = grad * *grad_scale                       (grad_scale NULL: g = grad)
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * g) * (1 - beta2)
+ *   master -= *lr * (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)
+ *                    + weight_decay * master)
+ *   param = bf16(master)
+ * step (int64), lr and grad_scale (fp32) are device scalars: a captured call
+ * takes their values at each replay.
+ * MOE_STATE_FP8: m and r = sqrt(v) are kept per group of 128 consecutive
+ * values as E4M3 codes and a scale: amax = max(max |x| over the group,
+ * 2^-100), scale = amax * fl(1/448), code = fp8_rne(x * (fl(1/amax) * 448));
+ * a positive r gets at least the smallest positive code (2^-9), since a second
+ * moment of 0 would let the step divide by eps alone.  The step itself uses m and v
+ * before they are coded.  An infinite value spoils its group.
+ * The last group of a tensor may be short.
+ * Errors: numel < 0 or > 2^40, num_tensors < 0, hyperparameters
+ * out of range (beta in [0, 1), eps >= 0, weight_decay >= 0, all finite):
+ * MOE_ERR_SHAPE; unknown formats, or masters that overlap:
+ * MOE_ERR_UNSUPPORTED.  Tensors with numel 0 are skipped.
+ */
+moe_status moe_adamw(
+    const moe_adamw_tensor* tensors, int num_tensors, const int64_t* step,
+    const float* lr, const float* grad_scale, double beta1, double beta2, double eps,
+    double weight_decay, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,7 @@ It is a plain, slow, obviously-correct restatement of what the pages define:
              gather), and a per-token brute force that uses no layout at all.
 * ``masked`` the decode path's fixed-height masked slab: the bridges from
              and back to the expanded layout and the layer on the slab.
+* ``backward`` gradients of the bf16 path in float64 and the AdamW step.
 
 Sources (cited by title and section in every function):
 
@@ -40,4 +41,4 @@ quantisation at rounding ties after a different fp32 accumulation order are
 bounded only by the output tolerance (see the layer tests).
 """
 
-from . import fp8, quant, layout, layer, masked  # noqa: F401
+from . import fp8, quant, layout, layer, masked, backward  # noqa: F401

@@ -1,0 +1,175 @@
+"""Argument checks of the training entry points (no GPU: every call fails a
+host-side check before anything is launched, or has nothing to do)."""
+
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import expanded_dispatch_layout_amd as M  # noqa: E402
+
+FAKE = 0x100000          # 16-byte aligned, never dereferenced
+MIS = FAKE + 4
+
+
+def _dgrad(**kw):
+    a = dict(dy=FAKE, w=FAKE, psum=FAKE, st=FAKE, cap=320, n=256, k=256, E=4, align=64, dx=FAKE)
+    a.update(kw)
+    return M.lib().moe_grouped_dgrad_bf16(a["dy"], a["w"], a["psum"], a["st"], a["cap"], a["n"],
+                                          a["k"], a["E"], a["align"], a["dx"], None)
+
+
+def _wgrad(**kw):
+    a = dict(dy=FAKE, x=FAKE, psum=FAKE, st=FAKE, cap=320, n=256, k=256, E=4, align=64, fmt=0,
+             acc=0, dw=FAKE, ws=None, wsb=0)
+    a.update(kw)
+    return M.lib().moe_grouped_wgrad_bf16(
+        a["dy"], a["x"], a["psum"], a["st"], a["cap"], a["n"], a["k"], a["E"], a["align"],
+        a["fmt"], a["acc"], a["dw"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("f", [_dgrad, _wgrad])
+def test_products_reject_bad_arguments(f):
+    assert f(n=100) == M.MOE_ERR_SHAPE
+    assert f(n=192) == M.MOE_ERR_SHAPE
+    assert f(k=96) == M.MOE_ERR_SHAPE
+    assert f(k=0) == M.MOE_ERR_SHAPE
+    assert f(cap=-64) == M.MOE_ERR_SHAPE
+    assert f(cap=100) == M.MOE_ERR_SHAPE
+    assert f(E=0) == M.MOE_ERR_SHAPE
+    assert f(E=1025) == M.MOE_ERR_SHAPE
+    assert f(align=48) == M.MOE_ERR_UNSUPPORTED
+    assert f(align=8) == M.MOE_ERR_UNSUPPORTED
+    assert f(k=512 * 64) == M.MOE_ERR_UNSUPPORTED
+    assert f(n=512 * 64) == M.MOE_ERR_UNSUPPORTED
+    assert f(psum=None) == M.MOE_ERR_NULL
+    assert f(st=None) == M.MOE_ERR_NULL
+    assert f(dy=None) == M.MOE_ERR_NULL
+    assert f(dy=MIS) == M.MOE_ERR_ALIGNMENT
+
+
+def test_product_operands():
+    assert _dgrad(w=None) == M.MOE_ERR_NULL
+    assert _dgrad(dx=None) == M.MOE_ERR_NULL
+    assert _dgrad(dx=MIS) == M.MOE_ERR_ALIGNMENT
+    assert _dgrad(w=MIS) == M.MOE_ERR_ALIGNMENT
+    assert _dgrad(cap=0) == M.MOE_OK                 # nothing to do, nothing launched
+    assert _wgrad(x=None) == M.MOE_ERR_NULL
+    assert _wgrad(dw=None) == M.MOE_ERR_NULL
+    assert _wgrad(x=MIS) == M.MOE_ERR_ALIGNMENT
+    assert _wgrad(dw=MIS) == M.MOE_ERR_ALIGNMENT
+    assert _wgrad(fmt=2) == M.MOE_ERR_UNSUPPORTED
+
+
+def test_silu_backward_rejects_bad_arguments():
+    def f(**kw):
+        a = dict(gu=FAKE, dy=FAKE, mi=FAKE, psum=FAKE, st=FAKE, cap=320, inter=128, E=4,
+                 align=64, out=FAKE)
+        a.update(kw)
+        return M.lib().moe_silu_mul_bf16_backward(
+            a["gu"], a["dy"], a["mi"], a["psum"], a["st"], a["cap"], a["inter"], a["E"],
+            a["align"], a["out"], None)
+    assert f(inter=100) == M.MOE_ERR_SHAPE
+    assert f(cap=100) == M.MOE_ERR_SHAPE
+    assert f(E=0) == M.MOE_ERR_SHAPE
+    assert f(align=48) == M.MOE_ERR_UNSUPPORTED
+    assert f(mi=None) == M.MOE_ERR_NULL
+    assert f(st=None) == M.MOE_ERR_NULL
+    assert f(dy=None) == M.MOE_ERR_NULL
+    assert f(out=None) == M.MOE_ERR_NULL
+    assert f(dy=MIS) == M.MOE_ERR_ALIGNMENT
+    assert f(out=MIS) == M.MOE_ERR_ALIGNMENT
+    assert f(cap=0) == M.MOE_OK
+
+
+def test_gather_backward_rejects_bad_arguments():
+    def f(**kw):
+        a = dict(do=FAKE, eo=FAKE, s2d=FAKE, w=None, f=1.0, prank=None, nsrc=0, rows=64,
+                 hidden=256, topk=2, cap=320, deo=FAKE, dw=FAKE)
+        a.update(kw)
+        return M.lib().moe_gather_backward(
+            a["do"], a["eo"], a["s2d"], a["w"], a["f"], a["prank"], a["nsrc"], a["rows"],
+            a["hidden"], a["topk"], a["cap"], a["deo"], a["dw"], None)
+    assert f(f=float("nan")) == M.MOE_ERR_UNSUPPORTED
+    assert f(f=float("-inf")) == M.MOE_ERR_UNSUPPORTED
+    assert f(hidden=100) == M.MOE_ERR_SHAPE
+    assert f(hidden=8320) == M.MOE_ERR_UNSUPPORTED
+    assert f(topk=0) == M.MOE_ERR_SHAPE
+    assert f(topk=33) == M.MOE_ERR_SHAPE
+    assert f(rows=-1) == M.MOE_ERR_SHAPE
+    assert f(prank=FAKE, nsrc=0) == M.MOE_ERR_SHAPE
+    assert f(s2d=None) == M.MOE_ERR_NULL
+    assert f(do=None) == M.MOE_ERR_NULL
+    assert f(deo=None) == M.MOE_ERR_NULL
+    assert f(eo=None) == M.MOE_ERR_NULL              # needed for d_topk_weights
+    assert f(do=MIS) == M.MOE_ERR_ALIGNMENT
+    assert f(deo=MIS) == M.MOE_ERR_ALIGNMENT
+    assert f(dw=FAKE + 2) == M.MOE_ERR_ALIGNMENT
+    assert f(rows=0) == M.MOE_OK
+
+
+def _adamw(tensors=None, num=None, step=FAKE, lr=FAKE, gs=None, b1=0.9, b2=0.95, eps=1e-8,
+           wd=0.1, **kw):
+    if tensors is None:
+        a = dict(master=FAKE, grad=FAKE, m=FAKE, v=FAKE, param=None, m_scale=None, v_scale=None,
+                 numel=10, grad_fmt=0, state_fmt=0)
+        a.update(kw)
+        tensors = [a]
+    arr = (M._AdamWTensor * max(len(tensors), 1))(*[M._AdamWTensor(**t) for t in tensors])
+    return M.lib().moe_adamw(arr, len(tensors) if num is None else num, step, lr, gs, b1, b2,
+                             eps, wd, None)
+
+
+def test_adamw_rejects_bad_arguments():
+    nan, inf = float("nan"), float("inf")
+    assert _adamw(num=-1) == M.MOE_ERR_SHAPE
+    for bad in (dict(b1=1.0), dict(b1=-0.1), dict(b2=nan), dict(b2=1.0), dict(eps=-1e-8),
+                dict(eps=inf), dict(wd=nan), dict(wd=-1.0)):
+        assert _adamw(**bad) == M.MOE_ERR_SHAPE, bad
+    assert _adamw(step=None) == M.MOE_ERR_NULL
+    assert _adamw(lr=None) == M.MOE_ERR_NULL
+    assert _adamw(step=FAKE + 4) == M.MOE_ERR_ALIGNMENT
+    assert _adamw(numel=-1) == M.MOE_ERR_SHAPE
+    assert _adamw(numel=(1 << 40) + 1) == M.MOE_ERR_SHAPE
+    assert _adamw(grad_fmt=2) == M.MOE_ERR_UNSUPPORTED
+    assert _adamw(state_fmt=2) == M.MOE_ERR_UNSUPPORTED
+    for name in ("master", "grad", "m", "v"):
+        assert _adamw(**{name: None}) == M.MOE_ERR_NULL
+        assert _adamw(**{name: MIS}) == M.MOE_ERR_ALIGNMENT
+    assert _adamw(param=MIS) == M.MOE_ERR_ALIGNMENT
+    assert _adamw(state_fmt=1) == M.MOE_ERR_NULL                    # no scales
+    assert _adamw(state_fmt=1, m_scale=FAKE, v_scale=FAKE + 2) == M.MOE_ERR_ALIGNMENT
+    assert _adamw(numel=0, master=None) == M.MOE_OK                 # skipped
+    assert _adamw(tensors=[]) == M.MOE_OK
+    two = [dict(master=FAKE + o, grad=FAKE, m=FAKE, v=FAKE, numel=10, grad_fmt=0, state_fmt=0)
+           for o in (0, 32)]
+    assert _adamw(tensors=two) == M.MOE_ERR_UNSUPPORTED             # masters overlap
+
+
+def test_header_matches_the_struct():
+    assert ctypes.sizeof(M._AdamWTensor) == 72
+
+
+def test_wgrad_workspace_bad_input():
+    f = M.moe_grouped_wgrad_workspace_bytes
+    assert f(-1, 256, 256, 4) == 0
+    assert f(256, 100, 256, 4) == 0
+    assert f(256, 256, 256, 0) == 0
+
+
+def test_binding_refuses_what_the_library_cannot_see():
+    """The binding raises on shapes, types, strides and devices before any call."""
+    bf = torch.bfloat16
+    z = lambda *s, d=bf: torch.zeros(s, dtype=d)  # noqa: E731
+    psum, st = z(2, d=torch.int32), z(2, d=torch.int32)
+    with pytest.raises(ValueError, match="not on the current GPU"):
+        M.moe_grouped_dgrad_bf16(z(64, 128), z(2, 128, 64), psum, st, 32, z(64, 64))
+    with pytest.raises(ValueError, match="contiguous"):
+        M.moe_grouped_dgrad_bf16(z(128, 64).t(), z(2, 128, 64), psum, st, 32, z(64, 64))
+    with pytest.raises(ValueError, match="dw must be"):
+        # dy and x are on the CPU too, but shapes are looked at first
+        M._need("moe_grouped_wgrad_bf16", "dw", z(2, 128, 64, d=torch.float16),
+                (bf, torch.float32), (2, 128, 64))
+    with pytest.raises(ValueError, match="m must be"):
+        M._need("AdamWTensors", "m", z(5), torch.float32, (5,))

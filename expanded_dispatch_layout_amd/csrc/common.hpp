@@ -78,4 +78,19 @@ __device__ __forceinline__ uint32_t e8m0_round_up(float s) {
   return ex + (bump ? 1u : 0u);
 }
 
+// Compute units of the current device (256 if it cannot be asked).
+inline int device_cus() {
+  static int cus[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cus[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+        n <= 0)
+      n = 256;
+    cus[dev] = n;
+  }
+  return cus[dev];
+}
+
 }  // namespace moe

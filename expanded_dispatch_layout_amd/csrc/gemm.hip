@@ -67,7 +67,7 @@
 //    moe_runner/deep_gemm.py source, _run_masked_gemm; SGLang PR 37261, "Why
 //    decode stays on V1 low_latency"): expert e owns slab rows
 //    [e * max_m, e * max_m + masked_m[e]); only the item decode differs.
-#include "common.hpp"
+#include "lds_dma.hpp"
 
 namespace moe {
 namespace {
@@ -137,73 +137,6 @@ static_assert(kWaves == 2 * kLoadWaves && B_LOADS == 4 && A_LOADS == 8, "load sp
 __device__ __forceinline__ int swz_key(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 __device__ __forceinline__ int swz(int row, int chunk) {  // byte offset in a [rows][128] tile
   return row * 128 + ((chunk ^ swz_key(row)) << 4);
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return __builtin_amdgcn_readfirstlane(
-      (uint32_t)(size_t)(__attribute__((address_space(3))) const void*)p);
-}
-
-// LDS reads by 32-bit LDS address (keeps addresses in single registers and
-// lets constant parts fold into the instruction's offset field).
-template <typename T>
-__device__ __forceinline__ T lds_load(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(addr);
-}
-template <typename T>
-__device__ __forceinline__ void lds_store(uint32_t addr, T v) {
-  *reinterpret_cast<__attribute__((address_space(3))) T*>(addr) = v;
-}
-
-// Direct HBM -> LDS loads.  Issued from inline assembly so the compiler does
-// not treat them as LDS writes that every later LDS read must wait for: the
-// kernel orders them itself (vmcnt waits + s_barrier).  Address = 64-bit
-// scalar base + 32-bit per-lane offset; lane i's data lands at lds + i * size,
-// the LDS base taken from M0, which the asm names as an input operand so the
-// compiler itself writes it and knows it is in use.
-// A wave-uniform pointer, held in scalar registers (the loads' base operand).
-__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const uint8_t*)(((uint64_t)hi << 32) | lo);
-}
-
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  base = uniform_ptr(base);                   // wave-uniform by construction
-  lds = __builtin_amdgcn_readfirstlane(lds);  // M0: wave-uniform by construction
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  base = uniform_ptr(base);
-  lds = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
-// Keep the compiler's scheduler from moving instructions across this point
-// (bounds how far it hoists the next step's fragment reads, and with them
-// the registers they occupy).
-__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
-// All of this wave's LDS reads have returned.
-__device__ __forceinline__ void wait_lgkm0() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
-// Wait until at most a * NL of this wave's vector-memory operations are
-// outstanding, a in [0, MAXA] at run time (s_waitcnt takes an immediate: a
-// short compare chain picks it).
-template <int NL, int MAXA>
-__device__ __forceinline__ void wait_ahead(int a) {
-  if constexpr (MAXA <= 0) {
-    wait_vmcnt<0>();
-  } else {
-    if (a >= MAXA) wait_vmcnt<MAXA * NL>();
-    else wait_ahead<NL, MAXA - 1>(a);
-  }
 }
 
 // Activation ring geometry for na 8-row blocks per loading wave per stage
@@ -360,14 +293,6 @@ __device__ __forceinline__ v8i frag2(uint32_t base, int lo_off, int hi_off) {
   const u32x4 hi = lds_load<u32x4>(base + hi_off);
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2],
              (int)hi[3]};
-}
-
-// Two floats -> packed bf16 pair (low = x), round to nearest even: one
-// v_cvt_pk_bf16_f32 on gfx950.
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pk_bf16(float x, float y) {
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{x, y}, bf16x2_t));
 }
 
 __device__ __forceinline__ v4f mfma_plain(const v8i& a, const v8i& b) {
@@ -889,20 +814,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_kernel(
       barrier();  // every wave is done with its staging area before the next item's loads
     }
   }
-}
-
-int device_cus() {
-  static int cus[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cus[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-        n <= 0)
-      n = 256;
-    cus[dev] = n;
-  }
-  return cus[dev];
 }
 
 // One workgroup per CU (the kernel uses ~154 KB of LDS), a whole number per

@@ -7,7 +7,7 @@
 // 64 x 64 tiles through LDS, four waves of one 16-row band each,
 // v_mfma_f32_16x16x32_bf16.  An operand whose reduction axis is not the
 // contiguous one is transposed on its way into LDS.
-#include "common.hpp"
+#include "gemm_backward.hpp"
 
 namespace moe {
 namespace {
@@ -100,57 +100,6 @@ __global__ __launch_bounds__(kThreads) void dgrad_kernel(
     }
 }
 
-template <bool kF32>
-__global__ __launch_bounds__(kThreads) void wgrad_kernel(
-    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ x,
-    const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
-    int k, int E, int align, int accumulate, void* __restrict__ dw) {
-  __shared__ __attribute__((aligned(16))) uint16_t A[T][LD], B[T][LD];
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int64_t nrows = min((int64_t)status[0], capacity);
-  const int kt = k / T, e = blockIdx.y;
-  const int j0 = blockIdx.x / kt * T, t0 = blockIdx.x % kt * T;
-  int64_t st, en;
-  expert_rows(psum, nrows, align, e, st, en);
-  v4f acc[4] = {};
-  for (int64_t m = st; m < en; m += T) {
-    const int live = (int)min((int64_t)T, en - m);
-    load_tile<true>(dy + m * n + j0, n, live, T, A);
-    load_tile<true>(x + m * k + t0, k, live, T, B);
-    __syncthreads();
-    tile_mma(A, B, wid * 16, lane, acc);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t o = ((int64_t)e * n + j0 + wid * 16 + (lane >> 4) * 4 + q) * k + t0 + j * 16 +
-                        (lane & 15);
-      float v = acc[j][q];
-      if constexpr (kF32) {
-        float* d = (float*)dw + o;
-        *d = accumulate ? *d + v : v;
-      } else {
-        uint16_t* d = (uint16_t*)dw + o;
-        *d = f32_to_bf16_rne(accumulate ? bf16_to_f32(*d) + v : v);
-      }
-    }
-}
-
-constexpr int kMaxBlocks64 = 511;  // n / 64 and k / 64, as the forward GEMM's k
-
-moe_status check_sizes(int64_t capacity, int n, int k, int num_experts, int align) {
-  if (capacity < 0 || capacity > (1LL << 30) || n <= 0 || k <= 0 || n % 128 || k % 64 ||
-      num_experts < 1 || num_experts > MOE_MAX_EXPERTS)
-    return MOE_ERR_SHAPE;
-  if (align < MOE_MIN_ALIGN || align > MOE_MAX_ALIGN || (align & (align - 1)))
-    return MOE_ERR_UNSUPPORTED;
-  if (capacity % align != 0) return MOE_ERR_SHAPE;
-  if (n / 64 > kMaxBlocks64 || k / 64 > kMaxBlocks64) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -160,7 +109,7 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
                                              const int32_t* status, int64_t capacity, int n,
                                              int k, int num_experts, int align, void* dx,
                                              void* stream) {
-  const moe_status c = check_sizes(capacity, n, k, num_experts, align);
+  const moe_status c = check_backward_sizes(capacity, n, k, num_experts, align);
   if (c != MOE_OK) return c;
   if (!psum || !status || !w) return MOE_ERR_NULL;
   if (capacity > 0 && (!dy || !dx)) return MOE_ERR_NULL;
@@ -171,30 +120,5 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
   hipLaunchKernelGGL(dgrad_kernel, grid, dim3(kThreads), 0, reinterpret_cast<hipStream_t>(stream),
                      (const uint16_t*)dy, (const uint16_t*)w, psum, status, capacity, n, k,
                      num_experts, align, (uint16_t*)dx);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
-}
-
-extern "C" size_t moe_grouped_wgrad_workspace_bytes(int64_t capacity, int n, int k,
-                                                    int num_experts) {
-  return 0;
-}
-
-extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, const int32_t* psum,
-                                             const int32_t* status, int64_t capacity, int n,
-                                             int k, int num_experts, int align, moe_grad_fmt fmt,
-                                             int accumulate, void* dw, void* workspace,
-                                             size_t workspace_bytes, void* stream) {
-  const moe_status c = check_sizes(capacity, n, k, num_experts, align);
-  if (c != MOE_OK) return c;
-  if (fmt != MOE_GRAD_BF16 && fmt != MOE_GRAD_F32) return MOE_ERR_UNSUPPORTED;
-  if (!psum || !status || !dw) return MOE_ERR_NULL;
-  if (capacity > 0 && (!dy || !x)) return MOE_ERR_NULL;
-  if (((uintptr_t)dy % 16) || ((uintptr_t)x % 16) || ((uintptr_t)dw % 16))
-    return MOE_ERR_ALIGNMENT;
-  const dim3 grid((unsigned)(n / T * (k / T)), (unsigned)num_experts);
-  auto kern = fmt == MOE_GRAD_F32 ? wgrad_kernel<true> : wgrad_kernel<false>;
-  hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, reinterpret_cast<hipStream_t>(stream),
-                     (const uint16_t*)dy, (const uint16_t*)x, psum, status, capacity, n, k,
-                     num_experts, align, accumulate, dw);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

@@ -1,0 +1,22 @@
+// Argument checks that the grouped products' gradients share.
+#pragma once
+
+#include "common.hpp"
+
+namespace moe {
+
+constexpr int kMaxBlocks64 = 511;  // n / 64 and k / 64, as the forward GEMM's k
+
+inline moe_status check_backward_sizes(int64_t capacity, int n, int k, int num_experts,
+                                       int align) {
+  if (capacity < 0 || capacity > (1LL << 30) || n <= 0 || k <= 0 || n % 128 || k % 64 ||
+      num_experts < 1 || num_experts > MOE_MAX_EXPERTS)
+    return MOE_ERR_SHAPE;
+  if (align < MOE_MIN_ALIGN || align > MOE_MAX_ALIGN || (align & (align - 1)))
+    return MOE_ERR_UNSUPPORTED;
+  if (capacity % align != 0) return MOE_ERR_SHAPE;
+  if (n / 64 > kMaxBlocks64 || k / 64 > kMaxBlocks64) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace moe

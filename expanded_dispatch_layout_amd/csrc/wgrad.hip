@@ -1,0 +1,258 @@
+// moe_grouped_wgrad_bf16: weight gradient of the grouped bf16 GEMM,
+//   dw[e, j, t] = sum over the live rows m of expert e of dy[m, j] * x[m, t].
+#include "gemm_backward.hpp"
+#include "lds_dma.hpp"
+
+namespace moe {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kXcds = 8;
+constexpr int TN = 256, TK = 256;            // output tile: dy columns x x columns
+constexpr int kStep = 32;                    // rows per stage
+constexpr int kRowBytes = 512;               // 256 bf16
+constexpr int kOpBytes = kStep * kRowBytes;  // 16 KB: one operand of a stage
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kStages = 4;
+constexpr int kRing = kStages * kStageBytes;   // 128 KB
+constexpr int kStage2 = 8192;                  // epilogue staging per wave
+constexpr int kLds = kRing + kWaves * kStage2; // 160 KB
+constexpr int kLoads = 8;                      // DMA instructions per wave and stage
+constexpr int F = 8;                           // 16-wide tiles per wave and axis (128)
+
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// The reduction axis is the rows' one, so both operands' fragments are
+// columns of the staged tiles: ds_read_b64_tr_b16 gives lane l of a 16-lane
+// group column l of 4 rows x 16 columns.  The 32-byte pieces of a row are
+// XOR-swizzled by key(row), which differs over the 8 rows that half a wave
+// reads at once.
+__device__ __forceinline__ int key(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
+
+__device__ __forceinline__ bf16x8 frag_tr(uint32_t addr) {
+  typedef __attribute__((address_space(3))) s16x4* p_t;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p_t)(size_t)addr);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p_t)(size_t)(addr + 4 * kRowBytes));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+struct Tile {
+  int e, j0, t0;
+  int64_t st;  // first row
+  int live;    // rows
+};
+
+// Items of one expert: panels of 8 tiles along t, j-major inside a panel, so
+// that the 32 neighbouring items of an XCD's CUs are a 4 x 8 block and share
+// their operands in its L2.
+__device__ __forceinline__ Tile decode(int64_t item, int NJ, int NT, const int32_t* psum,
+                                       int64_t nrows, int align) {
+  Tile t;
+  const int per = NJ * NT;
+  t.e = (int)(item / per);
+  const int local = (int)(item % per);
+  const int panel = local / (8 * NJ);
+  const int rem = local - panel * 8 * NJ;
+  const int w = min(8, NT - panel * 8);
+  t.j0 = rem / w * TN;
+  t.t0 = (panel * 8 + rem % w) * TK;
+  t.st = t.e ? max(0, align_up_i(psum[t.e - 1], align)) : 0;
+  const int64_t en = min((int64_t)psum[t.e], nrows);
+  t.live = en > t.st ? (int)(en - t.st) : 0;
+  return t;
+}
+
+template <bool kF32>
+__global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
+    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
+    const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
+    int k, int E, int align, int accumulate, void* __restrict__ dw) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds0 = lds_addr(lds);
+  const int64_t nrows = min((int64_t)status[0], capacity);
+  const int NJ = (n + TN - 1) / TN, NT = (k + TK - 1) / TK;
+  const int64_t nitems = (int64_t)E * NJ * NT;
+  const int per_xcd = gridDim.x / kXcds;
+  const int64_t first = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+
+  // Fragment addresses within a stage.
+  const int wj = wid >> 1, wt = wid & 1;
+  uint32_t fa[F], fb[F];  // x, dy
+  {
+    const int g = lane >> 4, r = (lane & 15) >> 2, q = lane & 3;
+    const int ky = r | ((g & 1) << 2);
+    const uint32_t base = (uint32_t)((8 * g + r) * kRowBytes + (q >> 1) * 16 + (q & 1) * 8);
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      fa[i] = lds0 + kOpBytes + wt * 256 + base + (uint32_t)((i ^ ky) << 5);
+      fb[i] = lds0 + wj * 256 + base + (uint32_t)((i ^ ky) << 5);
+    }
+  }
+
+  // DMA side: the next stage to load.
+  int64_t d_item = first;
+  int d_left = 0;  // rows left of its tile
+  const uint8_t *d_dy = nullptr, *d_x = nullptr;
+  uint32_t d_offa[4], d_offb[4];  // x, dy: offsets of this lane's chunks
+  uint32_t d_slot = 0;            // LDS offset of the next slot
+  auto d_open = [&]() __attribute__((always_inline)) {  // next tile that has rows
+    while (d_item < nitems) {
+      const Tile t = decode(d_item, NJ, NT, psum, nrows, align);
+      if (t.live > 0) {
+        d_left = t.live;
+        d_dy = dy + (t.st * n + t.j0) * 2;
+        d_x = x + (t.st * k + t.t0) * 2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = (wid * 4 + j) * 2 + (lane >> 5);
+          const int col = ((lane & 31) ^ (key(row) << 1)) * 8;
+          d_offb[j] = (uint32_t)(row * n + min(col, n - 8 - t.j0)) * 2u;
+          d_offa[j] = (uint32_t)(row * k + min(col, k - 8 - t.t0)) * 2u;
+        }
+        return;
+      }
+      d_item += gridDim.x;
+    }
+  };
+  auto d_issue = [&]() __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + d_slot + wid * 4096;
+    if (d_left >= kStep) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dma16(d_dy, d_offb[j], dst + j * 1024);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dma16(d_x, d_offa[j], dst + kOpBytes + j * 1024);
+    } else {  // rows past the last live one read zeros
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool ok = (wid * 4 + j) * 2 + (lane >> 5) < d_left;
+        dma16_ptr(ok ? d_dy + d_offb[j] : (const uint8_t*)kZeros, dst + j * 1024);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool ok = (wid * 4 + j) * 2 + (lane >> 5) < d_left;
+        dma16_ptr(ok ? d_x + d_offa[j] : (const uint8_t*)kZeros, dst + kOpBytes + j * 1024);
+      }
+    }
+    d_slot = d_slot + kStageBytes == kRing ? 0 : d_slot + kStageBytes;
+    d_left -= kStep;
+    d_dy += (int64_t)kStep * n * 2;
+    d_x += (int64_t)kStep * k * 2;
+    if (d_left <= 0) {
+      d_item += gridDim.x;
+      d_open();
+    }
+  };
+
+  int ahead = 0;  // stages issued and not yet computed
+  d_open();
+  while (ahead < kStages && d_item < nitems) d_issue(), ++ahead;
+
+  uint32_t c_slot = 0;  // slot of the stage to compute
+  v4f acc[F][F];
+  bf16x8 a[F], b[F];
+
+  for (int64_t item = first; item < nitems; item += gridDim.x) {
+    const Tile t = decode(item, NJ, NT, psum, nrows, align);
+    const int steps = (t.live + kStep - 1) / kStep;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (steps > 0) {
+      wait_vmcnt<0>();
+      barrier();
+#pragma unroll
+      for (int j = 0; j < F; ++j) b[j] = frag_tr(fb[j] + c_slot);
+#pragma unroll
+      for (int i = 0; i < F; ++i) a[i] = frag_tr(fa[i] + c_slot);
+      for (int s = 0; s < steps; ++s) {
+        wait_ahead<kLoads, kStages - 2>(ahead - 2);
+        wait_lgkm0();
+        barrier();
+        const uint32_t nslot = c_slot + kStageBytes == kRing ? 0 : c_slot + kStageBytes;
+        --ahead;
+        if (d_item < nitems) d_issue(), ++ahead;
+        c_slot = nslot;
+#pragma unroll
+        for (int u = 0; u < F * F; ++u) {
+          const int p = u / (2 * F), i = 2 * p + (u & 1), j = (u % (2 * F)) / 2;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+          sched_fence();
+          if (j == F - 1) a[i] = frag_tr(fa[i] + nslot);
+          if (i == F - 1) b[j] = frag_tr(fb[j] + nslot);
+          sched_fence();
+        }
+      }
+    } else if (accumulate) {
+      continue;
+    }
+    // Epilogue: lane holds t = 4 (lane / 16) + 0..3 of tile i, j = lane % 16 of
+    // tile j.
+    const int jc = t.j0 + wj * 128, tc = t.t0 + wt * 128 + (lane >> 4) * 4;
+    if (jc < n) {
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        const int64_t row = ((int64_t)t.e * n + jc + j * 16 + (lane & 15)) * k + tc;
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          if (t.t0 + wt * 128 + i * 16 < k) {
+            v4f v = acc[i][j];
+            if constexpr (kF32) {
+              v4f* o = reinterpret_cast<v4f*>((float*)dw + row + i * 16);
+              if (accumulate) v += *o;
+              *o = v;
+            } else {
+              uint2* o = reinterpret_cast<uint2*>((uint16_t*)dw + row + i * 16);
+              if (accumulate) {
+                const uint2 q = *o;
+                v += v4f{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
+                         __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)};
+              }
+              *o = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_grouped_wgrad_workspace_bytes(int64_t capacity, int n, int k,
+                                                    int num_experts) {
+  return 0;
+}
+
+extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, const int32_t* psum,
+                                             const int32_t* status, int64_t capacity, int n,
+                                             int k, int num_experts, int align, moe_grad_fmt fmt,
+                                             int accumulate, void* dw, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  const moe_status c = check_backward_sizes(capacity, n, k, num_experts, align);
+  if (c != MOE_OK) return c;
+  if (fmt != MOE_GRAD_BF16 && fmt != MOE_GRAD_F32) return MOE_ERR_UNSUPPORTED;
+  if (!psum || !status || !dw) return MOE_ERR_NULL;
+  if (capacity > 0 && (!dy || !x)) return MOE_ERR_NULL;
+  if (((uintptr_t)dy % 16) || ((uintptr_t)x % 16) || ((uintptr_t)dw % 16))
+    return MOE_ERR_ALIGNMENT;
+  const int64_t items = (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
+  int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
+  if (grid > items) grid = items;
+  grid = (grid + kXcds - 1) / kXcds * kXcds;
+  auto kern = fmt == MOE_GRAD_F32 ? wgrad_kernel<true> : wgrad_kernel<false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0,
+                     reinterpret_cast<hipStream_t>(stream), (const uint8_t*)dy, (const uint8_t*)x,
+                     psum, status, capacity, n, k, num_experts, align, accumulate, dw);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}

@@ -10,8 +10,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
+constexpr int kThreads = 512;
+constexpr int kWaves = 8;
 constexpr int kXcds = 8;
 constexpr int TN = 256, TK = 256;            // output tile: dy columns x x columns
 constexpr int kStep = 32;                    // rows per stage
@@ -20,10 +20,10 @@ constexpr int kOpBytes = kStep * kRowBytes;  // 16 KB: one operand of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr int kStages = 4;
 constexpr int kRing = kStages * kStageBytes;   // 128 KB
-constexpr int kStage2 = 8192;                  // epilogue staging per wave
+constexpr int kStage2 = 4096;                  // epilogue staging per wave
 constexpr int kLds = kRing + kWaves * kStage2; // 160 KB
-constexpr int kLoads = 8;                      // DMA instructions per wave and stage
-constexpr int F = 8;                           // 16-wide tiles per wave and axis (128)
+constexpr int kLoads = 4;                      // DMA instructions per wave and stage
+constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
 
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
@@ -84,23 +84,24 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
 
   // Fragment addresses within a stage.
   const int wj = wid >> 1, wt = wid & 1;
-  uint32_t fa[F], fb[F];  // x, dy
+  uint32_t fa[FI], fb[FJ];  // x, dy
   {
     const int g = lane >> 4, r = (lane & 15) >> 2, q = lane & 3;
     const int ky = r | ((g & 1) << 2);
     const uint32_t base = (uint32_t)((8 * g + r) * kRowBytes + (q >> 1) * 16 + (q & 1) * 8);
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
+    for (int i = 0; i < FI; ++i)
       fa[i] = lds0 + kOpBytes + wt * 256 + base + (uint32_t)((i ^ ky) << 5);
-      fb[i] = lds0 + wj * 256 + base + (uint32_t)((i ^ ky) << 5);
-    }
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+      fb[j] = lds0 + (wj >> 1) * 256 + base + (uint32_t)((((wj & 1) * FJ + j) ^ ky) << 5);
   }
 
   // DMA side: the next stage to load.
   int64_t d_item = first;
   int d_left = 0;  // rows left of its tile
   const uint8_t *d_dy = nullptr, *d_x = nullptr;
-  uint32_t d_offa[4], d_offb[4];  // x, dy: offsets of this lane's chunks
+  uint32_t d_offa[2], d_offb[2];  // x, dy: offsets of this lane's chunks
   uint32_t d_slot = 0;            // LDS offset of the next slot
   auto d_open = [&]() __attribute__((always_inline)) {  // next tile that has rows
     while (d_item < nitems) {
@@ -110,8 +111,8 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
         d_dy = dy + (t.st * n + t.j0) * 2;
         d_x = x + (t.st * k + t.t0) * 2;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = (wid * 4 + j) * 2 + (lane >> 5);
+        for (int j = 0; j < 2; ++j) {
+          const int row = (wid * 2 + j) * 2 + (lane >> 5);
           const int col = ((lane & 31) ^ (key(row) << 1)) * 8;
           d_offb[j] = (uint32_t)(row * n + min(col, n - 8 - t.j0)) * 2u;
           d_offa[j] = (uint32_t)(row * k + min(col, k - 8 - t.t0)) * 2u;
@@ -121,87 +122,83 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       d_item += gridDim.x;
     }
   };
-  auto d_issue = [&]() __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + d_slot + wid * 4096;
-    if (d_left >= kStep) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dma16(d_dy, d_offb[j], dst + j * 1024);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dma16(d_x, d_offa[j], dst + kOpBytes + j * 1024);
-    } else {  // rows past the last live one read zeros
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool ok = (wid * 4 + j) * 2 + (lane >> 5) < d_left;
-        dma16_ptr(ok ? d_dy + d_offb[j] : (const uint8_t*)kZeros, dst + j * 1024);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool ok = (wid * 4 + j) * 2 + (lane >> 5) < d_left;
-        dma16_ptr(ok ? d_x + d_offa[j] : (const uint8_t*)kZeros, dst + kOpBytes + j * 1024);
-      }
-    }
+  // Load q (0..3) of the next stage: dy rows first, then x.  Rows past the
+  // tile's last live one, and every row once there is no tile left, read
+  // zeros, so that each step issues the same loads without a branch.
+  const int d_row = wid * 4 + (lane >> 5);  // this lane's row in load 0; 2 more per load
+  auto d_load = [&](int q) __attribute__((always_inline)) {
+    const int j = q & 1;
+    const uint8_t* p = q < 2 ? d_dy + d_offb[j] : d_x + d_offa[j];
+    p = d_row + 2 * j < d_left ? p : (const uint8_t*)kZeros;
+    dma16_ptr(p, lds0 + d_slot + wid * 2048 + (q < 2 ? 0 : kOpBytes) + j * 1024);
+  };
+  auto d_advance = [&]() __attribute__((always_inline)) {
     d_slot = d_slot + kStageBytes == kRing ? 0 : d_slot + kStageBytes;
     d_left -= kStep;
     d_dy += (int64_t)kStep * n * 2;
     d_x += (int64_t)kStep * k * 2;
-    if (d_left <= 0) {
+    if (d_left <= 0 && d_item < nitems) {
       d_item += gridDim.x;
       d_open();
     }
   };
 
-  int ahead = 0;  // stages issued and not yet computed
   d_open();
-  while (ahead < kStages && d_item < nitems) d_issue(), ++ahead;
+  for (int g = 0; g < kStages; ++g) {
+    for (int q = 0; q < kLoads; ++q) d_load(q);
+    d_advance();
+  }
 
   uint32_t c_slot = 0;  // slot of the stage to compute
-  v4f acc[F][F];
-  bf16x8 a[F], b[F];
+  v4f acc[FI][FJ];
+  bf16x8 a[FI], b[FJ];
 
   for (int64_t item = first; item < nitems; item += gridDim.x) {
     const Tile t = decode(item, NJ, NT, psum, nrows, align);
     const int steps = (t.live + kStep - 1) / kStep;
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < FJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     if (steps > 0) {
       wait_vmcnt<0>();
       barrier();
 #pragma unroll
-      for (int j = 0; j < F; ++j) b[j] = frag_tr(fb[j] + c_slot);
+      for (int j = 0; j < FJ; ++j) b[j] = frag_tr(fb[j] + c_slot);
 #pragma unroll
-      for (int i = 0; i < F; ++i) a[i] = frag_tr(fa[i] + c_slot);
+      for (int i = 0; i < FI; ++i) a[i] = frag_tr(fa[i] + c_slot);
       for (int s = 0; s < steps; ++s) {
-        wait_ahead<kLoads, kStages - 2>(ahead - 2);
-        wait_lgkm0();
-        barrier();
         const uint32_t nslot = c_slot + kStageBytes == kRing ? 0 : c_slot + kStageBytes;
-        --ahead;
-        if (d_item < nitems) d_issue(), ++ahead;
-        c_slot = nslot;
 #pragma unroll
-        for (int u = 0; u < F * F; ++u) {
-          const int p = u / (2 * F), i = 2 * p + (u & 1), j = (u % (2 * F)) / 2;
+        for (int u = 0; u < FI * FJ; ++u) {
+          const int p = u / (2 * FJ), i = 2 * p + (u & 1), j = (u % (2 * FJ)) / 2;
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
           sched_fence();
-          if (j == F - 1) a[i] = frag_tr(fa[i] + nslot);
-          if (i == F - 1) b[j] = frag_tr(fb[j] + nslot);
+          if (u == 2 * FJ - 3) {
+            wait_vmcnt<(kStages - 2) * kLoads>();
+            wait_lgkm0();
+            barrier();
+          }
+          if (j == FJ - 1) a[i] = frag_tr(fa[i] + nslot);
+          if (i == FI - 1) b[j] = frag_tr(fb[j] + nslot);
+          if (u >= 2 * FJ && u % 4 == 1 && (u - 2 * FJ) / 4 < kLoads) d_load((u - 2 * FJ) / 4);
           sched_fence();
         }
+        c_slot = nslot;
+        d_advance();
       }
     } else if (accumulate) {
       continue;
     }
     // Epilogue: lane holds t = 4 (lane / 16) + 0..3 of tile i, j = lane % 16 of
     // tile j.
-    const int jc = t.j0 + wj * 128, tc = t.t0 + wt * 128 + (lane >> 4) * 4;
+    const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128 + (lane >> 4) * 4;
     if (jc < n) {
 #pragma unroll
-      for (int j = 0; j < F; ++j) {
+      for (int j = 0; j < FJ; ++j) {
         const int64_t row = ((int64_t)t.e * n + jc + j * 16 + (lane & 15)) * k + tc;
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
+        for (int i = 0; i < FI; ++i) {
           if (t.t0 + wt * 128 + i * 16 < k) {
             v4f v = acc[i][j];
             if constexpr (kF32) {
@@ -222,6 +219,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       }
     }
   }
+  wait_vmcnt<0>();  // no load may land after the workgroup's LDS has been given away
 }
 
 }  // namespace

@@ -11,17 +11,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
-constexpr int kWaves = 8;
 constexpr int kXcds = 8;
 constexpr int TN = 256, TK = 256;            // output tile: dy columns x x columns
 constexpr int kStep = 32;                    // rows per stage
 constexpr int kRowBytes = 512;               // 256 bf16
 constexpr int kOpBytes = kStep * kRowBytes;  // 16 KB: one operand of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kRing = kStages * kStageBytes;   // 128 KB
-constexpr int kStage2 = 4096;                  // epilogue staging per wave
-constexpr int kLds = kRing + kWaves * kStage2; // 160 KB
+constexpr int kLds = kRing; // 160 KB
 constexpr int kLoads = 4;                      // DMA instructions per wave and stage
 constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
 
@@ -67,6 +65,11 @@ __device__ __forceinline__ Tile decode(int64_t item, int NJ, int NT, const int32
   return t;
 }
 
+// Stages of a tile: computed in pairs, so an odd count gets one of zeros.
+__device__ __forceinline__ int stages_of(int live) {
+  return 2 * ((live + 2 * kStep - 1) / (2 * kStep));
+}
+
 template <bool kF32>
 __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
@@ -82,24 +85,22 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   const int per_xcd = gridDim.x / kXcds;
   const int64_t first = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
 
-  // Fragment addresses within a stage.
+  // Fragment addresses within a stage: tile i of a wave is its 32-byte piece
+  // i ^ key of a row, so one lane base serves all of them through an XOR.
   const int wj = wid >> 1, wt = wid & 1;
-  uint32_t fa[FI], fb[FJ];  // x, dy
+  uint32_t fx, fy;  // x, dy
   {
     const int g = lane >> 4, r = (lane & 15) >> 2, q = lane & 3;
-    const int ky = r | ((g & 1) << 2);
-    const uint32_t base = (uint32_t)((8 * g + r) * kRowBytes + (q >> 1) * 16 + (q & 1) * 8);
-#pragma unroll
-    for (int i = 0; i < FI; ++i)
-      fa[i] = lds0 + kOpBytes + wt * 256 + base + (uint32_t)((i ^ ky) << 5);
-#pragma unroll
-    for (int j = 0; j < FJ; ++j)
-      fb[j] = lds0 + (wj >> 1) * 256 + base + (uint32_t)((((wj & 1) * FJ + j) ^ ky) << 5);
+    const uint32_t base = lds0 + (uint32_t)((8 * g + r) * kRowBytes + key(8 * g + r) * 32 +
+                                            (q >> 1) * 16 + (q & 1) * 8);
+    fx = base + kOpBytes + wt * 256;
+    fy = (base + (wj >> 1) * 256) ^ (uint32_t)((wj & 1) * FJ * 32);
   }
 
   // DMA side: the next stage to load.
   int64_t d_item = first;
-  int d_left = 0;  // rows left of its tile
+  int d_left = 0;    // rows left of its tile (<= 0: a stage of zeros)
+  int d_stages = 0;  // stages left of its tile
   const uint8_t *d_dy = nullptr, *d_x = nullptr;
   uint32_t d_offa[2], d_offb[2];  // x, dy: offsets of this lane's chunks
   uint32_t d_slot = 0;            // LDS offset of the next slot
@@ -108,6 +109,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       const Tile t = decode(d_item, NJ, NT, psum, nrows, align);
       if (t.live > 0) {
         d_left = t.live;
+        d_stages = stages_of(t.live);
         d_dy = dy + (t.st * n + t.j0) * 2;
         d_x = x + (t.st * k + t.t0) * 2;
 #pragma unroll
@@ -137,25 +139,25 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     d_left -= kStep;
     d_dy += (int64_t)kStep * n * 2;
     d_x += (int64_t)kStep * k * 2;
-    if (d_left <= 0 && d_item < nitems) {
+    if (--d_stages <= 0 && d_item < nitems) {
       d_item += gridDim.x;
       d_open();
     }
   };
 
   d_open();
-  for (int g = 0; g < kStages; ++g) {
+  for (int g = 0; g < kStages - 1; ++g) {
     for (int q = 0; q < kLoads; ++q) d_load(q);
     d_advance();
   }
 
   uint32_t c_slot = 0;  // slot of the stage to compute
   v4f acc[FI][FJ];
-  bf16x8 a[FI], b[FJ];
+  bf16x8 a[2][FI], b[2][FJ];
 
   for (int64_t item = first; item < nitems; item += gridDim.x) {
     const Tile t = decode(item, NJ, NT, psum, nrows, align);
-    const int steps = (t.live + kStep - 1) / kStep;
+    const int steps = stages_of(t.live);
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -164,28 +166,32 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       wait_vmcnt<0>();
       barrier();
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) b[j] = frag_tr(fb[j] + c_slot);
+      for (int j = 0; j < FJ; ++j) b[0][j] = frag_tr((fy + c_slot) ^ (j << 5));
 #pragma unroll
-      for (int i = 0; i < FI; ++i) a[i] = frag_tr(fa[i] + c_slot);
-      for (int s = 0; s < steps; ++s) {
-        const uint32_t nslot = c_slot + kStageBytes == kRing ? 0 : c_slot + kStageBytes;
+      for (int i = 0; i < FI; ++i) a[0][i] = frag_tr((fx + c_slot) ^ (i << 5));
+      for (int s = 0; s < steps; s += 2) {
 #pragma unroll
-        for (int u = 0; u < FI * FJ; ++u) {
-          const int p = u / (2 * FJ), i = 2 * p + (u & 1), j = (u % (2 * FJ)) / 2;
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t nslot = c_slot + kStageBytes == kRing ? 0 : c_slot + kStageBytes;
+          const uint32_t nx = fx + nslot, ny = fy + nslot;
+          wait_vmcnt<(kStages - 3) * kLoads>();
+          barrier();
           sched_fence();
-          if (u == 2 * FJ - 3) {
-            wait_vmcnt<(kStages - 2) * kLoads>();
-            wait_lgkm0();
-            barrier();
+#pragma unroll
+          for (int u = 0; u < FI * FJ; ++u) {
+            const int i = u / FJ, j = u % FJ;
+            acc[i][j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
+            sched_fence();
+            if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr(ny ^ ((u / 2) << 5));
+            else if (u % 2 == 0 && u / 2 < FJ + FI)
+              a[h ^ 1][u / 2 - FJ] = frag_tr(nx ^ ((u / 2 - FJ) << 5));
+            else if (u % 4 == 1 && u / 4 < kLoads) d_load(u / 4);
+            sched_fence();
           }
-          if (j == FJ - 1) a[i] = frag_tr(fa[i] + nslot);
-          if (i == FI - 1) b[j] = frag_tr(fb[j] + nslot);
-          if (u >= 2 * FJ && u % 4 == 1 && (u - 2 * FJ) / 4 < kLoads) d_load((u - 2 * FJ) / 4);
-          sched_fence();
+          c_slot = nslot;
+          d_advance();
         }
-        c_slot = nslot;
-        d_advance();
       }
     } else if (accumulate) {
       continue;

@@ -237,6 +237,7 @@ struct WaveLoads {
   }
   // Weights of one stage from src (row 0 at K block q) into the slot at lds.
   __device__ __forceinline__ void weights(const uint8_t* src, uint32_t lds) const {
+    src = settled(src);
 #pragma unroll
     for (int j = 0; j < B_LOADS; ++j) dma16(src, off[j], lds + lds_off[j]);
   }
@@ -244,6 +245,7 @@ struct WaveLoads {
   template <int NA, bool kScales>
   __device__ __forceinline__ void acts(const uint8_t* src, uint32_t lds, const uint8_t* ssrc,
                                        uint32_t slds) const {
+    src = settled(src);
 #pragma unroll
     for (int j = 0; j < NA; ++j) dma16(src, off[j], lds + lds_off[j]);
     if constexpr (kScales) dma4(ssrc, scale_off, dummy ? dummy : slds + scale_rel);

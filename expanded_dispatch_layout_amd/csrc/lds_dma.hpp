@@ -28,6 +28,12 @@ __device__ __forceinline__ void lds_store(uint32_t addr, T v) {
 // scalar base + 32-bit per-lane offset; lane i's data lands at lds + i * size,
 // the LDS base taken from M0, which the asm names as an input operand so the
 // compiler itself writes it and knows it is in use.
+// The compiler's hazard pass does not look inside inline assembly, so the asm
+// brings the wait states itself: one between a scalar write of M0 and the
+// load, five between a vector instruction that writes a scalar register
+// (v_readfirstlane) and a load that takes its address from it.  The bases of
+// a stage's dma16 loads are held in scalar registers by settled(), which waits
+// once for all of them.
 // A wave-uniform pointer, held in scalar registers (the loads' base operand).
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   const uint64_t v = (uint64_t)p;
@@ -36,21 +42,27 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return (const uint8_t*)(((uint64_t)hi << 32) | lo);
 }
 
+// A base for dma16 (wave-uniform by construction).
+__device__ __forceinline__ const uint8_t* settled(const uint8_t* p) {
+  p = uniform_ptr(p);
+  asm volatile("s_nop 4" : "+s"(p));
+  return p;
+}
+
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  base = uniform_ptr(base);                   // wave-uniform by construction
   lds = __builtin_amdgcn_readfirstlane(lds);  // M0: wave-uniform by construction
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
   base = uniform_ptr(base);
   lds = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 
 // The same from a 64-bit address per lane.
 __device__ __forceinline__ void dma16_ptr(const uint8_t* p, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 
 template <int N>

@@ -85,7 +85,6 @@ constexpr int WSC_SLOT = 1024;      // the weight-scale ring (4 waves x 256 B pe
 
 constexpr int kThreads = 512;  // 8 waves: 2 per SIMD
 constexpr int kWaves = kThreads / 64;
-constexpr int kXcds = 8;       // MI355X: 8 XCDs, workgroups dispatched round-robin
 constexpr int GM = 256;        // rows per work item
 constexpr int BN = 128;
 constexpr int BK = 128;

@@ -2,9 +2,13 @@
 // order those loads themselves.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
+
+constexpr int kXcds = 8;       // MI355X: 8 XCDs, workgroups dispatched round-robin
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return __builtin_amdgcn_readfirstlane(
@@ -97,6 +101,54 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pk_bf16(float x, float y) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{x, y}, bf16x2_t));
+}
+
+// 16 bytes of zeros, as a source of dma16_ptr.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+__device__ __forceinline__ const uint8_t* zero_chunk() { return (const uint8_t*)kZeros; }
+
+// Fragments of an operand that is staged with its reduction axis along the
+// rows: a stage is 32 rows of 512 bytes (256 bf16 columns), and a fragment
+// (16 columns x 32 rows) is read through ds_read_b64_tr_b16, which gives lane
+// l of a 16-lane group column l of 4 rows x 16 columns.  Group g = lane / 16
+// reads rows 8 g + 0..3 and then 8 g + 4..7, so that each lane holds 8
+// consecutive rows of its column, the order in which the MFMA takes them.
+// The 32-byte pieces of a row (16 columns each) are XOR-swizzled within 256
+// bytes by tr_key(row), which differs over the 8 rows that half a wave reads
+// at once: no bank conflicts (counted: none).
+__device__ __forceinline__ int tr_key(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
+// This lane's address of piece 0; piece p of the same 256 bytes is at ^ (p << 5).
+__device__ __forceinline__ uint32_t tr_lane_offset(int lane) {
+  const int row = 8 * (lane >> 4) + ((lane & 15) >> 2), q = lane & 3;
+  return (uint32_t)(row * 512 + tr_key(row) * 32 + (q >> 1) * 16 + (q & 1) * 8);
+}
+template <int kRowBytes>
+__device__ __forceinline__ auto frag_tr(uint32_t addr) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  typedef __attribute__((address_space(3))) s16x4* lds_p;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(size_t)addr);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(size_t)(addr + 4 * kRowBytes));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Two 16x16 MFMA results that are neighbours along their rows (lane l holds
+// rows 4 (l / 16) + 0..3 of column l % 16 of each) as bf16: afterwards lane l
+// holds rows 8 ((l / 16) % 2) + 0..7 of tile l / 32, 16 consecutive bytes.
+__device__ __forceinline__ u32x4 pack_tiles(const float __attribute__((ext_vector_type(4))) x,
+                                            const float __attribute__((ext_vector_type(4))) y) {
+  uint32_t a[2] = {pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+  uint32_t b[2] = {pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // a's upper half against b's lower half, then a's odd 16-lane rows
+    // against b's even ones.
+    const auto h = __builtin_amdgcn_permlane32_swap(a[i], b[i], false, false);
+    const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    a[i] = r[0];
+    b[i] = r[1];
+  }
+  return u32x4{a[0], a[1], b[0], b[1]};
 }
 
 }  // namespace moe

@@ -7,11 +7,9 @@ namespace moe {
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
-constexpr int kXcds = 8;
 constexpr int TN = 256, TK = 256;            // output tile: dy columns x x columns
 constexpr int kStep = 32;                    // rows per stage
 constexpr int kRowBytes = 512;               // 256 bf16
@@ -22,22 +20,6 @@ constexpr int kRing = kStages * kStageBytes;   // 128 KB
 constexpr int kLds = kRing; // 160 KB
 constexpr int kLoads = 4;                      // DMA instructions per wave and stage
 constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
-
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
-
-// The reduction axis is the rows' one, so both operands' fragments are
-// columns of the staged tiles: ds_read_b64_tr_b16 gives lane l of a 16-lane
-// group column l of 4 rows x 16 columns.  The 32-byte pieces of a row are
-// XOR-swizzled by key(row), which differs over the 8 rows that half a wave
-// reads at once.
-__device__ __forceinline__ int key(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
-
-__device__ __forceinline__ bf16x8 frag_tr(uint32_t addr) {
-  typedef __attribute__((address_space(3))) s16x4* p_t;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p_t)(size_t)addr);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p_t)(size_t)(addr + 4 * kRowBytes));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
 
 struct Tile {
   int e, j0, t0;
@@ -75,7 +57,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
     int k, int E, int align, int accumulate, void* __restrict__ dw) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_addr(lds);
@@ -90,9 +72,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   const int wj = wid >> 1, wt = wid & 1;
   uint32_t fx, fy;  // x, dy
   {
-    const int g = lane >> 4, r = (lane & 15) >> 2, q = lane & 3;
-    const uint32_t base = lds0 + (uint32_t)((8 * g + r) * kRowBytes + key(8 * g + r) * 32 +
-                                            (q >> 1) * 16 + (q & 1) * 8);
+    const uint32_t base = lds0 + tr_lane_offset(lane);
     fx = base + kOpBytes + wt * 256;
     fy = (base + (wj >> 1) * 256) ^ (uint32_t)((wj & 1) * FJ * 32);
   }
@@ -115,7 +95,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int row = (wid * 2 + j) * 2 + (lane >> 5);
-          const int col = ((lane & 31) ^ (key(row) << 1)) * 8;
+          const int col = ((lane & 31) ^ (tr_key(row) << 1)) * 8;
           d_offb[j] = (uint32_t)(row * n + min(col, n - 8 - t.j0)) * 2u;
           d_offa[j] = (uint32_t)(row * k + min(col, k - 8 - t.t0)) * 2u;
         }
@@ -131,7 +111,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   auto d_load = [&](int q) __attribute__((always_inline)) {
     const int j = q & 1;
     const uint8_t* p = q < 2 ? d_dy + d_offb[j] : d_x + d_offa[j];
-    p = d_row + 2 * j < d_left ? p : (const uint8_t*)kZeros;
+    p = d_row + 2 * j < d_left ? p : zero_chunk();
     dma16_ptr(p, lds0 + d_slot + wid * 2048 + (q < 2 ? 0 : kOpBytes) + j * 1024);
   };
   auto d_advance = [&]() __attribute__((always_inline)) {
@@ -166,9 +146,9 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       wait_vmcnt<0>();
       barrier();
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) b[0][j] = frag_tr((fy + c_slot) ^ (j << 5));
+      for (int j = 0; j < FJ; ++j) b[0][j] = frag_tr<kRowBytes>((fy + c_slot) ^ (j << 5));
 #pragma unroll
-      for (int i = 0; i < FI; ++i) a[0][i] = frag_tr((fx + c_slot) ^ (i << 5));
+      for (int i = 0; i < FI; ++i) a[0][i] = frag_tr<kRowBytes>((fx + c_slot) ^ (i << 5));
       for (int s = 0; s < steps; s += 2) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -183,9 +163,9 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
             acc[i][j] =
                 __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
             sched_fence();
-            if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr(ny ^ ((u / 2) << 5));
+            if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr<kRowBytes>(ny ^ ((u / 2) << 5));
             else if (u % 2 == 0 && u / 2 < FJ + FI)
-              a[h ^ 1][u / 2 - FJ] = frag_tr(nx ^ ((u / 2 - FJ) << 5));
+              a[h ^ 1][u / 2 - FJ] = frag_tr<kRowBytes>(nx ^ ((u / 2 - FJ) << 5));
             else if (u % 4 == 1 && u / 4 < kLoads) d_load(u / 4);
             sched_fence();
           }

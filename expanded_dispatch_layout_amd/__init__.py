@@ -130,14 +130,18 @@ def moe_expand_workspace_bytes(rows, topk, num_experts) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is not None:
-        return ctypes.c_void_p(int(stream))
+        return int(stream)
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    # The handle of torch.cuda.current_stream(), without making a Stream
+    # object of it (3 us of a call's 10).
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(fn, code):
@@ -295,26 +299,24 @@ def moe_silu_mul_bf16(gate_up, m_indices, psum, status, num_experts, align, out,
     _check("moe_silu_mul_bf16", code)
 
 
-def _need(fn, name, t, dtype, shape):
-    """t is a contiguous GPU tensor of the current device, of this dtype and
-    shape (the library sees plain pointers and cannot tell)."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in (dtype if isinstance(dtype, tuple)
-                                                         else (dtype,)):
-        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)}, "
-                         f"got {t.dtype} of shape {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
+def _need(fn, *specs):
+    """Each (name, tensor, dtype, shape) is a contiguous tensor of that type and
+    shape on the current GPU (the library sees plain pointers and cannot
+    tell).  Tensors that are None are passed over."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
-
-
-def _need_layout(fn, psum, status, num_experts, m_indices=None, capacity=0):
-    import torch
-    _need(fn, "psum", psum, torch.int32, (num_experts,))
-    _need(fn, "status", status, torch.int32, (2,))
-    if m_indices is not None:
-        _need(fn, "m_indices", m_indices, torch.int32, (capacity,))
+    device = None
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)}, "
+                             f"got {t.dtype} of shape {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        if device is None:
+            device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+        if t.get_device() != device:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
 
 
 def moe_grouped_dgrad_bf16(dy, w, psum, status, align, dx, stream=None):
@@ -322,10 +324,9 @@ def moe_grouped_dgrad_bf16(dy, w, psum, status, align, dx, stream=None):
     import torch
     fn, bf = "moe_grouped_dgrad_bf16", torch.bfloat16
     (capacity, n), (E, _, k) = dy.shape, w.shape
-    _need(fn, "dy", dy, bf, (capacity, n))
-    _need(fn, "w", w, bf, (E, n, k))
-    _need(fn, "dx", dx, bf, (capacity, k))
-    _need_layout(fn, psum, status, E)
+    _need(fn, ("dy", dy, bf, (capacity, n)), ("w", w, bf, (E, n, k)),
+          ("dx", dx, bf, (capacity, k)), ("psum", psum, torch.int32, (E,)),
+          ("status", status, torch.int32, (2,)))
     code = lib().moe_grouped_dgrad_bf16(_ptr(dy), _ptr(w), _ptr(psum), _ptr(status), capacity,
                                         n, k, E, align, _ptr(dx), _stream(stream))
     _check(fn, code)
@@ -343,14 +344,11 @@ def moe_grouped_wgrad_bf16(dy, x, psum, status, align, dw, workspace=None, accum
     import torch
     fn, bf = "moe_grouped_wgrad_bf16", torch.bfloat16
     (capacity, n), k, E = dy.shape, x.shape[1], dw.shape[0]
-    _need(fn, "dy", dy, bf, (capacity, n))
-    _need(fn, "x", x, bf, (capacity, k))
-    _need(fn, "dw", dw, (bf, torch.float32), (E, n, k))
-    _need_layout(fn, psum, status, E)
-    size = 0
-    if workspace is not None:
-        _need(fn, "workspace", workspace, torch.uint8, (workspace.numel(),))
-        size = workspace.numel()
+    size = 0 if workspace is None else workspace.numel()
+    _need(fn, ("dy", dy, bf, (capacity, n)), ("x", x, bf, (capacity, k)),
+          ("dw", dw, bf if dw.dtype == bf else torch.float32, (E, n, k)),
+          ("psum", psum, torch.int32, (E,)), ("status", status, torch.int32, (2,)),
+          ("workspace", workspace, torch.uint8, (size,)))
     code = lib().moe_grouped_wgrad_bf16(
         _ptr(dy), _ptr(x), _ptr(psum), _ptr(status), capacity, n, k, E, align,
         MOE_GRAD_BF16 if dw.dtype == bf else MOE_GRAD_F32, int(bool(accumulate)), _ptr(dw),
@@ -365,10 +363,10 @@ def moe_silu_mul_bf16_backward(gate_up, dy, m_indices, psum, status, num_experts
     import torch
     fn, bf = "moe_silu_mul_bf16_backward", torch.bfloat16
     capacity, inter = dy.shape
-    _need(fn, "gate_up", gate_up, bf, (capacity, 2 * inter))
-    _need(fn, "dy", dy, bf, (capacity, inter))
-    _need(fn, "d_gate_up", d_gate_up, bf, (capacity, 2 * inter))
-    _need_layout(fn, psum, status, num_experts, m_indices, capacity)
+    _need(fn, ("gate_up", gate_up, bf, (capacity, 2 * inter)), ("dy", dy, bf, (capacity, inter)),
+          ("d_gate_up", d_gate_up, bf, (capacity, 2 * inter)),
+          ("m_indices", m_indices, torch.int32, (capacity,)),
+          ("psum", psum, torch.int32, (num_experts,)), ("status", status, torch.int32, (2,)))
     code = lib().moe_silu_mul_bf16_backward(
         _ptr(gate_up), _ptr(dy), _ptr(m_indices), _ptr(psum), _ptr(status), capacity, inter,
         num_experts, align, _ptr(d_gate_up), _stream(stream))
@@ -383,21 +381,16 @@ def moe_gather_backward(dout, expert_out, src2dst, topk_weights, psum_recv_per_r
     import torch
     fn, bf = "moe_gather_backward", torch.bfloat16
     (rows, topk), (capacity, hidden) = src2dst.shape, d_expert_out.shape
-    _need(fn, "dout", dout, bf, (rows, hidden))
-    _need(fn, "src2dst", src2dst, torch.int32, (rows, topk))
-    _need(fn, "d_expert_out", d_expert_out, bf, (capacity, hidden))
-    if expert_out is not None:
-        _need(fn, "expert_out", expert_out, bf, (capacity, hidden))
-    for name, t in (("topk_weights", topk_weights), ("d_topk_weights", d_topk_weights)):
-        if t is not None:
-            _need(fn, name, t, torch.float32, (rows, topk))
-    if psum_recv_per_rank is not None:
-        _need(fn, "psum_recv_per_rank", psum_recv_per_rank, torch.int32,
-              (psum_recv_per_rank.numel(),))
+    nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
+    _need(fn, ("dout", dout, bf, (rows, hidden)), ("src2dst", src2dst, torch.int32, (rows, topk)),
+          ("d_expert_out", d_expert_out, bf, (capacity, hidden)),
+          ("expert_out", expert_out, bf, (capacity, hidden)),
+          ("topk_weights", topk_weights, torch.float32, (rows, topk)),
+          ("d_topk_weights", d_topk_weights, torch.float32, (rows, topk)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
     code = lib().moe_gather_backward(
         _ptr(dout), _ptr(expert_out), _ptr(src2dst), _ptr(topk_weights),
-        float(routed_scaling_factor), _ptr(psum_recv_per_rank),
-        0 if psum_recv_per_rank is None else psum_recv_per_rank.numel(), rows, hidden, topk,
+        float(routed_scaling_factor), _ptr(psum_recv_per_rank), nsrc, rows, hidden, topk,
         capacity, _ptr(d_expert_out), _ptr(d_topk_weights), _stream(stream))
     _check(fn, code)
 
@@ -426,17 +419,15 @@ class AdamWTensors:
         for i, (master, grad, m, v, param, ms, vs) in enumerate(self.entries):
             shape, n = master.shape, master.numel()
             fp8 = ms is not None
-            _need(fn, f"master {i}", master, f32, shape)
-            _need(fn, f"grad {i}", grad, (bf, f32), shape)
-            for name, t, sc in (("m", m, ms), ("v", v, vs)):
-                _need(fn, f"{name} {i}", t, codes if fp8 else f32, shape)
-                if fp8:
-                    _need(fn, f"{name}_scale {i}", sc, f32,
-                          (-(-n // MOE_STATE_GROUP),))
-                elif sc is not None:
-                    raise ValueError(f"{fn}: tensor {i} has one state with a scale only")
-            if param is not None:
-                _need(fn, f"param {i}", param, bf, shape)
+            if fp8 != (vs is not None):
+                raise ValueError(f"{fn}: tensor {i} has one state with a scale only")
+            state = lambda t: (t.dtype if t.dtype in codes else codes[0]) if fp8 else f32  # noqa: E731
+            groups = (-(-n // MOE_STATE_GROUP),)
+            _need(fn, (f"master {i}", master, f32, shape),
+                  (f"grad {i}", grad, bf if grad.dtype == bf else f32, shape),
+                  (f"m {i}", m, state(m), shape), (f"v {i}", v, state(v), shape),
+                  (f"param {i}", param, bf, shape), (f"m_scale {i}", ms, f32, groups),
+                  (f"v_scale {i}", vs, f32, groups))
             self.array[i] = _AdamWTensor(
                 _ptr(master), _ptr(grad), _ptr(m), _ptr(v), _ptr(param), _ptr(ms), _ptr(vs), n,
                 MOE_GRAD_BF16 if grad.dtype == bf else MOE_GRAD_F32,
@@ -449,10 +440,8 @@ def moe_adamw(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=
     of this step, from 1), lr and grad_scale fp32 [1], all on the GPU."""
     import torch
     fn = "moe_adamw"
-    _need(fn, "step", step, torch.int64, (1,))
-    _need(fn, "lr", lr, torch.float32, (1,))
-    if grad_scale is not None:
-        _need(fn, "grad_scale", grad_scale, torch.float32, (1,))
+    _need(fn, ("step", step, torch.int64, (1,)), ("lr", lr, torch.float32, (1,)),
+          ("grad_scale", grad_scale, torch.float32, (1,)))
     code = lib().moe_adamw(tensors.array, len(tensors.entries), _ptr(step), _ptr(lr),
                            _ptr(grad_scale), beta1, beta2, eps, weight_decay, _stream(stream))
     _check(fn, code)

@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libmoe_expand.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["abi.cpp", "layout.hip", "gemm.hip", "act_quant.hip", "gather.hip", "masked.hip",
-           "dgrad.hip", "wgrad.hip", "silu_backward.hip",
+           "dgrad.hip", "wgrad.hip", "grad_narrow.hip", "silu_backward.hip",
            "gather_backward.hip", "adamw.hip"]
 
 FLAGS = [

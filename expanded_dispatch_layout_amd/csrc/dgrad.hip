@@ -23,6 +23,8 @@ constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
 constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of stages)
 constexpr int FI = 4, FJ = 8;                  // 16-wide tiles per wave: 64 columns, 128 rows
 
+constexpr int64_t kMinTiles = 256;
+
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row: the 16 rows that
 // a fragment reads at one chunk fall on different banks.
 __device__ __forceinline__ int a_key(int row) { return (row & 7) ^ ((row >> 3) & 1); }
@@ -284,6 +286,9 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
     return MOE_ERR_ALIGNMENT;
   if (capacity == 0) return MOE_OK;
   const int64_t max_items = ((capacity + TM - 1) / TM + num_experts) * (int64_t)((k + TK - 1) / TK);
+  if (max_items < kMinTiles)
+    return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx,
+                               reinterpret_cast<hipStream_t>(stream));
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
   if (grid > max_items) grid = max_items;
   grid = (grid + kXcds - 1) / kXcds * kXcds;

@@ -1,4 +1,4 @@
-// Argument checks that the grouped products' gradients share.
+// What the grouped products' gradients share.
 #pragma once
 
 #include "common.hpp"
@@ -18,5 +18,15 @@ inline moe_status check_backward_sizes(int64_t capacity, int n, int k, int num_e
   if (n / 64 > kMaxBlocks64 || k / 64 > kMaxBlocks64) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
+
+// Launches of grad_narrow.hip.
+constexpr int kNarrowTile = 64;
+moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psum,
+                               const int32_t* status, int64_t capacity, int n, int k,
+                               int num_experts, int align, void* dx, hipStream_t s);
+moe_status launch_wgrad_narrow(const void* dy, const void* x, const int32_t* psum,
+                               const int32_t* status, int64_t capacity, int n, int k,
+                               int num_experts, int align, moe_grad_fmt fmt, int accumulate,
+                               int splits, void* dw, void* workspace, hipStream_t s);
 
 }  // namespace moe

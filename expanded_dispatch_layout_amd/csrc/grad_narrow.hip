@@ -1,0 +1,345 @@
+// The grouped products' gradients where the 256 x 256 tiles of dgrad.hip and
+// wgrad.hip are too few to fill the CUs: 64 x 64 tiles, the reduction split
+// over the eight waves of a workgroup (and, for the weight gradient, over
+// workgroups too).
+//
+//  - A wave takes every eighth 32-deep stage of the reduction.  Its stages are
+//    its own: it loads them HBM -> LDS into its own two slots of 8 KB and
+//    waits for its own loads only, so there is no barrier in the loop.
+//  - The eight partial tiles (fp32) meet in LDS, each in its wave's own slots,
+//    and are summed in the waves' order: equal calls give equal bits.
+//  - Each stage is 64 MFMA-rows and 64 MFMA-columns by 32: 16
+//    v_mfma_f32_16x16x32_bf16 on fragments read through ds_read_b64_tr_b16
+//    where the reduction runs along the staged rows (w, and both operands of
+//    the weight gradient), and as 16-byte pieces where it runs along the
+//    columns (dy of the input gradient).
+#include "gemm_backward.hpp"
+#include "lds_dma.hpp"
+
+namespace moe {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 512, kWaves = 8;
+constexpr int T = kNarrowTile;            // 64
+constexpr int kStep = 32;
+constexpr int kOpBytes = 4096;            // one operand of a stage: 32 x 64 bf16
+constexpr int kSlotBytes = 2 * kOpBytes;
+constexpr int kWaveBytes = 2 * kSlotBytes;  // two slots; later one fp32 64 x 64 tile
+constexpr int kLoads = 8;                 // per stage
+static_assert(kWaveBytes == T * T * 4, "a partial tile fills its wave's slots");
+
+// Row-staged operand (reduction along the rows): 32 rows of 128 bytes.  Four
+// 32-byte pieces per row, XOR-swizzled by row so that the 8 rows that half a
+// wave reads at once fall on different banks (two rows make 256 bytes).
+__device__ __forceinline__ int row_key(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
+// Column-staged operand (reduction along the columns): 64 rows of 64 bytes,
+// four 16-byte chunks per row, XOR-swizzled by row / 4.
+__device__ __forceinline__ int col_key(int row) { return (row >> 2) & 3; }
+
+// Fragment addresses of this lane within an operand: tile i is at ^ (i << 5)
+// (row-staged) or + i * 1024 (column-staged).
+__device__ __forceinline__ uint32_t row_lane(int lane) {
+  const int row = 8 * (lane >> 4) + ((lane & 15) >> 2), q = lane & 3;
+  return (uint32_t)(row * 128 + row_key(row) * 32 + (q >> 1) * 16 + (q & 1) * 8);
+}
+__device__ __forceinline__ uint32_t col_lane(int lane) {
+  const int row = lane & 15;
+  return (uint32_t)(row * 64 + (((lane >> 4) ^ col_key(row)) << 4));
+}
+
+// Loads q = 0..3 of a row-staged operand: rows 8 q + lane / 8, from a matrix
+// whose row 0 and column 0 are at src (pitch ld bytes); rows >= nr are zeros.
+__device__ __forceinline__ void load_rows(const uint8_t* src, int64_t ld, int nr, uint32_t lds,
+                                          int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = 8 * q + (lane >> 3);
+    const uint8_t* p = src + row * ld + (((lane & 7) ^ (row_key(row) << 1)) << 4);
+    dma16_ptr(row < nr ? p : zero_chunk(), lds + q * 1024);
+  }
+}
+// The same of a column-staged operand: rows 16 q + lane / 4.
+__device__ __forceinline__ void load_cols(const uint8_t* src, int64_t ld, int nr, uint32_t lds,
+                                          int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = 16 * q + (lane >> 2);
+    const uint8_t* p = src + row * ld + (((lane & 3) ^ col_key(row)) << 4);
+    dma16_ptr(row < nr ? p : zero_chunk(), lds + q * 1024);
+  }
+}
+
+// Sum over this wave's stages s = s0, s0 + ds, .. < ns: load(s, lds) issues a
+// stage's loads; x's fragments (the tile's columns) are row-staged, y's (its
+// rows) row- or column-staged.
+template <bool kYRows, typename Load>
+__device__ __forceinline__ void wave_sum(int s0, int ds, int ns, uint32_t base, int lane,
+                                         Load&& load, v4f (&acc)[4][4]) {
+  const uint32_t fx = base + kOpBytes + row_lane(lane);
+  const uint32_t fy = base + (kYRows ? row_lane(lane) : col_lane(lane));
+  if (s0 < ns) load(s0, base);
+  if (s0 + ds < ns) load(s0 + ds, base + kSlotBytes);
+  uint32_t slot = 0;
+  for (int s = s0; s < ns; s += ds) {
+    if (s + ds < ns) wait_vmcnt<kLoads>();
+    else wait_vmcnt<0>();
+    bf16x8 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = frag_tr<128>((fx + slot) ^ (uint32_t)(i << 5));
+      if constexpr (kYRows) y[i] = frag_tr<128>((fy + slot) ^ (uint32_t)(i << 5));
+      else y[i] = lds_load<bf16x8>(fy + slot + i * 1024);
+    }
+    wait_lgkm0();  // the slot has been read: it may be loaded anew
+    sched_fence();
+    if (s + 2 * ds < ns) load(s + 2 * ds, base + slot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+    slot ^= kSlotBytes;
+  }
+}
+
+// The eight waves' tiles -> their sum: thread t gets row t / 8, columns
+// 8 (t % 8) + 0..7.  16-byte chunks are XOR-swizzled by row.
+__device__ __forceinline__ void join_waves(uint32_t lds0, int wid, int lane,
+                                           const v4f (&acc)[4][4], float (&out)[8]) {
+  const uint32_t own = lds0 + wid * kWaveBytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = j * 16 + (lane & 15), c = i * 4 + (lane >> 4);
+      lds_store<v4f>(own + row * 256 + ((c ^ (row & 15)) << 4), acc[i][j]);
+    }
+  __syncthreads();
+  const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;
+  v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const uint32_t r = lds0 + w * kWaveBytes + row * 256;
+    lo += lds_load<v4f>(r + ((c ^ (row & 15)) << 4));
+    hi += lds_load<v4f>(r + (((c + 1) ^ (row & 15)) << 4));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = lo[i], out[4 + i] = hi[i];
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]),
+               pk_bf16(v[6], v[7])};
+}
+
+// 8 consecutive gradients to dw (fp32 or bf16), added to what is there.
+template <bool kF32>
+__device__ __forceinline__ void store_grad8(void* dw, int64_t at, const float (&v)[8],
+                                            int accumulate) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+  if constexpr (kF32) {
+    v4f* o = reinterpret_cast<v4f*>((float*)dw + at);
+    v4f lo = {r[0], r[1], r[2], r[3]}, hi = {r[4], r[5], r[6], r[7]};
+    if (accumulate) {
+      lo += o[0];
+      hi += o[1];
+    }
+    o[0] = lo;
+    o[1] = hi;
+  } else {
+    u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)dw + at);
+    if (accumulate) {
+      const u32x4 q = *o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[2 * i] += __uint_as_float(q[i] << 16);
+        r[2 * i + 1] += __uint_as_float(q[i] & 0xffff0000u);
+      }
+    }
+    *o = pack8(r);
+  }
+}
+
+// Live rows [st, en) of expert e.
+__device__ __forceinline__ void expert_rows(const int32_t* psum, int64_t nrows, int align, int e,
+                                            int64_t& st, int64_t& en) {
+  st = e ? max(0, align_up_i(psum[e - 1], align)) : 0;
+  en = min((int64_t)psum[e], nrows);
+}
+
+__global__ __launch_bounds__(kThreads) void dgrad_narrow_kernel(
+    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ w,
+    const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
+    int k, int E, int align, uint16_t* __restrict__ dx) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kWaveBytes];
+  __shared__ int gp[MOE_MAX_EXPERTS + 1];  // prefix of 64-row groups per expert
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds0 = lds_addr(lds);
+  const int64_t nrows = min((int64_t)status[0], capacity);
+  if (wid == 0) {
+    int sum = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      int ng = 0;
+      if (e < E) {
+        int64_t st, en;
+        expert_rows(psum, nrows, align, e, st, en);
+        ng = en > st ? (int)((en - st + T - 1) / T) : 0;
+      }
+      const int incl = wave_incl_scan_i(ng);
+      if (e < E) gp[e] = sum + incl - ng;
+      sum += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) gp[E] = sum;
+  }
+  __syncthreads();
+  const int NT = k / T;
+  const int64_t nitems = (int64_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT;
+  const int per_xcd = gridDim.x / kXcds;
+  for (int64_t item = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+       item < nitems; item += gridDim.x) {
+    const int q = (int)(item / NT);
+    int lo = 0, hi = E - 1;  // last e with gp[e] <= q
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (gp[mid] <= q) lo = mid;
+      else hi = mid - 1;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
+    const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
+    const int local = (int)(item - (int64_t)NT * g0);
+    const int t0 = local / ge * T;
+    int64_t st, en;
+    expert_rows(psum, nrows, align, e, st, en);
+    const int64_t m0 = st + (int64_t)(local % ge) * T;
+    const int live = (int)min((int64_t)T, en - m0);
+    const uint8_t* a = dy + m0 * n * 2;
+    const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
+    v4f acc[4][4] = {};
+    wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
+                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                      load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
+                      load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
+                                dst + kOpBytes, lane);
+                    },
+                    acc);
+    float v[8];
+    join_waves(lds0, wid, lane, acc, v);
+    const int row = threadIdx.x >> 3;
+    if (row < live)
+      *reinterpret_cast<u32x4*>(dx + (m0 + row) * k + t0 + (threadIdx.x & 7) * 8) = pack8(v);
+    __syncthreads();  // the partial tiles have been read
+  }
+}
+
+// splits > 1: this workgroup's part of the sum goes to part[z][e][j][t].
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
+    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
+    const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
+    int k, int E, int align, int accumulate, int splits, void* __restrict__ dw,
+    float* __restrict__ part) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kWaveBytes];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds0 = lds_addr(lds);
+  const int64_t nrows = min((int64_t)status[0], capacity);
+  const int NJ = n / T, NT = k / T;
+  const int64_t nitems = (int64_t)E * NJ * NT * splits;
+  for (int64_t item = blockIdx.x; item < nitems; item += gridDim.x) {
+    const int z = (int)(item % splits);
+    const int64_t tile = item / splits;
+    const int t0 = (int)(tile % NT) * T, j0 = (int)(tile / NT % NJ) * T;
+    const int e = (int)(tile / ((int64_t)NT * NJ));
+    int64_t st, en;
+    expert_rows(psum, nrows, align, e, st, en);
+    const int live = en > st ? (int)(en - st) : 0;
+    if (live == 0 && accumulate && splits == 1) continue;  // dw[e] stays (uniform)
+    const uint8_t* a = dy + (st * n + j0) * 2;
+    const uint8_t* b = x + (st * k + t0) * 2;
+    v4f acc[4][4] = {};
+    wave_sum<true>(z * kWaves + wid, splits * kWaves, (live + kStep - 1) / kStep,
+                   lds0 + wid * kWaveBytes, lane,
+                   [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                     const int64_t r = (int64_t)s * kStep;
+                     const int nr = (int)min((int64_t)kStep, live - r);
+                     load_rows(a + r * n * 2, (int64_t)n * 2, nr, dst, lane);
+                     load_rows(b + r * k * 2, (int64_t)k * 2, nr, dst + kOpBytes, lane);
+                   },
+                   acc);
+    float v[8];
+    join_waves(lds0, wid, lane, acc, v);
+    const int64_t at =
+        ((int64_t)e * n + j0 + (threadIdx.x >> 3)) * k + t0 + (threadIdx.x & 7) * 8;
+    if (splits > 1) {
+      v4f* o = reinterpret_cast<v4f*>(part + (int64_t)z * E * n * k + at);
+      o[0] = v4f{v[0], v[1], v[2], v[3]};
+      o[1] = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+      store_grad8<kF32>(dw, at, v, accumulate);
+    }
+    __syncthreads();  // the partial tiles have been read
+  }
+}
+
+// dw = (dw +) the sum of the parts, in their order.
+template <bool kF32>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part,
+                                                         int splits, int64_t count,
+                                                         int accumulate, void* __restrict__ dw) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= count) return;
+  v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+  for (int z = 0; z < splits; ++z) {
+    const v4f* p = reinterpret_cast<const v4f*>(part + z * count + at);
+    lo += p[0];
+    hi += p[1];
+  }
+  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  store_grad8<kF32>(dw, at, v, accumulate);
+}
+
+}  // namespace
+
+moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psum,
+                               const int32_t* status, int64_t capacity, int n, int k,
+                               int num_experts, int align, void* dx, hipStream_t s) {
+  int64_t grid = ((capacity + T - 1) / T + num_experts) * (int64_t)(k / T);
+  if (grid > 2048) grid = 2048;
+  grid = (grid + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL(dgrad_narrow_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
+                     (const uint8_t*)dy, (const uint8_t*)w, psum, status, capacity, n, k,
+                     num_experts, align, (uint16_t*)dx);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+moe_status launch_wgrad_narrow(const void* dy, const void* x, const int32_t* psum,
+                               const int32_t* status, int64_t capacity, int n, int k,
+                               int num_experts, int align, moe_grad_fmt fmt, int accumulate,
+                               int splits, void* dw, void* workspace, hipStream_t s) {
+  const bool f32 = fmt == MOE_GRAD_F32;
+  int64_t grid = (int64_t)num_experts * (n / T) * (k / T) * splits;
+  if (grid > 4096) grid = 4096;
+  auto kern = f32 ? wgrad_narrow_kernel<true> : wgrad_narrow_kernel<false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, (const uint8_t*)dy,
+                     (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,
+                     accumulate, splits, dw, (float*)workspace);
+  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
+  if (splits > 1) {
+    const int64_t count = (int64_t)num_experts * n * k;
+    auto join = f32 ? wgrad_join_kernel<true> : wgrad_join_kernel<false>;
+    hipLaunchKernelGGL(join, dim3((unsigned)((count + 2047) / 2048)), dim3(256), 0, s,
+                       (const float*)workspace, splits, count, accumulate, dw);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -21,6 +21,9 @@ constexpr int kLds = kRing; // 160 KB
 constexpr int kLoads = 4;                      // DMA instructions per wave and stage
 constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
 
+constexpr int64_t kMinTiles = 256;
+constexpr int64_t kMaxSplitTiles = 512;
+
 struct Tile {
   int e, j0, t0;
   int64_t st;  // first row
@@ -213,9 +216,32 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
 
 using namespace moe;
 
+namespace moe {
+namespace {
+
+int64_t wide_tiles(int n, int k, int num_experts) {
+  return (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
+}
+
+// Parts that each expert's sum is cut into.  Only the narrow tiles are split,
+// where they leave workgroups to spare, and at most so that a wave keeps two
+// stages of an average expert's rows.
+int wgrad_splits(int64_t capacity, int n, int k, int num_experts) {
+  if (wide_tiles(n, k, num_experts) >= kMinTiles) return 1;
+  const int64_t tiles = (int64_t)num_experts * (n / kNarrowTile) * (k / kNarrowTile);
+  const int64_t by_rows = capacity / num_experts / (8 * kStep * 2);
+  const int64_t s = min(kMaxSplitTiles / tiles, by_rows);
+  return s > 1 ? (int)s : 1;
+}
+
+}  // namespace
+}  // namespace moe
+
 extern "C" size_t moe_grouped_wgrad_workspace_bytes(int64_t capacity, int n, int k,
                                                     int num_experts) {
-  return 0;
+  if (check_backward_sizes(capacity, n, k, num_experts, MOE_MIN_ALIGN) != MOE_OK) return 0;
+  const int splits = wgrad_splits(capacity, n, k, num_experts);
+  return splits > 1 ? (size_t)splits * num_experts * n * k * sizeof(float) : 0;
 }
 
 extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, const int32_t* psum,
@@ -230,7 +256,18 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
   if (capacity > 0 && (!dy || !x)) return MOE_ERR_NULL;
   if (((uintptr_t)dy % 16) || ((uintptr_t)x % 16) || ((uintptr_t)dw % 16))
     return MOE_ERR_ALIGNMENT;
-  const int64_t items = (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
+  const int splits = wgrad_splits(capacity, n, k, num_experts);
+  if (splits > 1) {
+    if (!workspace ||
+        workspace_bytes < moe_grouped_wgrad_workspace_bytes(capacity, n, k, num_experts))
+      return MOE_ERR_WORKSPACE;
+    if ((uintptr_t)workspace % 256) return MOE_ERR_ALIGNMENT;
+  }
+  const int64_t items = wide_tiles(n, k, num_experts);
+  if (items < kMinTiles)
+    return launch_wgrad_narrow(dy, x, psum, status, capacity, n, k, num_experts, align, fmt,
+                               accumulate, splits, dw, workspace,
+                               reinterpret_cast<hipStream_t>(stream));
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
   if (grid > items) grid = items;
   grid = (grid + kXcds - 1) / kXcds * kXcds;

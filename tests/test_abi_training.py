@@ -167,9 +167,9 @@ def test_binding_refuses_what_the_library_cannot_see():
         M.moe_grouped_dgrad_bf16(z(64, 128), z(2, 128, 64), psum, st, 32, z(64, 64))
     with pytest.raises(ValueError, match="contiguous"):
         M.moe_grouped_dgrad_bf16(z(128, 64).t(), z(2, 128, 64), psum, st, 32, z(64, 64))
-    with pytest.raises(ValueError, match="dw must be"):
-        # dy and x are on the CPU too, but shapes are looked at first
-        M._need("moe_grouped_wgrad_bf16", "dw", z(2, 128, 64, d=torch.float16),
-                (bf, torch.float32), (2, 128, 64))
-    with pytest.raises(ValueError, match="m must be"):
-        M._need("AdamWTensors", "m", z(5), torch.float32, (5,))
+    with pytest.raises(ValueError, match="dy must be"):
+        M.moe_grouped_wgrad_bf16(z(64, 128, d=torch.float16), z(64, 64), psum, st, 32,
+                                 z(2, 128, 64))
+    with pytest.raises(ValueError, match="master 0 must be"):
+        f = z(5, d=torch.float32)
+        M.AdamWTensors([(z(5), f, f, f, None, None, None)])

@@ -1,12 +1,10 @@
 // moe_grouped_dgrad_bf16: input gradient of the grouped bf16 GEMM,
 //   dx[m, t] = sum_j dy[m, j] * w[e, j, t] for the live rows m of expert e.
 #include "gemm_backward.hpp"
-#include "lds_dma.hpp"
 
 namespace moe {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;                  // 8 waves, two per SIMD
@@ -23,7 +21,7 @@ constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
 constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of stages)
 constexpr int FI = 4, FJ = 8;                  // 16-wide tiles per wave: 64 columns, 128 rows
 
-constexpr int64_t kMinTiles = 256;
+constexpr int64_t kMinTiles = 80;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row: the 16 rows that
 // a fragment reads at one chunk fall on different banks.

@@ -1,7 +1,7 @@
 // What the grouped products' gradients share.
 #pragma once
 
-#include "common.hpp"
+#include "lds_dma.hpp"
 
 namespace moe {
 
@@ -19,6 +19,43 @@ inline moe_status check_backward_sizes(int64_t capacity, int n, int k, int num_e
   return MOE_OK;
 }
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]),
+               pk_bf16(v[6], v[7])};
+}
+
+// 8 consecutive gradients to dw (fp32 or bf16), added to what is there.
+template <bool kF32>
+__device__ __forceinline__ void store_grad8(void* dw, int64_t at, const float (&v)[8],
+                                            int accumulate) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+  if constexpr (kF32) {
+    v4f* o = reinterpret_cast<v4f*>((float*)dw + at);
+    v4f lo = {r[0], r[1], r[2], r[3]}, hi = {r[4], r[5], r[6], r[7]};
+    if (accumulate) {
+      lo += o[0];
+      hi += o[1];
+    }
+    o[0] = lo;
+    o[1] = hi;
+  } else {
+    u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)dw + at);
+    if (accumulate) {
+      const u32x4 q = *o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[2 * i] += __uint_as_float(q[i] << 16);
+        r[2 * i + 1] += __uint_as_float(q[i] & 0xffff0000u);
+      }
+    }
+    *o = pack8(r);
+  }
+}
+
 // Launches of grad_narrow.hip.
 constexpr int kNarrowTile = 64;
 moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psum,
@@ -27,6 +64,6 @@ moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psu
 moe_status launch_wgrad_narrow(const void* dy, const void* x, const int32_t* psum,
                                const int32_t* status, int64_t capacity, int n, int k,
                                int num_experts, int align, moe_grad_fmt fmt, int accumulate,
-                               int splits, void* dw, void* workspace, hipStream_t s);
+                               void* dw, hipStream_t s);
 
 }  // namespace moe

@@ -1,7 +1,6 @@
 // The grouped products' gradients where the 256 x 256 tiles of dgrad.hip and
 // wgrad.hip are too few to fill the CUs: 64 x 64 tiles, the reduction split
-// over the eight waves of a workgroup (and, for the weight gradient, over
-// workgroups too).
+// over the eight waves of a workgroup 
 //
 //  - A wave takes every eighth 32-deep stage of the reduction.  Its stages are
 //    its own: it loads them HBM -> LDS into its own two slots of 8 KB and
@@ -14,12 +13,10 @@
 //    the weight gradient), and as 16-byte pieces where it runs along the
 //    columns (dy of the input gradient).
 #include "gemm_backward.hpp"
-#include "lds_dma.hpp"
 
 namespace moe {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512, kWaves = 8;
@@ -130,41 +127,6 @@ __device__ __forceinline__ void join_waves(uint32_t lds0, int wid, int lane,
   for (int i = 0; i < 4; ++i) out[i] = lo[i], out[4 + i] = hi[i];
 }
 
-__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
-  return u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]),
-               pk_bf16(v[6], v[7])};
-}
-
-// 8 consecutive gradients to dw (fp32 or bf16), added to what is there.
-template <bool kF32>
-__device__ __forceinline__ void store_grad8(void* dw, int64_t at, const float (&v)[8],
-                                            int accumulate) {
-  float r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = v[i];
-  if constexpr (kF32) {
-    v4f* o = reinterpret_cast<v4f*>((float*)dw + at);
-    v4f lo = {r[0], r[1], r[2], r[3]}, hi = {r[4], r[5], r[6], r[7]};
-    if (accumulate) {
-      lo += o[0];
-      hi += o[1];
-    }
-    o[0] = lo;
-    o[1] = hi;
-  } else {
-    u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)dw + at);
-    if (accumulate) {
-      const u32x4 q = *o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r[2 * i] += __uint_as_float(q[i] << 16);
-        r[2 * i + 1] += __uint_as_float(q[i] & 0xffff0000u);
-      }
-    }
-    *o = pack8(r);
-  }
-}
-
 // Live rows [st, en) of expert e.
 __device__ __forceinline__ void expert_rows(const int32_t* psum, int64_t nrows, int align, int e,
                                             int64_t& st, int64_t& en) {
@@ -239,34 +201,29 @@ __global__ __launch_bounds__(kThreads) void dgrad_narrow_kernel(
   }
 }
 
-// splits > 1: this workgroup's part of the sum goes to part[z][e][j][t].
 template <bool kF32>
 __global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
-    int k, int E, int align, int accumulate, int splits, void* __restrict__ dw,
-    float* __restrict__ part) {
+    int k, int E, int align, int accumulate, void* __restrict__ dw) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kWaveBytes];
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_addr(lds);
   const int64_t nrows = min((int64_t)status[0], capacity);
   const int NJ = n / T, NT = k / T;
-  const int64_t nitems = (int64_t)E * NJ * NT * splits;
+  const int64_t nitems = (int64_t)E * NJ * NT;
   for (int64_t item = blockIdx.x; item < nitems; item += gridDim.x) {
-    const int z = (int)(item % splits);
-    const int64_t tile = item / splits;
-    const int t0 = (int)(tile % NT) * T, j0 = (int)(tile / NT % NJ) * T;
-    const int e = (int)(tile / ((int64_t)NT * NJ));
+    const int t0 = (int)(item % NT) * T, j0 = (int)(item / NT % NJ) * T;
+    const int e = (int)(item / ((int64_t)NT * NJ));
     int64_t st, en;
     expert_rows(psum, nrows, align, e, st, en);
     const int live = en > st ? (int)(en - st) : 0;
-    if (live == 0 && accumulate && splits == 1) continue;  // dw[e] stays (uniform)
+    if (live == 0 && accumulate) continue;  // dw[e] stays (uniform)
     const uint8_t* a = dy + (st * n + j0) * 2;
     const uint8_t* b = x + (st * k + t0) * 2;
     v4f acc[4][4] = {};
-    wave_sum<true>(z * kWaves + wid, splits * kWaves, (live + kStep - 1) / kStep,
-                   lds0 + wid * kWaveBytes, lane,
+    wave_sum<true>(wid, kWaves, (live + kStep - 1) / kStep, lds0 + wid * kWaveBytes, lane,
                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
                      const int64_t r = (int64_t)s * kStep;
                      const int nr = (int)min((int64_t)kStep, live - r);
@@ -278,32 +235,9 @@ __global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
     join_waves(lds0, wid, lane, acc, v);
     const int64_t at =
         ((int64_t)e * n + j0 + (threadIdx.x >> 3)) * k + t0 + (threadIdx.x & 7) * 8;
-    if (splits > 1) {
-      v4f* o = reinterpret_cast<v4f*>(part + (int64_t)z * E * n * k + at);
-      o[0] = v4f{v[0], v[1], v[2], v[3]};
-      o[1] = v4f{v[4], v[5], v[6], v[7]};
-    } else {
-      store_grad8<kF32>(dw, at, v, accumulate);
-    }
+    store_grad8<kF32>(dw, at, v, accumulate);
     __syncthreads();  // the partial tiles have been read
   }
-}
-
-// dw = (dw +) the sum of the parts, in their order.
-template <bool kF32>
-__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part,
-                                                         int splits, int64_t count,
-                                                         int accumulate, void* __restrict__ dw) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (at >= count) return;
-  v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-  for (int z = 0; z < splits; ++z) {
-    const v4f* p = reinterpret_cast<const v4f*>(part + z * count + at);
-    lo += p[0];
-    hi += p[1];
-  }
-  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  store_grad8<kF32>(dw, at, v, accumulate);
 }
 
 }  // namespace
@@ -323,23 +257,15 @@ moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psu
 moe_status launch_wgrad_narrow(const void* dy, const void* x, const int32_t* psum,
                                const int32_t* status, int64_t capacity, int n, int k,
                                int num_experts, int align, moe_grad_fmt fmt, int accumulate,
-                               int splits, void* dw, void* workspace, hipStream_t s) {
+                               void* dw, hipStream_t s) {
   const bool f32 = fmt == MOE_GRAD_F32;
-  int64_t grid = (int64_t)num_experts * (n / T) * (k / T) * splits;
+  int64_t grid = (int64_t)num_experts * (n / T) * (k / T);
   if (grid > 4096) grid = 4096;
   auto kern = f32 ? wgrad_narrow_kernel<true> : wgrad_narrow_kernel<false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, (const uint8_t*)dy,
                      (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,
-                     accumulate, splits, dw, (float*)workspace);
-  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
-  if (splits > 1) {
-    const int64_t count = (int64_t)num_experts * n * k;
-    auto join = f32 ? wgrad_join_kernel<true> : wgrad_join_kernel<false>;
-    hipLaunchKernelGGL(join, dim3((unsigned)((count + 2047) / 2048)), dim3(256), 0, s,
-                       (const float*)workspace, splits, count, accumulate, dw);
-    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
-  }
-  return MOE_OK;
+                     accumulate, dw);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
 }  // namespace moe

@@ -132,22 +132,25 @@ __device__ __forceinline__ auto frag_tr(uint32_t addr) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Two 16x16 MFMA results that are neighbours along their rows (lane l holds
-// rows 4 (l / 16) + 0..3 of column l % 16 of each) as bf16: afterwards lane l
-// holds rows 8 ((l / 16) % 2) + 0..7 of tile l / 32, 16 consecutive bytes.
-__device__ __forceinline__ u32x4 pack_tiles(const float __attribute__((ext_vector_type(4))) x,
-                                            const float __attribute__((ext_vector_type(4))) y) {
+// Two 16x16 MFMA results that are neighbours along their rows: lane l holds
+// rows 4 (l / 16) + 0..3 of column l % 16 of each.  With register r of both
+// swapped for every r, lane l holds rows 8 ((l / 16) % 2) + 0..3 (in x) and
+// + 4..7 (in y) of tile l / 32: 8 consecutive values.
+__device__ __forceinline__ void swap_tiles(uint32_t& x, uint32_t& y) {
+  // x's upper half against y's lower half, then x's odd 16-lane rows against
+  // y's even ones.
+  const auto h = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+  x = r[0];
+  y = r[1];
+}
+// The same as bf16: 16 consecutive bytes per lane.
+template <typename V4>
+__device__ __forceinline__ u32x4 pack_tiles(const V4& x, const V4& y) {
   uint32_t a[2] = {pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
   uint32_t b[2] = {pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    // a's upper half against b's lower half, then a's odd 16-lane rows
-    // against b's even ones.
-    const auto h = __builtin_amdgcn_permlane32_swap(a[i], b[i], false, false);
-    const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
-    a[i] = r[0];
-    b[i] = r[1];
-  }
+  for (int i = 0; i < 2; ++i) swap_tiles(a[i], b[i]);
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 

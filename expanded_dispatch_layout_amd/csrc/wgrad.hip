@@ -1,12 +1,12 @@
 // moe_grouped_wgrad_bf16: weight gradient of the grouped bf16 GEMM,
 //   dw[e, j, t] = sum over the live rows m of expert e of dy[m, j] * x[m, t].
+#include <math.h>
+
 #include "gemm_backward.hpp"
-#include "lds_dma.hpp"
 
 namespace moe {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
@@ -21,24 +21,31 @@ constexpr int kLds = kRing; // 160 KB
 constexpr int kLoads = 4;                      // DMA instructions per wave and stage
 constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
 
-constexpr int64_t kMinTiles = 256;
-constexpr int64_t kMaxSplitTiles = 512;
+constexpr int64_t kMinTiles = 64;
+constexpr int64_t kFullTiles = 256;  // one per CU
 
 struct Tile {
-  int e, j0, t0;
-  int64_t st;  // first row
-  int live;    // rows
+  int e, j0, t0, z;  // expert, first dy and x column, part of the sum
+  int64_t st;        // first row
+  int live;          // rows
 };
+
+// Stages of a tile: computed in pairs, so an odd count gets one of zeros.
+__device__ __forceinline__ int stages_of(int live) {
+  return 2 * ((live + 2 * kStep - 1) / (2 * kStep));
+}
 
 // Items of one expert: panels of 8 tiles along t, j-major inside a panel, so
 // that the 32 neighbouring items of an XCD's CUs are a 4 x 8 block and share
 // their operands in its L2.
-__device__ __forceinline__ Tile decode(int64_t item, int NJ, int NT, const int32_t* psum,
-                                       int64_t nrows, int align) {
+__device__ __forceinline__ Tile decode(uint32_t item, int NJ, int NT, int splits,
+                                       const int32_t* psum, int64_t nrows, int align) {
   Tile t;
-  const int per = NJ * NT;
+  const uint32_t per = NJ * NT;
+  t.z = splits > 1 ? (int)(item % (uint32_t)splits) : 0;
+  if (splits > 1) item /= (uint32_t)splits;
   t.e = (int)(item / per);
-  const int local = (int)(item % per);
+  const int local = (int)(item - t.e * per);
   const int panel = local / (8 * NJ);
   const int rem = local - panel * 8 * NJ;
   const int w = min(8, NT - panel * 8);
@@ -47,28 +54,28 @@ __device__ __forceinline__ Tile decode(int64_t item, int NJ, int NT, const int32
   t.st = t.e ? max(0, align_up_i(psum[t.e - 1], align)) : 0;
   const int64_t en = min((int64_t)psum[t.e], nrows);
   t.live = en > t.st ? (int)(en - t.st) : 0;
+  if (splits > 1) {  // part z: an even share of the stages, in pairs
+    const int share = 2 * ((stages_of(t.live) / 2 + splits - 1) / splits) * kStep;
+    t.st += (int64_t)t.z * share;
+    t.live = max(0, min(share, t.live - t.z * share));
+  }
   return t;
-}
-
-// Stages of a tile: computed in pairs, so an odd count gets one of zeros.
-__device__ __forceinline__ int stages_of(int live) {
-  return 2 * ((live + 2 * kStep - 1) / (2 * kStep));
 }
 
 template <bool kF32>
 __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
-    int k, int E, int align, int accumulate, void* __restrict__ dw) {
+    int k, int E, int align, int accumulate, int splits, void* __restrict__ dw) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_addr(lds);
   const int64_t nrows = min((int64_t)status[0], capacity);
   const int NJ = (n + TN - 1) / TN, NT = (k + TK - 1) / TK;
-  const int64_t nitems = (int64_t)E * NJ * NT;
-  const int per_xcd = gridDim.x / kXcds;
-  const int64_t first = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+  // At most 2^24 tiles (1024 experts, 128 x 128), and a split sum has few.
+  const uint32_t nitems = (uint32_t)E * NJ * NT * splits;
+  const uint32_t first = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
 
   // Fragment addresses within a stage: tile i of a wave is its 32-byte piece
   // i ^ key of a row, so one lane base serves all of them through an XOR.
@@ -81,7 +88,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   }
 
   // DMA side: the next stage to load.
-  int64_t d_item = first;
+  uint32_t d_item = first;
   int d_left = 0;    // rows left of its tile (<= 0: a stage of zeros)
   int d_stages = 0;  // stages left of its tile
   const uint8_t *d_dy = nullptr, *d_x = nullptr;
@@ -89,7 +96,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   uint32_t d_slot = 0;            // LDS offset of the next slot
   auto d_open = [&]() __attribute__((always_inline)) {  // next tile that has rows
     while (d_item < nitems) {
-      const Tile t = decode(d_item, NJ, NT, psum, nrows, align);
+      const Tile t = decode(d_item, NJ, NT, splits, psum, nrows, align);
       if (t.live > 0) {
         d_left = t.live;
         d_stages = stages_of(t.live);
@@ -138,8 +145,8 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   v4f acc[FI][FJ];
   bf16x8 a[2][FI], b[2][FJ];
 
-  for (int64_t item = first; item < nitems; item += gridDim.x) {
-    const Tile t = decode(item, NJ, NT, psum, nrows, align);
+  for (uint32_t item = first; item < nitems; item += gridDim.x) {
+    const Tile t = decode(item, NJ, NT, splits, psum, nrows, align);
     const int steps = stages_of(t.live);
 #pragma unroll
     for (int i = 0; i < FI; ++i)
@@ -177,31 +184,40 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
         }
       }
     } else if (accumulate) {
-      continue;
+      continue;  // dw[e] stays
     }
-    // Epilogue: lane holds t = 4 (lane / 16) + 0..3 of tile i, j = lane % 16 of
-    // tile j.
-    const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128 + (lane >> 4) * 4;
+    // Epilogue: the lane holds columns t = 4 (lane / 16) + 0..3 of tile i for
+    // row j = lane % 16 of tile j: in fp32 16 bytes, 64 in a row of dw.  bf16
+    // tiles are swapped in pairs for the same (8-byte stores into 32-byte
+    // pieces: PLACEHOLDER).
+    const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128;
     if (jc < n) {
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
-        const int64_t row = ((int64_t)t.e * n + jc + j * 16 + (lane & 15)) * k + tc;
+        const int64_t row =
+            (((int64_t)t.z * E + t.e) * n + jc + j * 16 + (lane & 15)) * k + tc;
 #pragma unroll
-        for (int i = 0; i < FI; ++i) {
-          if (t.t0 + wt * 128 + i * 16 < k) {
-            v4f v = acc[i][j];
-            if constexpr (kF32) {
-              v4f* o = reinterpret_cast<v4f*>((float*)dw + row + i * 16);
-              if (accumulate) v += *o;
-              *o = v;
-            } else {
-              uint2* o = reinterpret_cast<uint2*>((uint16_t*)dw + row + i * 16);
-              if (accumulate) {
-                const uint2 q = *o;
-                v += v4f{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
-                         __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)};
+        for (int i = 0; i < FI; i += 2) {
+          if (tc + i * 16 >= k) break;  // k is a multiple of 64: pairs end together
+          if constexpr (kF32) {
+            v4f* o = reinterpret_cast<v4f*>((float*)dw + row + i * 16 + (lane >> 4) * 4);
+            o[0] = accumulate ? acc[i][j] + o[0] : acc[i][j];
+            o[4] = accumulate ? acc[i + 1][j] + o[4] : acc[i + 1][j];
+          } else {
+            u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)dw + row + (i + (lane >> 5)) * 16 +
+                                                ((lane >> 4) & 1) * 8);
+            if (accumulate) {
+              float v[8];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                uint32_t x = __float_as_uint(acc[i][j][r]), y = __float_as_uint(acc[i + 1][j][r]);
+                swap_tiles(x, y);
+                v[r] = __uint_as_float(x);
+                v[4 + r] = __uint_as_float(y);
               }
-              *o = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+              store_grad8<false>(o, 0, v, 1);
+            } else {
+              *o = pack_tiles(acc[i][j], acc[i + 1][j]);
             }
           }
         }
@@ -209,6 +225,27 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     }
   }
   wait_vmcnt<0>();  // no load may land after the workgroup's LDS has been given away
+}
+
+// dw = (dw +) the sum of the parts, in their order.  One wave per workgroup and
+// several parts' loads in flight: the sum over many parts of a small dw is
+// bound by latency.
+constexpr int kJoinThreads = 64;
+template <bool kF32>
+__global__ __launch_bounds__(kJoinThreads) void wgrad_join_kernel(const float* __restrict__ part,
+                                                         int splits, int64_t count,
+                                                         int accumulate, void* __restrict__ dw) {
+  const int64_t at = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 8;
+  if (at >= count) return;
+  v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll 8
+  for (int z = 0; z < splits; ++z) {
+    const v4f* p = reinterpret_cast<const v4f*>(part + z * count + at);
+    lo += p[0];
+    hi += p[1];
+  }
+  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  store_grad8<kF32>(dw, at, v, accumulate);
 }
 
 }  // namespace
@@ -223,14 +260,17 @@ int64_t wide_tiles(int n, int k, int num_experts) {
   return (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
 }
 
-// Parts that each expert's sum is cut into.  Only the narrow tiles are split,
-// where they leave workgroups to spare, and at most so that a wave keeps two
-// stages of an average expert's rows.
+// Parts that each expert's sum is cut into where the tiles leave CUs idle.  A
+// stage of a tile takes about 0.5 us, so the sum of an average expert's R rows
+// takes R / 64 us / S in S parts; writing and joining them moves 8 S E n k
+// bytes, at about 6 bytes a picosecond.  The S that makes the sum of the two
+// smallest is the root of their ratio: PLACEHOLDER
 int wgrad_splits(int64_t capacity, int n, int k, int num_experts) {
-  if (wide_tiles(n, k, num_experts) >= kMinTiles) return 1;
-  const int64_t tiles = (int64_t)num_experts * (n / kNarrowTile) * (k / kNarrowTile);
-  const int64_t by_rows = capacity / num_experts / (8 * kStep * 2);
-  const int64_t s = min(kMaxSplitTiles / tiles, by_rows);
+  const int64_t tiles = wide_tiles(n, k, num_experts), rows = capacity / num_experts;
+  if (tiles * 2 > kFullTiles) return 1;
+  const double best =
+      sqrt((double)rows / 64.0 * 0.75e6 / ((double)num_experts * (double)n * (double)k));
+  const int64_t s = min((int64_t)best, min(kFullTiles / tiles, rows / (4 * kStep)));
   return s > 1 ? (int)s : 1;
 }
 
@@ -264,16 +304,26 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
     if ((uintptr_t)workspace % 256) return MOE_ERR_ALIGNMENT;
   }
   const int64_t items = wide_tiles(n, k, num_experts);
-  if (items < kMinTiles)
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (splits == 1 && items < kMinTiles)
     return launch_wgrad_narrow(dy, x, psum, status, capacity, n, k, num_experts, align, fmt,
-                               accumulate, splits, dw, workspace,
-                               reinterpret_cast<hipStream_t>(stream));
+                               accumulate, dw, st);
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
-  if (grid > items) grid = items;
+  if (grid > items * splits) grid = items * splits;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
-  auto kern = fmt == MOE_GRAD_F32 ? wgrad_kernel<true> : wgrad_kernel<false>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0,
-                     reinterpret_cast<hipStream_t>(stream), (const uint8_t*)dy, (const uint8_t*)x,
-                     psum, status, capacity, n, k, num_experts, align, accumulate, dw);
+  const bool f32 = fmt == MOE_GRAD_F32;
+  // The parts of a split sum are written as fp32 [splits][E][n][k].
+  auto kern = f32 || splits > 1 ? wgrad_kernel<true> : wgrad_kernel<false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, (const uint8_t*)dy,
+                     (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,
+                     splits > 1 ? 0 : accumulate, splits, splits > 1 ? workspace : dw);
+  if (splits > 1) {
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
+    const int64_t count = (int64_t)num_experts * n * k;
+    auto join = f32 ? wgrad_join_kernel<true> : wgrad_join_kernel<false>;
+    hipLaunchKernelGGL(join, dim3((unsigned)((count + 8 * kJoinThreads - 1) / (8 * kJoinThreads))),
+                       dim3(kJoinThreads), 0, st,
+                       (const float*)workspace, splits, count, accumulate, dw);
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

@@ -89,6 +89,8 @@ PRODUCTS = [
     ([3000], 256, 256, 128, 0),                        # one long reduction, few tiles
     ([1500, 0, 700], 128, 64, 128, 4),
     ([20000, 1], 128, 128, 16, 0),
+    ([40, 0, 1, 70] * 16, 384, 320, 16, 1),            # tiles enough for the wide kernels
+    ([129, 300, 0, 513, 64, 1, 256, 33] * 2, 256, 1088, 64, 1),
 ]
 PIDS = [f"{'_'.join(map(str, c[0][:4]))}-n{c[1]}-k{c[2]}-a{c[3]}" for c in PRODUCTS]
 

@@ -191,22 +191,31 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     // tiles are swapped in pairs for the same (8-byte stores into 32-byte
     // pieces: PLACEHOLDER).
     const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128;
-    if (jc < n) {
+    auto store = [&](auto add) __attribute__((always_inline)) {
+      constexpr bool kAdd = decltype(add)::value;
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
         const int64_t row =
             (((int64_t)t.z * E + t.e) * n + jc + j * 16 + (lane & 15)) * k + tc;
+        if constexpr (kF32) {
+          v4f* o = reinterpret_cast<v4f*>((float*)dw + row + (lane >> 4) * 4);
 #pragma unroll
-        for (int i = 0; i < FI; i += 2) {
-          if (tc + i * 16 >= k) break;  // k is a multiple of 64: pairs end together
-          if constexpr (kF32) {
-            v4f* o = reinterpret_cast<v4f*>((float*)dw + row + i * 16 + (lane >> 4) * 4);
-            o[0] = accumulate ? acc[i][j] + o[0] : acc[i][j];
-            o[4] = accumulate ? acc[i + 1][j] + o[4] : acc[i + 1][j];
-          } else {
+          for (int i0 = 0; i0 < FI; i0 += 4) {
+            if (tc + i0 * 16 >= k) break;  // k is a multiple of 64
+            v4f old[4];  // asked for together
+#pragma unroll
+            for (int i = 0; i < 4; ++i) old[i] = kAdd ? o[(i0 + i) * 4] : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[(i0 + i) * 4] = kAdd ? acc[i0 + i][j] + old[i] : acc[i0 + i][j];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < FI; i += 2) {
+            if (tc + i * 16 >= k) break;  // k is a multiple of 64: pairs end together
             u32x4* o = reinterpret_cast<u32x4*>((uint16_t*)dw + row + (i + (lane >> 5)) * 16 +
                                                 ((lane >> 4) & 1) * 8);
-            if (accumulate) {
+            if constexpr (kAdd) {
               float v[8];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -222,6 +231,10 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
           }
         }
       }
+    };
+    if (jc < n) {
+      if (accumulate) store(std::true_type());
+      else store(std::false_type());
     }
   }
   wait_vmcnt<0>();  // no load may land after the workgroup's LDS has been given away

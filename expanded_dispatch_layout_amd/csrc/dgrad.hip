@@ -32,11 +32,27 @@ struct Item {
   int64_t m0;
 };
 
+// The workgroups take the items in rounds.  Where the last round leaves half
+// of them idle, its items are cut into their upper and lower 128 rows, which
+// waves 0-3 compute in about half the time: PLACEHOLDER.  `whole` items come
+// first, then `count - whole` halves.
+struct Rounds {
+  int64_t whole, count;
+  __device__ __forceinline__ Rounds(int64_t items, int64_t grid) {
+    const int64_t left = items % grid;
+    const bool cut = 2 * left <= grid;
+    whole = cut ? items - left : items;
+    count = cut ? items + left : items;
+  }
+};
+
 // Item -> expert, row group and column tile.  Expert e's items are
 // [NT * gp[e], NT * gp[e+1]), column-tile-major with the row groups innermost:
 // the groups of a tile read the same weights side by side on one XCD.
-__device__ __forceinline__ Item decode(int64_t item, int NT, int E, int align, int64_t nrows,
-                                       const int* gp, const int* pe) {
+__device__ __forceinline__ Item decode(int64_t item, int64_t whole, int NT, int E, int align,
+                                       int64_t nrows, const int* gp, const int* pe) {
+  const int half = item < whole ? -1 : (int)((item - whole) & 1);
+  if (half >= 0) item = whole + ((item - whole) >> 1);
   const int q = (int)(item / NT);
   int lo = 0, hi = E - 1;  // last e with gp[e] <= q
   while (lo < hi) {
@@ -55,6 +71,11 @@ __device__ __forceinline__ Item decode(int64_t item, int NT, int E, int align, i
   it.m0 = st + (int64_t)(local % ge) * TM;
   const int64_t end = min((int64_t)__builtin_amdgcn_readfirstlane(pe[it.e]), nrows);
   it.live = (int)min((int64_t)TM, end - it.m0);
+  if (half == 0) it.live = min(it.live, TM / 2);
+  if (half == 1) {
+    it.m0 += TM / 2;
+    it.live = max(it.live - TM / 2, 0);
+  }
   return it;
 }
 
@@ -64,7 +85,8 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
                                     const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
                                     int k, int E, int align, uint16_t* dx, int lane, int wid) {
   const int NT = (k + TK - 1) / TK;
-  const int64_t nitems = (int64_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT;
+  const Rounds rounds((int64_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT, gridDim.x);
+  const int64_t whole = rounds.whole, nitems = rounds.count;
   const int per_xcd = gridDim.x / kXcds;
   const int64_t first = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
   const int steps = n / kStep;  // even: n % 128 == 0
@@ -93,7 +115,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   auto d_open = [&]() __attribute__((always_inline)) {
     d_live = 0;
     if (d_item >= nitems) return;
-    const Item it = decode(d_item, NT, E, align, nrows, gp, pe);
+    const Item it = decode(d_item, whole, NT, E, align, nrows, gp, pe);
     d_live = it.live;
     if constexpr (kW) {
       d_src = w + ((int64_t)it.e * n * k + it.t0) * 2;
@@ -159,7 +181,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   };
 
   for (int64_t item = first; item < nitems; item += gridDim.x) {
-    const Item it = decode(item, NT, E, align, nrows, gp, pe);
+    const Item it = decode(item, whole, NT, E, align, nrows, gp, pe);
     const bool busy = wr * 128 < it.live;  // uniform: the wave has live rows
 #pragma unroll
     for (int i = 0; i < FI; ++i)

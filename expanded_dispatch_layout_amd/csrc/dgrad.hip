@@ -8,20 +8,21 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;                  // 8 waves, two per SIMD
-constexpr int TM = 256, TK = 256;              // output tile: rows x columns of w
-constexpr int kStep = 32;                      // reduction per stage of w
-constexpr int kRowBytes = TK * 2;              // a staged row of w
-constexpr int kWBytes = kStep * kRowBytes;     // 16 KB
+constexpr int TM = 256;                        // rows of an output tile
+constexpr int kStep = 32;                      // reduction per step
+constexpr int kWBytes = 16384;                 // a stage of w: 32 x 256 or 64 x 128 values
 constexpr int kWStages = 5;
-constexpr int kABytes = TM * 128;              // 32 KB: 64 values of each row of dy (two stages)
-constexpr int kAStages = 2;
+// dy: 64 values of each row (two steps) per stage, two stages of 256 rows or,
+// in the 128-column tiles where no expert has more than 128, four of 128: few
+// rows leave little to compute while the loads are under way (64 rows, 8 x
+// 4096 x 2048: 42 against 57 us).
+constexpr int kARing = 2 * TM * 128;           // 64 KB
 constexpr int kABase = kWStages * kWBytes;
-constexpr int kLds = kABase + kAStages * kABytes;  // 144 KB
+constexpr int kLds = kABase + kARing;          // 144 KB
 constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
-constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of stages)
-constexpr int FI = 4, FJ = 8;                  // 16-wide tiles per wave: 64 columns, 128 rows
-
-constexpr int64_t kMinTiles = 80;
+constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of steps)
+constexpr int FJ = 8;                          // 16-row tiles per wave: 128 rows
+constexpr int64_t kMinTiles = 80, kMinWide = 256;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row: the 16 rows that
 // a fragment reads at one chunk fall on different banks.
@@ -36,11 +37,12 @@ struct Item {
 // of them idle, its items are cut into their upper and lower 128 rows, which
 // waves 0-3 compute in about half the time: PLACEHOLDER.  `whole` items come
 // first, then `count - whole` halves.
+// Items fit 32 bits: at most 2^22 + 2^10 row groups and 2^8 column tiles.
 struct Rounds {
-  int64_t whole, count;
-  __device__ __forceinline__ Rounds(int64_t items, int64_t grid) {
-    const int64_t left = items % grid;
-    const bool cut = 2 * left <= grid;
+  uint32_t whole, count;
+  __device__ __forceinline__ Rounds(uint32_t items, uint32_t grid, bool few_rows) {
+    const uint32_t left = items % grid;
+    const bool cut = 2 * left <= grid && !few_rows;
     whole = cut ? items - left : items;
     count = cut ? items + left : items;
   }
@@ -49,11 +51,12 @@ struct Rounds {
 // Item -> expert, row group and column tile.  Expert e's items are
 // [NT * gp[e], NT * gp[e+1]), column-tile-major with the row groups innermost:
 // the groups of a tile read the same weights side by side on one XCD.
-__device__ __forceinline__ Item decode(int64_t item, int64_t whole, int NT, int E, int align,
+template <int TK>
+__device__ __forceinline__ Item decode(uint32_t item, uint32_t whole, int NT, int E, int align,
                                        int64_t nrows, const int* gp, const int* pe) {
   const int half = item < whole ? -1 : (int)((item - whole) & 1);
   if (half >= 0) item = whole + ((item - whole) >> 1);
-  const int q = (int)(item / NT);
+  const int q = (int)(item / (uint32_t)NT);
   int lo = 0, hi = E - 1;  // last e with gp[e] <= q
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -64,7 +67,7 @@ __device__ __forceinline__ Item decode(int64_t item, int64_t whole, int NT, int 
   it.e = __builtin_amdgcn_readfirstlane(lo);
   const int g0 = __builtin_amdgcn_readfirstlane(gp[it.e]);
   const int ge = __builtin_amdgcn_readfirstlane(gp[it.e + 1]) - g0;
-  const int local = (int)(item - (int64_t)NT * g0);
+  const int local = (int)(item - (uint32_t)NT * (uint32_t)g0);
   it.t0 = local / ge * TK;
   const int st =
       it.e ? max(0, align_up_i(__builtin_amdgcn_readfirstlane(pe[it.e - 1]), align)) : 0;
@@ -79,16 +82,21 @@ __device__ __forceinline__ Item decode(int64_t item, int64_t whole, int NT, int 
   return it;
 }
 
-// kW: this wave loads w, else dy.
-template <bool kW>
+// TK: columns of an output tile, 256 or 128.  kW: this wave loads w, else dy.
+template <int TK, bool kW>
 __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
-                                    const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
+                                    bool few_rows, const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
                                     int k, int E, int align, uint16_t* dx, int lane, int wid) {
+  constexpr int kRowBytes = TK * 2;                      // a staged row of w
+  constexpr int kStageRows = kWBytes / kRowBytes;        // 32 or 64
+  constexpr int kStageSteps = kStageRows / kStep;        // steps per stage of w: 1 or 2
+  constexpr int kLoadRows = 1024 / kRowBytes;            // rows of w per load: 2 or 4
+  constexpr int FI = TK / 64;                            // 16-column tiles per wave
   const int NT = (k + TK - 1) / TK;
-  const Rounds rounds((int64_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT, gridDim.x);
-  const int64_t whole = rounds.whole, nitems = rounds.count;
-  const int per_xcd = gridDim.x / kXcds;
-  const int64_t first = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+  const Rounds rounds((uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT, gridDim.x,
+                      few_rows);
+  const uint32_t whole = rounds.whole, nitems = rounds.count;
+  const uint32_t first = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
   const int steps = n / kStep;  // even: n % 128 == 0
   const int wr = wid >> 2, wc = wid & 3;
 
@@ -97,32 +105,38 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   uint32_t fw, fa;
   {
     const int g = lane >> 4;
-    fw = (lds0 + tr_lane_offset(lane) + (wc >> 1) * 256) ^ (uint32_t)((wc & 1) * FI * 32);
+    const int piece = wc * FI;  // 32-byte pieces, eight to 256 bytes
+    fw = (lds0 + tr_lane_offset<kRowBytes>(lane) + (piece >> 3) * 256) ^
+         (uint32_t)((piece & 7) << 5);
     const int row = wr * 128 + (lane & 15);
     fa = lds0 + kABase + (uint32_t)(row * 128 + ((g ^ a_key(row)) << 4));
   }
 
   // Loading side: this wave's stream of stages, running ahead of the
   // computation across items.
-  int64_t d_item = first;
+  const uint32_t a_bytes = few_rows ? kARing / 4 : kARing / 2;  // a stage of dy
+  // Waves 6 and 7 load rows 128..255: none where there are few rows.
+  const bool loads = kW || !few_rows || wid < kLoadWaves + 2;
+  uint32_t d_item = first;
   int d_step = 0, d_live = 0;
   const uint8_t* d_src = nullptr;
-  // Load q covers rows r + q * (2 or 8): the offset of row r's chunk (the
-  // swizzle repeats with every second load) plus a uniform q * d_pitch.
+  // Load q covers rows r + q * (kLoadRows or 8): the offset of row r's chunk
+  // (one of two, by the swizzle) plus a uniform q * d_pitch.
   uint32_t d_off[2];
-  const int64_t d_pitch = kW ? (int64_t)k * 4 : (int64_t)n * 16;
+  const int64_t d_pitch = kW ? (int64_t)k * 2 * kLoadRows : (int64_t)n * 16;
   uint32_t d_slot = 0;
   auto d_open = [&]() __attribute__((always_inline)) {
     d_live = 0;
     if (d_item >= nitems) return;
-    const Item it = decode(d_item, whole, NT, E, align, nrows, gp, pe);
+    const Item it = decode<TK>(d_item, whole, NT, E, align, nrows, gp, pe);
     d_live = it.live;
     if constexpr (kW) {
       d_src = w + ((int64_t)it.e * n * k + it.t0) * 2;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = wid * kWLoads * 2 + (lane >> 5);
-        const int col = ((lane & 31) ^ (tr_key(row + 2 * j) << 1)) * 8;
+        constexpr int kLanes = 64 / kLoadRows;  // per row
+        const int row = wid * kWLoads * kLoadRows + lane / kLanes;
+        const int col = (lane % kLanes ^ (tr_key(row + (TK == 256 ? 2 : 8) * j) << 1)) * 8;
         d_off[j] = (uint32_t)(row * k + min(col, k - 8 - it.t0)) * 2u;
       }
     } else {
@@ -135,7 +149,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
     }
   };
   auto d_load = [&](int q) __attribute__((always_inline)) {
-    const uint8_t* p = d_src + q * d_pitch + d_off[q & 1];
+    const uint8_t* p = d_src + q * d_pitch + d_off[kW && TK == 128 ? q >> 1 : q & 1];
     if constexpr (kW) {
       p = d_live > 0 ? p : zero_chunk();
       dma16_ptr(p, lds0 + d_slot + (wid * kWLoads + q) * 1024);
@@ -148,10 +162,10 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   auto d_advance = [&]() __attribute__((always_inline)) {
     if constexpr (kW) {
       d_slot = d_slot + kWBytes == kWStages * kWBytes ? 0 : d_slot + kWBytes;
-      d_src += (int64_t)kStep * k * 2;
-      d_step += 1;
+      d_src += (int64_t)kStageRows * k * 2;
+      d_step += kStageSteps;
     } else {
-      d_slot = d_slot + kABytes == kAStages * kABytes ? 0 : d_slot + kABytes;
+      d_slot = d_slot + a_bytes == kARing ? 0 : d_slot + a_bytes;
       d_src += 128;
       d_step += 2;
     }
@@ -164,9 +178,10 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
 
   d_open();
 #pragma unroll 1
-  for (int g = 0; g < (kW ? kWStages : kAStages); ++g) {
+  for (int g = 0; g < (kW ? kWStages : few_rows ? 4 : 2); ++g) {
+    if (loads)
 #pragma unroll
-    for (int q = 0; q < (kW ? kWLoads : kALoads); ++q) d_load(q);
+      for (int q = 0; q < (kW ? kWLoads : kALoads); ++q) d_load(q);
     d_advance();
   }
 
@@ -174,14 +189,15 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   v4f acc[FI][FJ];
   bf16x8 a[2][FJ], b[2][FI];
   auto read_w = [&](int h, int i, uint32_t slot) __attribute__((always_inline)) {
-    b[h][i] = frag_tr<kRowBytes>((fw + slot) ^ (uint32_t)(i << 5));
+    const int row = kStageSteps == 2 ? h * kStep : 0;
+    b[h][i] = frag_tr<kRowBytes>(((fw + slot) ^ (uint32_t)(i << 5)) + row * kRowBytes);
   };
   auto read_a = [&](int h, int j, uint32_t slot) __attribute__((always_inline)) {
     a[h][j] = lds_load<bf16x8>(((fa + slot) ^ (uint32_t)(h << 6)) + j * 16 * 128);
   };
 
-  for (int64_t item = first; item < nitems; item += gridDim.x) {
-    const Item it = decode(item, whole, NT, E, align, nrows, gp, pe);
+  for (uint32_t item = first; item < nitems; item += gridDim.x) {
+    const Item it = decode<TK>(item, whole, NT, E, align, nrows, gp, pe);
     const bool busy = wr * 128 < it.live;  // uniform: the wave has live rows
 #pragma unroll
     for (int i = 0; i < FI; ++i)
@@ -189,20 +205,26 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
       for (int j = 0; j < FJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     wait_vmcnt<0>();
     barrier();
-    // Step c (half h of a pair): the next step's stage has landed; the slot of
-    // step c (its fragments are in registers) is loaded anew.
+    // One step (half h of a pair).  Where the next step starts a new stage: it
+    // has landed, and the slot that this step's fragments came from (they are
+    // in registers) is loaded anew.
     auto half = [&](auto is_busy, auto hh) __attribute__((always_inline)) {
       constexpr bool kBusy = decltype(is_busy)::value;
       constexpr int h = decltype(hh)::value;
-      const uint32_t nw = w_slot + kWBytes == kWStages * kWBytes ? 0 : w_slot + kWBytes;
-      const uint32_t na = h == 0 ? a_slot : a_slot + kABytes == kAStages * kABytes ? 0
-                                                                                : a_slot + kABytes;
-      if constexpr (kW) wait_vmcnt<(kWStages - 2) * kWLoads>();
-      else if constexpr (h == 1) wait_vmcnt<0>();
-      wait_lgkm0();
-      barrier();
+      constexpr bool kNewW = kStageSteps == 1 || h == 1, kNewA = h == 1;
+      const uint32_t nw = !kNewW ? w_slot : w_slot + kWBytes == kWStages * kWBytes
+                                                ? 0
+                                                : w_slot + kWBytes;
+      const uint32_t na = !kNewA ? a_slot : a_slot + a_bytes == kARing ? 0 : a_slot + a_bytes;
+      if constexpr (kNewW) {
+        if constexpr (kW) wait_vmcnt<(kWStages - 2) * kWLoads>();
+        else if (kNewA && few_rows) wait_vmcnt<2 * kALoads>();
+        else if (kNewA) wait_vmcnt<0>();
+        wait_lgkm0();
+        barrier();
+      }
       sched_fence();
-      constexpr int kL = kW ? kWLoads : h == 1 ? kALoads : 0;
+      constexpr int kL = kW ? (kNewW ? kWLoads : 0) : kNewA ? kALoads : 0;
 #pragma unroll
       for (int u = 0; u < FI * FJ; ++u) {
         if constexpr (kBusy) {
@@ -210,10 +232,15 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
           acc[i][j] =
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[h][i], a[h][j], acc[i][j], 0, 0, 0);
           sched_fence();
-          if (u % 2 == 0 && u / 2 < FI) read_w(h ^ 1, u / 2, nw);
-          else if (u % 2 == 0 && u / 2 < FI + FJ) read_a(h ^ 1, u / 2 - FI, na);
+          if (TK == 128 && u < FI + FJ) {  // 16 MFMAs: a read beside each
+            if (u < FI) read_w(h ^ 1, u, nw);
+            else read_a(h ^ 1, u - FI, na);
+          } else if (TK == 256 && u % 2 == 0 && u / 2 < FI + FJ) {
+            if (u / 2 < FI) read_w(h ^ 1, u / 2, nw);
+            else read_a(h ^ 1, u / 2 - FI, na);
+          }
         }
-        if (u % 2 == 1 && u / 2 < kL) d_load(u / 2);
+        if (u % 2 == 1 && u / 2 < kL && loads) d_load(u / 2);
         sched_fence();
       }
       w_slot = nw;
@@ -232,7 +259,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
       // The lane holds columns t = 4 (lane / 16) + 0..3 of tile i for row
       // lane % 16 of tile j.  Two lane swaps turn the columns of two tiles
       // into 8 neighbouring ones per lane: 16-byte stores, 64 bytes per row.
-      const int tc = it.t0 + wc * 64, hf = lane >> 5, r1 = (lane >> 4) & 1;
+      const int tc = it.t0 + wc * FI * 16, hf = lane >> 5, r1 = (lane >> 4) & 1;
       if (tc < k) {
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
@@ -255,6 +282,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   wait_vmcnt<0>();  // no load may land after the workgroup's LDS has been given away
 }
 
+template <int TK>
 __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ w,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
@@ -262,11 +290,12 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
   __shared__ int gp[MOE_MAX_EXPERTS + 1];  // prefix of row groups per expert
   __shared__ int pe[MOE_MAX_EXPERTS];      // end of each expert's live rows
+  __shared__ int few;                      // no expert has more than 128 of them
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nrows = min((int64_t)status[0], capacity);
   if (wid == 0) {
-    int sum = 0;
+    int sum = 0, most = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
       int ng = 0;
@@ -274,6 +303,7 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
         const int64_t st = e ? max(0, align_up_i(psum[e - 1], align)) : 0;
         const int64_t en = min((int64_t)psum[e], nrows);
         ng = en > st ? (int)((en - st + TM - 1) / TM) : 0;
+        most = max(most, (int)max((int64_t)0, en - st));
         pe[e] = psum[e];
       }
       const int incl = wave_incl_scan_i(ng);
@@ -281,12 +311,14 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
       sum += __shfl(incl, 63, 64);
     }
     if (lane == 0) gp[E] = sum;
+    few = __any(most > TM / 2) ? 0 : 1;
   }
   __syncthreads();
+  const bool few_rows = TK == 128 && __builtin_amdgcn_readfirstlane(few);
   if (wid < kLoadWaves)
-    run<true>(lds_addr(lds), gp, pe, dy, w, nrows, n, k, E, align, dx, lane, wid);
+    run<TK, true>(lds_addr(lds), gp, pe, few_rows, dy, w, nrows, n, k, E, align, dx, lane, wid);
   else
-    run<false>(lds_addr(lds), gp, pe, dy, w, nrows, n, k, E, align, dx, lane, wid);
+    run<TK, false>(lds_addr(lds), gp, pe, few_rows, dy, w, nrows, n, k, E, align, dx, lane, wid);
 }
 
 }  // namespace
@@ -305,15 +337,20 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
   if (((uintptr_t)dy % 16) || ((uintptr_t)w % 16) || ((uintptr_t)dx % 16))
     return MOE_ERR_ALIGNMENT;
   if (capacity == 0) return MOE_OK;
-  const int64_t max_items = ((capacity + TM - 1) / TM + num_experts) * (int64_t)((k + TK - 1) / TK);
-  if (max_items < kMinTiles)
-    return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx,
-                               reinterpret_cast<hipStream_t>(stream));
+  // Bounds on the tiles: the rows of an expert are only known on the device.
+  const int64_t groups = (capacity + TM - 1) / TM + num_experts;
+  const int64_t wide = groups * ((k + 255) / 256);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (wide < kMinTiles)
+    return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx, st);
+  const bool half_wide = wide < kMinWide && capacity <= (int64_t)TM * num_experts;
+  const int64_t tiles = half_wide ? groups * ((k + 127) / 128) : wide;
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
-  if (grid > max_items) grid = max_items;
+  if (grid > 2 * tiles) grid = 2 * tiles;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL(dgrad_kernel, dim3((unsigned)grid), dim3(kThreads), 0,
-                     reinterpret_cast<hipStream_t>(stream), (const uint8_t*)dy, (const uint8_t*)w,
-                     psum, status, capacity, n, k, num_experts, align, (uint16_t*)dx);
+  auto kern = half_wide ? dgrad_kernel<128> : dgrad_kernel<256>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, (const uint8_t*)dy,
+                     (const uint8_t*)w, psum, status, capacity, n, k, num_experts, align,
+                     (uint16_t*)dx);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

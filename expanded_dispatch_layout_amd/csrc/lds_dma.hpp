@@ -108,7 +108,7 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 __device__ __forceinline__ const uint8_t* zero_chunk() { return (const uint8_t*)kZeros; }
 
 // Fragments of an operand that is staged with its reduction axis along the
-// rows: a stage is 32 rows of 512 bytes (256 bf16 columns), and a fragment
+// rows (a multiple of 256 bytes each).  A fragment
 // (16 columns x 32 rows) is read through ds_read_b64_tr_b16, which gives lane
 // l of a 16-lane group column l of 4 rows x 16 columns.  Group g = lane / 16
 // reads rows 8 g + 0..3 and then 8 g + 4..7, so that each lane holds 8
@@ -118,9 +118,10 @@ __device__ __forceinline__ const uint8_t* zero_chunk() { return (const uint8_t*)
 // at once: no bank conflicts (counted: none).
 __device__ __forceinline__ int tr_key(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
 // This lane's address of piece 0; piece p of the same 256 bytes is at ^ (p << 5).
+template <int kRowBytes>
 __device__ __forceinline__ uint32_t tr_lane_offset(int lane) {
   const int row = 8 * (lane >> 4) + ((lane & 15) >> 2), q = lane & 3;
-  return (uint32_t)(row * 512 + tr_key(row) * 32 + (q >> 1) * 16 + (q & 1) * 8);
+  return (uint32_t)(row * kRowBytes + tr_key(row) * 32 + (q >> 1) * 16 + (q & 1) * 8);
 }
 template <int kRowBytes>
 __device__ __forceinline__ auto frag_tr(uint32_t addr) {

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   const int wj = wid >> 1, wt = wid & 1;
   uint32_t fx, fy;  // x, dy
   {
-    const uint32_t base = lds0 + tr_lane_offset(lane);
+    const uint32_t base = lds0 + tr_lane_offset<kRowBytes>(lane);
     fx = base + kOpBytes + wt * 256;
     fy = (base + (wj >> 1) * 256) ^ (uint32_t)((wj & 1) * FJ * 32);
   }

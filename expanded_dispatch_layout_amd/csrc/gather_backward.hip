@@ -10,7 +10,10 @@
 // fixed order.  The slots of a token are neighbouring waves, so dout[r] comes
 // from HBM once and from the caches for its other slots; there is nothing to
 // join between waves, and a token's slots run side by side however few tokens
-// there are.
+// there are.  4096 tokens of H = 7168 with 8 slots each: 205 us, 4.9 TB/s, the
+// rate of a plain copy.  (Loads and stores that pass the caches by take 191,
+// but then the products that read the gradient rows next take 10 us longer in
+// all.)
 #include "common.hpp"
 
 namespace moe {

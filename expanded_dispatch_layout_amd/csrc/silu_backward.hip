@@ -12,7 +12,10 @@
 // pass, so short rows fill a workgroup several at a time.  A row's data is
 // loaded before its label is known (the row lies below the total, so the
 // loads are in bounds; an alignment pad's values are dropped): one memory
-// round trip per row instead of three.
+// round trip per row instead of three.  Loads and stores pass the caches by
+// (nothing here is read twice): 18432 rows of I = 2048 take 61.8 us, 6.1 TB/s,
+// against 67.2 with plain ones; a backward pass around it takes the same time
+// with both.
 #include "common.hpp"
 
 namespace moe {
@@ -43,9 +46,10 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(
     uint16_t* drow = dgu + m * (2 * (int64_t)inter);
     bool live = false, known = false;
     for (int c = tc * 8; c < inter; c += tpr * 8) {
-      const u32x4 gv = *reinterpret_cast<const u32x4*>(grow + c);
-      const u32x4 uv = *reinterpret_cast<const u32x4*>(grow + inter + c);
-      const u32x4 yv = *reinterpret_cast<const u32x4*>(yrow + c);
+      const u32x4 gv = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(grow + c));
+      const u32x4 uv =
+          __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(grow + inter + c));
+      const u32x4 yv = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(yrow + c));
       if (!known) {
         live = e >= 0 && e < E && m < psum[e];
         known = true;
@@ -62,8 +66,8 @@ __global__ __launch_bounds__(kThreads) void silu_backward_kernel(
         og[i] = (uint32_t)f32_to_bf16_rne(a.dg) | ((uint32_t)f32_to_bf16_rne(b.dg) << 16);
         ou[i] = (uint32_t)f32_to_bf16_rne(a.du) | ((uint32_t)f32_to_bf16_rne(b.du) << 16);
       }
-      *reinterpret_cast<u32x4*>(drow + c) = og;
-      *reinterpret_cast<u32x4*>(drow + inter + c) = ou;
+      __builtin_nontemporal_store(og, reinterpret_cast<u32x4*>(drow + c));
+      __builtin_nontemporal_store(ou, reinterpret_cast<u32x4*>(drow + inter + c));
     }
   }
 }

@@ -91,6 +91,8 @@ PRODUCTS = [
     ([20000, 1], 128, 128, 16, 0),
     ([40, 0, 1, 70] * 16, 384, 320, 16, 1),            # tiles enough for the wide kernels
     ([129, 300, 0, 513, 64, 1, 256, 33] * 2, 256, 1088, 64, 1),
+    ([3000, 700, 0, 129], 128, 5056, 64, 1),           # ... and with a cut last round
+    ([2, 0, 0, 17] * 50, 128, 64, 16, 0),
 ]
 PIDS = [f"{'_'.join(map(str, c[0][:4]))}-n{c[1]}-k{c[2]}-a{c[3]}" for c in PRODUCTS]
 

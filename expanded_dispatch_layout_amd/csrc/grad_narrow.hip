@@ -33,8 +33,10 @@ static_assert(kWaveBytes == T * T * 4, "a partial tile fills its wave's slots");
 // wave reads at once fall on different banks (two rows make 256 bytes).
 __device__ __forceinline__ int row_key(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
 // Column-staged operand (reduction along the columns): 64 rows of 64 bytes,
-// four 16-byte chunks per row, XOR-swizzled by row / 4.
-__device__ __forceinline__ int col_key(int row) { return (row >> 2) & 3; }
+// four 16-byte chunks per row, XOR-swizzled by row / 4 -> 0, 2, 3, 1: no bank
+// conflicts between 16 consecutive lanes, nor between lanes 0-3 and 12-15 of
+// one 16-lane group and 4-11 of the next.
+__device__ __forceinline__ int col_key(int row) { return 0x78 >> (2 * ((row >> 2) & 3)) & 3; }
 
 // Fragment addresses of this lane within an operand: tile i is at ^ (i << 5)
 // (row-staged) or + i * 1024 (column-staged).

@@ -280,14 +280,20 @@ extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors
   if (!step || !lr || (num_tensors > 0 && !tensors)) return MOE_ERR_NULL;
   if (((uintptr_t)step % 8) || ((uintptr_t)lr % 4) || ((uintptr_t)grad_scale % 4))
     return MOE_ERR_ALIGNMENT;
+  // Two updates of one value would race.  A tensor beyond the range of all
+  // earlier ones (the usual order of allocations) needs no look at each.
+  uintptr_t lo = UINTPTR_MAX, hi = 0;
   for (int i = 0; i < num_tensors; ++i) {
     const moe_status s = check_tensor(tensors[i]);
     if (s != MOE_OK) return s;
+    if (tensors[i].numel == 0) continue;
     const uintptr_t a = (uintptr_t)tensors[i].master, an = (uintptr_t)tensors[i].numel * 4;
-    for (int j = 0; j < i; ++j) {  // two updates of one value would race
+    for (int j = 0; j < i && a < hi && lo < a + an; ++j) {
       const uintptr_t c = (uintptr_t)tensors[j].master, cn = (uintptr_t)tensors[j].numel * 4;
-      if (an && cn && a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
+      if (a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
     }
+    lo = a < lo ? a : lo;
+    hi = a + an > hi ? a + an : hi;
   }
   const Hyper h = {beta1, beta2, (float)beta1, (float)(1.0 - beta1), (float)beta2,
                    (float)(1.0 - beta2), (float)eps, (float)weight_decay};

@@ -1,5 +1,26 @@
 // moe_grouped_dgrad_bf16: input gradient of the grouped bf16 GEMM,
 //   dx[m, t] = sum_j dy[m, j] * w[e, j, t] for the live rows m of expert e.
+//
+// Bound by the stream of the weights where experts have few rows (a rank's
+// share of about 128 each), by the matrix cores where they have many.
+//
+//  - One persistent workgroup per CU, tiles of 256 rows x 256 columns, eight
+//    waves (two per SIMD) of 128 rows x 64 columns, v_mfma_f32_16x16x32_bf16
+//    with w as the first operand, so that a lane ends up with neighbouring
+//    columns of a row.
+//  - The sum runs over w's rows, so w is staged as rows and read through
+//    ds_read_b64_tr_b16 (lds_dma.hpp); dy's rows hold the sum's axis and are
+//    read as they are.
+//  - Operands go HBM -> LDS directly: waves 0-3 load w (32 rows a stage, five
+//    stages, four steps ahead), waves 4-7 dy (64 columns of 256 rows, whole
+//    128-byte lines, two stages).  The load counter is per wave, so each
+//    stream keeps its own depth.  Both run ahead across tiles.  Rows that are
+//    not live are loaded from a chunk of zeros and cost no traffic; a wave
+//    whose 128 rows hold none skips its MFMAs.
+//  - What it reaches: 106 us at one rank's share (1024 rows, 8 x 4096 x 7168:
+//    4.7 TB/s), 420 us at 18432 uneven rows of 6144 x 2048 (1.10 PFLOP/s) and
+//    800 at 4096 x 6144 (1.16; with zeros as inputs 649: power, as in
+//    wgrad.hip).
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -22,6 +43,13 @@ constexpr int kLds = kABase + kARing;          // 144 KB
 constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
 constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of steps)
 constexpr int FJ = 8;                          // 16-row tiles per wave: 128 rows
+// Which kernel, by the bound on the number of 256 x 256 tiles that the sizes
+// give (the rows of an expert are only known on the device).  Below kMinTiles
+// the narrow one (512 rows, 8 x 2048 x 1024, 56 tiles: 21.5 us against 23.8 with
+// 128 columns and 30.7 with 256; 64 rows, 8 x 4096 x 2048, 96: 54.5, 42, 59).
+// Below kMinWide, where an average expert has one row group, 128 columns
+// (300 rows, 32 x 1024 x 512, 98 tiles: 16.3 against 18.9; 8 rows, 8 x 4096 x
+// 7168, 336: 84 against 77; but 20000 rows, 4 x 4096 x 256, 84: 98 against 80).
 constexpr int64_t kMinTiles = 80, kMinWide = 256;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row so that the 16
@@ -38,7 +66,8 @@ struct Item {
 
 // The workgroups take the items in rounds.  Where the last round leaves half
 // of them idle, its items are cut into their upper and lower 128 rows, which
-// waves 0-3 compute in about half the time: PLACEHOLDER.  `whole` items come
+// waves 0-3 compute in about half the time (18432 rows, 6144 x 2048: 454 ->
+// 420 us; 16384 rows, 2 x 2048 x 1024: 97 -> 83).  `whole` items come
 // first, then `count - whole` halves.
 // Items fit 32 bits: at most 2^22 + 2^10 row groups and 2^8 column tiles.
 struct Rounds {

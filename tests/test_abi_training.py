@@ -145,6 +145,9 @@ def test_adamw_rejects_bad_arguments():
     two = [dict(master=FAKE + o, grad=FAKE, m=FAKE, v=FAKE, numel=10, grad_fmt=0, state_fmt=0)
            for o in (0, 32)]
     assert _adamw(tensors=two) == M.MOE_ERR_UNSUPPORTED             # masters overlap
+    far = [dict(two[0], master=FAKE + 0x1000 * i) for i in (5, 9, 1, 7, 5)]
+    assert _adamw(tensors=far) == M.MOE_ERR_UNSUPPORTED             # the first again, last
+    assert _adamw(tensors=[dict(t, numel=0) for t in far]) == M.MOE_OK
 
 
 def test_header_matches_the_struct():

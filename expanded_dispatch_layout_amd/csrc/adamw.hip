@@ -20,7 +20,7 @@
 // one after the other, 14.6 against 8.9 us at 1M values with fp32 states and
 // 590 against 565 at 100M.)  354M values with 8-bit states: 1154 us, 4.95 TB/s,
 // as a plain copy.
-#include "common.hpp"
+#include "lds_dma.hpp"
 
 // Each operation rounded by itself: plain operators under this pragma (the
 // header's __fmul_rn and __fadd_rn may still be joined into one fma).
@@ -59,15 +59,21 @@ __device__ __forceinline__ double pow_int(double b, int64_t t) {
 }
 
 struct Step {
-  float c1, c2, lr, gs;
+  float rc1, rr2, lr, gs;  // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
 };
 
+// New m and v (and r = sqrt(v)), each operation rounded by itself.  The step
+// takes them with one reciprocal and two products where the formula has three
+// quotients and another root: a few fp32 steps off the update, which moves
+// the master by far less than its own last rounding does.  (The reciprocal's
+// argument is normal: the root of any positive fp32 value is at least 2^-75.)
 __device__ __forceinline__ void update(const Hyper& h, const Step& st, float grad, float& p,
-                                       float& m, float& v) {
+                                       float& m, float& v, float& r) {
   const float g = grad * st.gs;
   m = m * h.b1 + g * h.one_b1;
   v = v * h.b2 + (g * g) * h.one_b2;
-  const float u = (m / st.c1) / (sqrtf(v / st.c2) + h.eps);
+  r = sqrtf(v);
+  const float u = (m * st.rc1) * __builtin_amdgcn_rcpf(r * st.rr2 + h.eps);
   p = p - (u + p * h.wd) * st.lr;
 }
 
@@ -152,7 +158,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, int64_t i, int n, const 
     u32x4 a;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      a[j] = (uint32_t)f32_to_bf16_rne(x[2 * j]) | ((uint32_t)f32_to_bf16_rne(x[2 * j + 1]) << 16);
+      a[j] = pk_bf16(x[2 * j], x[2 * j + 1]);
     *reinterpret_cast<u32x4*>(p + i) = a;
   } else {
 #pragma unroll
@@ -186,7 +192,7 @@ __device__ __forceinline__ void run_chunk(const moe_adamw_tensor& t, int64_t bas
   // Values past the end are 0 and stay so; their lanes take part in the
   // group's maximum.
   const int n = (int)max((int64_t)0, min((int64_t)kVec, t.numel - i));
-  float g[kVec] = {}, p[kVec] = {}, m[kVec] = {}, v[kVec] = {};
+  float g[kVec] = {}, p[kVec] = {}, m[kVec] = {}, v[kVec] = {}, r[kVec] = {};
   if (n > 0) {
     if (kGradF32) load_f32((const float*)t.grad, i, n, g);
     else load_bf16((const uint16_t*)t.grad, i, n, g);
@@ -203,15 +209,13 @@ __device__ __forceinline__ void run_chunk(const moe_adamw_tensor& t, int64_t bas
       load_f32((const float*)t.v, i, n, v);
     }
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) update(h, st, g[j], p[j], m[j], v[j]);
+    for (int j = 0; j < kVec; ++j) update(h, st, g[j], p[j], m[j], v[j], r[j]);
     store_f32(t.master, i, n, p);
     if (t.param) store_bf16((uint16_t*)t.param, i, n, p);
   }
   if constexpr (kFp8) {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = sqrtf(v[j]);
     float sm, sv;
-    const uint2 cm = encode<false>(m, sm), cv = encode<true>(v, sv);
+    const uint2 cm = encode<false>(m, sm), cv = encode<true>(r, sv);
     if (n > 0) {
       store_codes((uint8_t*)t.m, i, n, cm);
       store_codes((uint8_t*)t.v, i, n, cv);
@@ -235,8 +239,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch b, const Hy
   const moe_adamw_tensor& t = b.t[q];
   const int64_t base = ((int64_t)blockIdx.x - b.first[q]) * kChunk;
   const int64_t n = *step;
-  const Step st = {(float)(1.0 - pow_int(h.beta1, n)), (float)(1.0 - pow_int(h.beta2, n)), *lr,
-                   grad_scale ? *grad_scale : 1.f};
+  const float c1 = (float)(1.0 - pow_int(h.beta1, n)), c2 = (float)(1.0 - pow_int(h.beta2, n));
+  const Step st = {1.f / c1, 1.f / sqrtf(c2), *lr, grad_scale ? *grad_scale : 1.f};
   if (t.state_fmt == MOE_STATE_FP8) {
     if (t.grad_fmt == MOE_GRAD_F32) run_chunk<true, true>(t, base, h, st);
     else run_chunk<false, true>(t, base, h, st);

@@ -584,7 +584,8 @@ typedef struct {
 /*
  * One AdamW step over num_tensors tensors (host array, read before the call
  * returns), with decoupled weight decay.  With t = *step (the number of this
- * step, from 1), in fp32, each operation rounded:
+ * step, from 1), in fp32 (m and v: each operation rounded by itself; the
+ * quotients of the step within a few fp32 steps):
  *   g = grad * *grad_scale                       (grad_scale NULL: g = grad)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)

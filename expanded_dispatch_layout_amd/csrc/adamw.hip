@@ -12,14 +12,15 @@
 // operation rounded in the order above (no contraction), so they are the ones
 // that the same sequence of elementwise fp32 operations gives.
 //
-// HBM-bound: everything is read once and written once.  A workgroup takes 2048
-// values of one tensor; the list of tensors travels in the kernel's arguments
-// (nothing is copied to the device), up to kMaxTensors per launch.  Each lane
-// owns 8 consecutive values, so a group of 128 is 16 lanes and its maximum is
-// four exchanges.  (Measured: four times as many values per workgroup, taken
-// one after the other, 14.6 against 8.9 us at 1M values with fp32 states and
-// 590 against 565 at 100M.)  354M values with 8-bit states: 1154 us, 4.95 TB/s,
-// as a plain copy.
+// HBM-bound: everything is read once and written once, past the caches.  A
+// workgroup takes 1024 or 2048 values of one tensor; the list of tensors
+// travels in the kernel's arguments (nothing is copied to the device), up to
+// kMaxTensors per launch.  Each lane owns 4 consecutive values, so that every
+// access of a wave is one contiguous run (8 per lane, in two pieces for the
+// fp32 arrays: 566 us against 527 at 100M values with fp32 states), and a group
+// of 128 is 32 lanes.  354M values with 8-bit states take 1015 us, 5.6 TB/s;
+// 100M with fp32 states 463 us, 6.0 TB/s (with accesses through the caches
+// 1110 and 527).
 #include "lds_dma.hpp"
 
 // Each operation rounded by itself: plain operators under this pragma (the
@@ -30,11 +31,18 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;                              // values per lane and pass
-constexpr int kChunk = kThreads * kVec;              // values per workgroup
+constexpr int kVec = 4;                              // consecutive values per lane
+constexpr int kPart = kThreads * kVec;
+// Parts per workgroup.  With 8-bit states two, whose loads are asked for
+// together (354M values: 1015 us against 1100 with one), with fp32 ones one
+// (100M: 463 against 492 with two).
+__host__ __device__ constexpr int parts(int state_fmt) { return state_fmt == MOE_STATE_FP8 ? 2 : 1; }
+__host__ __device__ constexpr int chunk(int state_fmt) { return kPart * parts(state_fmt); }
+// Values of a tensor: a launch has fewer than 2^32 threads.
+constexpr int64_t kMaxNumel = 1LL << 33;
 constexpr int kMaxTensors = 32;                      // per launch (kernel arguments: 4 KB)
 constexpr float kFp8Max = 448.f, kCodeMin = 0x1p-9f, kAmaxFloor = 0x1p-100f;
-static_assert(MOE_STATE_GROUP == 128 && kChunk % MOE_STATE_GROUP == 0, "groups fill chunks");
+static_assert(MOE_STATE_GROUP == 128 && kPart % MOE_STATE_GROUP == 0, "groups fill parts");
 
 struct Batch {
   moe_adamw_tensor t[kMaxTensors];
@@ -77,19 +85,19 @@ __device__ __forceinline__ void update(const Hyper& h, const Step& st, float gra
   p = p - (u + p * h.wd) * st.lr;
 }
 
-// Largest magnitude of the 16 lanes that hold a group, not below the floor.
+// Largest magnitude of the 32 lanes that hold a group, not below the floor.
 __device__ __forceinline__ float group_amax(const float (&x)[kVec]) {
   float a = kAmaxFloor;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) a = fmaxf(a, fabsf(x[i]));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor(a, o, kWave));
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor(a, o, kWave));
   return a;
 }
 
 // Codes of x and their group's scale.
 template <bool kPositive>
-__device__ __forceinline__ uint2 encode(const float (&x)[kVec], float& scale) {
+__device__ __forceinline__ uint32_t encode(const float (&x)[kVec], float& scale) {
   const float amax = group_amax(x);
   scale = amax * (1.f / kFp8Max);
   const float inv = (1.f / amax) * kFp8Max;
@@ -99,32 +107,29 @@ __device__ __forceinline__ uint2 encode(const float (&x)[kVec], float& scale) {
     q[i] = x[i] * inv;
     if (kPositive && x[i] > 0.f) q[i] = fmaxf(q[i], kCodeMin);
   }
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
-  return make_uint2((uint32_t)lo, (uint32_t)hi);
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
 }
 
-__device__ __forceinline__ void decode(uint2 c, float scale, float (&x)[kVec]) {
+__device__ __forceinline__ void decode(uint32_t c, float scale, float (&x)[kVec]) {
   typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
-  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
-  const f2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
-  const f2 e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
-  const float y[kVec] = {a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
+  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+  const float y[kVec] = {a[0], a[1], b[0], b[1]};
 #pragma unroll
   for (int i = 0; i < kVec; ++i) x[i] = y[i] * scale;
 }
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 // n (1..kVec) consecutive values at p + i; whole vectors where n == kVec (the
 // base is 16-byte aligned and i a multiple of kVec).
 __device__ __forceinline__ void load_f32(const float* p, int64_t i, int n, float (&x)[kVec]) {
   if (n == kVec) {
-    const float4 a = *reinterpret_cast<const float4*>(p + i);
-    const float4 b = *reinterpret_cast<const float4*>(p + i + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = a[j];
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) x[j] = j < n ? p[i + j] : 0.f;
@@ -132,8 +137,7 @@ __device__ __forceinline__ void load_f32(const float* p, int64_t i, int n, float
 }
 __device__ __forceinline__ void store_f32(float* p, int64_t i, int n, const float (&x)[kVec]) {
   if (n == kVec) {
-    *reinterpret_cast<float4*>(p + i) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + i + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4*>(p + i));
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
@@ -142,9 +146,9 @@ __device__ __forceinline__ void store_f32(float* p, int64_t i, int n, const floa
 }
 __device__ __forceinline__ void load_bf16(const uint16_t* p, int64_t i, int n, float (&x)[kVec]) {
   if (n == kVec) {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(p + i);
+    const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + i));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       x[2 * j] = __uint_as_float(a[j] << 16);
       x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
     }
@@ -155,78 +159,85 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, int64_t i, int n, f
 }
 __device__ __forceinline__ void store_bf16(uint16_t* p, int64_t i, int n, const float (&x)[kVec]) {
   if (n == kVec) {
-    u32x4 a;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      a[j] = pk_bf16(x[2 * j], x[2 * j + 1]);
-    *reinterpret_cast<u32x4*>(p + i) = a;
+    __builtin_nontemporal_store(u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])},
+                                reinterpret_cast<u32x2*>(p + i));
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
       if (j < n) p[i + j] = f32_to_bf16_rne(x[j]);
   }
 }
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t i, int n) {
-  if (n == kVec) return *reinterpret_cast<const uint2*>(p + i);
-  uint32_t w[2] = {0u, 0u};
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int n) {
+  if (n == kVec) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + i));
+  uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < kVec; ++j)
-    if (j < n) w[j / 4] |= (uint32_t)p[i + j] << (8 * (j % 4));
-  return make_uint2(w[0], w[1]);
+    if (j < n) w |= (uint32_t)p[i + j] << (8 * j);
+  return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int n, uint2 c) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int n, uint32_t c) {
   if (n == kVec) {
-    *reinterpret_cast<uint2*>(p + i) = c;
+    __builtin_nontemporal_store(c, reinterpret_cast<uint32_t*>(p + i));
   } else {
-    const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      if (j < n) p[i + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+      if (j < n) p[i + j] = (uint8_t)(c >> (8 * j));
   }
 }
 
 template <bool kGradF32, bool kFp8>
 __device__ __forceinline__ void run_chunk(const moe_adamw_tensor& t, int64_t base,
                                           const Hyper& h, const Step& st) {
-  const int64_t i = base + threadIdx.x * kVec;
+  constexpr int kParts = parts(kFp8 ? MOE_STATE_FP8 : MOE_STATE_F32);
   // Values past the end are 0 and stay so; their lanes take part in the
   // group's maximum.
-  const int n = (int)max((int64_t)0, min((int64_t)kVec, t.numel - i));
-  float g[kVec] = {}, p[kVec] = {}, m[kVec] = {}, v[kVec] = {}, r[kVec] = {};
-  if (n > 0) {
-    if (kGradF32) load_f32((const float*)t.grad, i, n, g);
-    else load_bf16((const uint16_t*)t.grad, i, n, g);
-    load_f32(t.master, i, n, p);
+  float g[kParts][kVec] = {}, p[kParts][kVec] = {}, m[kParts][kVec] = {}, v[kParts][kVec] = {};
+  int n[kParts];
+#pragma unroll
+  for (int u = 0; u < kParts; ++u) {
+    const int64_t i = base + u * kPart + threadIdx.x * kVec;
+    n[u] = (int)max((int64_t)0, min((int64_t)kVec, t.numel - i));
+    if (n[u] <= 0) continue;
+    if (kGradF32) load_f32((const float*)t.grad, i, n[u], g[u]);
+    else load_bf16((const uint16_t*)t.grad, i, n[u], g[u]);
+    load_f32(t.master, i, n[u], p[u]);
     if constexpr (kFp8) {
-      const uint2 cm = load_codes((const uint8_t*)t.m, i, n);
-      const uint2 cv = load_codes((const uint8_t*)t.v, i, n);
-      decode(cm, t.m_scale[i / MOE_STATE_GROUP], m);
-      decode(cv, t.v_scale[i / MOE_STATE_GROUP], v);
+      const uint32_t cm = load_codes((const uint8_t*)t.m, i, n[u]);
+      const uint32_t cv = load_codes((const uint8_t*)t.v, i, n[u]);
+      decode(cm, t.m_scale[i / MOE_STATE_GROUP], m[u]);
+      decode(cv, t.v_scale[i / MOE_STATE_GROUP], v[u]);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = v[j] * v[j];
+      for (int j = 0; j < kVec; ++j) v[u][j] = v[u][j] * v[u][j];
     } else {
-      load_f32((const float*)t.m, i, n, m);
-      load_f32((const float*)t.v, i, n, v);
+      load_f32((const float*)t.m, i, n[u], m[u]);
+      load_f32((const float*)t.v, i, n[u], v[u]);
     }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) update(h, st, g[j], p[j], m[j], v[j], r[j]);
-    store_f32(t.master, i, n, p);
-    if (t.param) store_bf16((uint16_t*)t.param, i, n, p);
   }
-  if constexpr (kFp8) {
-    float sm, sv;
-    const uint2 cm = encode<false>(m, sm), cv = encode<true>(r, sv);
-    if (n > 0) {
-      store_codes((uint8_t*)t.m, i, n, cm);
-      store_codes((uint8_t*)t.v, i, n, cv);
-      if ((threadIdx.x & 15) == 0) {
-        t.m_scale[i / MOE_STATE_GROUP] = sm;
-        t.v_scale[i / MOE_STATE_GROUP] = sv;
-      }
+#pragma unroll
+  for (int u = 0; u < kParts; ++u) {
+    const int64_t i = base + u * kPart + threadIdx.x * kVec;
+    float r[kVec] = {};
+    if (n[u] > 0) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) update(h, st, g[u][j], p[u][j], m[u][j], v[u][j], r[j]);
+      store_f32(t.master, i, n[u], p[u]);
+      if (t.param) store_bf16((uint16_t*)t.param, i, n[u], p[u]);
     }
-  } else if (n > 0) {
-    store_f32((float*)t.m, i, n, m);
-    store_f32((float*)t.v, i, n, v);
+    if constexpr (kFp8) {
+      float sm, sv;
+      const uint32_t cm = encode<false>(m[u], sm), cv = encode<true>(r, sv);
+      if (n[u] > 0) {
+        store_codes((uint8_t*)t.m, i, n[u], cm);
+        store_codes((uint8_t*)t.v, i, n[u], cv);
+        if ((threadIdx.x & 31) == 0) {
+          t.m_scale[i / MOE_STATE_GROUP] = sm;
+          t.v_scale[i / MOE_STATE_GROUP] = sv;
+        }
+      }
+    } else if (n[u] > 0) {
+      store_f32((float*)t.m, i, n[u], m[u]);
+      store_f32((float*)t.v, i, n[u], v[u]);
+    }
   }
 }
 
@@ -237,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch b, const Hy
   int q = 0;
   while (q + 1 < b.count && (int64_t)blockIdx.x >= b.first[q + 1]) ++q;  // uniform
   const moe_adamw_tensor& t = b.t[q];
-  const int64_t base = ((int64_t)blockIdx.x - b.first[q]) * kChunk;
+  const int64_t base = ((int64_t)blockIdx.x - b.first[q]) * chunk(t.state_fmt);
   const int64_t n = *step;
   const float c1 = (float)(1.0 - pow_int(h.beta1, n)), c2 = (float)(1.0 - pow_int(h.beta2, n));
   const Step st = {1.f / c1, 1.f / sqrtf(c2), *lr, grad_scale ? *grad_scale : 1.f};
@@ -252,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch b, const Hy
 
 // One tensor's arguments; MOE_OK also for an empty one.
 moe_status check_tensor(const moe_adamw_tensor& t) {
-  if (t.numel < 0 || t.numel > (1LL << 40)) return MOE_ERR_SHAPE;
+  if (t.numel < 0 || t.numel > kMaxNumel) return MOE_ERR_SHAPE;
   if ((t.grad_fmt != MOE_GRAD_BF16 && t.grad_fmt != MOE_GRAD_F32) ||
       (t.state_fmt != MOE_STATE_F32 && t.state_fmt != MOE_STATE_FP8))
     return MOE_ERR_UNSUPPORTED;
@@ -307,9 +318,10 @@ extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors
     b.count = 0;
     b.first[0] = 0;
     int64_t blocks = 0;
-    constexpr int64_t kMaxBlocks = 1LL << 30;  // one tensor has at most 2^29
+    constexpr int64_t kMaxBlocks = kMaxNumel / kPart;  // one tensor has no more
     for (; i < num_tensors && b.count < kMaxTensors; ++i) {
-      const int64_t n = (tensors[i].numel + kChunk - 1) / kChunk;
+      const int c = chunk(tensors[i].state_fmt);
+      const int64_t n = (tensors[i].numel + c - 1) / c;
       if (n == 0) continue;
       if (b.count > 0 && blocks + n > kMaxBlocks) break;
       b.t[b.count] = tensors[i];

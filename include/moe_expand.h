@@ -601,7 +601,7 @@ typedef struct {
  * moment of 0 would let the step divide by eps alone.  The step itself uses m and v
  * before they are coded.  An infinite value spoils its group.
  * The last group of a tensor may be short.
- * Errors: numel < 0 or > 2^40, num_tensors < 0, hyperparameters
+ * Errors: numel < 0 or > 2^33, num_tensors < 0, hyperparameters
  * out of range (beta in [0, 1), eps >= 0, weight_decay >= 0, all finite):
  * MOE_ERR_SHAPE; unknown formats, or masters that overlap:
  * MOE_ERR_UNSUPPORTED.  Tensors with numel 0 are skipped.

@@ -131,7 +131,7 @@ def test_adamw_rejects_bad_arguments():
     assert _adamw(lr=None) == M.MOE_ERR_NULL
     assert _adamw(step=FAKE + 4) == M.MOE_ERR_ALIGNMENT
     assert _adamw(numel=-1) == M.MOE_ERR_SHAPE
-    assert _adamw(numel=(1 << 40) + 1) == M.MOE_ERR_SHAPE
+    assert _adamw(numel=(1 << 33) + 1) == M.MOE_ERR_SHAPE
     assert _adamw(grad_fmt=2) == M.MOE_ERR_UNSUPPORTED
     assert _adamw(state_fmt=2) == M.MOE_ERR_UNSUPPORTED
     for name in ("master", "grad", "m", "v"):

@@ -56,22 +56,6 @@ __device__ __forceinline__ void store_grad8(void* dw, int64_t at, const float (&
   }
 }
 
-// 4 consecutive gradients of dw in fp32.
-template <bool kF32>
-__device__ __forceinline__ v4f load_grad4(const void* dw, int64_t at) {
-  if constexpr (kF32) return *reinterpret_cast<const v4f*>((const float*)dw + at);
-  const uint2 q = *reinterpret_cast<const uint2*>((const uint16_t*)dw + at);
-  return v4f{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
-             __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)};
-}
-template <bool kF32>
-__device__ __forceinline__ void store_grad4(void* dw, int64_t at, v4f v) {
-  if constexpr (kF32) *reinterpret_cast<v4f*>((float*)dw + at) = v;
-  else
-    *reinterpret_cast<uint2*>((uint16_t*)dw + at) =
-        make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-}
-
 // Launches of grad_narrow.hip.
 constexpr int kNarrowTile = 64;
 moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psum,

@@ -21,9 +21,9 @@
 //  - Fragments are double-buffered in registers: a step's 32 MFMAs run while
 //    the next one's 24 reads are under way, with one barrier per step.
 //  - What it reaches: 765 us at 18432 rows of 4096 x 6144 (1.21 PFLOP/s; the
-//    library's plain product of that layout and size takes 890), 136 us at one
-//    rank's share in bf16 and 394 accumulating in fp32 (1024 rows, 8 x 4096 x
-//    7168; 4.8 TB/s).  The large one is bound by power: with zeros as inputs
+//    library's plain product of that layout and size takes 890), 114 us at one
+//    rank's share in bf16 and 378 accumulating in fp32 (1024 rows, 8 x 4096 x
+//    7168; 4.3 and 5.0 TB/s).  The large one is bound by power: with zeros as inputs
 //    the same instructions take 612 us.
 #include <math.h>
 
@@ -91,11 +91,13 @@ __device__ __forceinline__ Tile decode(uint32_t item, int NJ, int NT, int splits
   return t;
 }
 
-template <bool kF32>
+// kF32: dw is fp32, else bf16.  kAdd: the sums are added to it.  kParts: part z
+// of a split sum goes to dw[z][E][n][k].
+template <bool kF32, bool kAdd, bool kParts>
 __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
-    int k, int E, int align, int accumulate, int splits, void* __restrict__ dw) {
+    int k, int E, int align, int splits, void* __restrict__ dw) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -212,43 +214,85 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
           d_advance();
         }
       }
-    } else if (accumulate) {
+    } else if (kAdd) {
       continue;  // dw[e] stays
     }
     // Epilogue.  The lane holds columns t = 4 (lane / 16) + 0..3 of tile i for
     // row j = lane % 16 of tile j.  Each wave passes 16 rows at a time through
     // its 4 KB of the slot that the last stage has left (16-byte chunks
     // XOR-swizzled by row), so that a store covers 256 bytes of 4 rows instead
-    // of 64 bytes of 16 (one rank's share, 1024 rows of 8 x 4096 x 7168: 136 us
-    // against 160 in bf16, 394 against 432 accumulating in fp32).
+    // of 64 bytes of 16 (one rank's share, 1024 rows of 8 x 4096 x 7168, through
+    // the caches: 137 us against 160 in bf16, 394 against 432 accumulating in
+    // fp32).
     barrier();  // every wave has read that slot
     const uint32_t own =
         lds0 + (c_slot == 0 ? kRing : c_slot) - kStageBytes + (uint32_t)wid * 4096u;
     const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128;
     const int fr = lane & 15, g = lane >> 4;
-    auto store = [&](auto add) __attribute__((always_inline)) {
-      constexpr bool kAdd = decltype(add)::value;
+    // 64 columns (tiles i0..) of 16 rows into LDS as fp32.
+    auto stage = [&](int i0, int j) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        lds_store<v4f>(own + fr * 256 + (((i * 4 + g) ^ fr) << 4), acc[i0 + i][j]);
+    };
+    auto staged = [&](int r, int c) __attribute__((always_inline)) {  // row r, chunk c
+      return lds_load<v4f>(own + r * 256 + ((c ^ r) << 4));
+    };
+    // dw is not read again here: its accesses pass the caches by (one rank's
+    // share: 114 us against 137 in bf16, 378 against 394 accumulating in fp32;
+    // a backward pass and AdamW around them 2-3% less).  The parts of a split
+    // sum are read next by the join and stay in them.
+    if (jc < n) {
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
-        const int64_t row = ((int64_t)t.z * E + t.e) * n + jc + j * 16 + g;  // + 4 q
-        if constexpr (kF32 || kAdd) {  // 64 columns at a time in fp32
+        const int64_t row0 = ((int64_t)t.z * E + t.e) * n + jc + j * 16;
+        if constexpr (kF32) {
 #pragma unroll
           for (int i0 = 0; i0 < FI; i0 += 4) {
             if (tc + i0 * 16 >= k) break;  // k is a multiple of 64
-            const int64_t col = tc + i0 * 16 + fr * 4;
+            float* o = (float*)dw + (row0 + g) * k + tc + i0 * 16 + fr * 4;  // rows 4 q + g
             v4f old[4];
             if constexpr (kAdd) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) old[q] = load_grad4<kF32>(dw, (row + 4 * q) * k + col);
+              for (int q = 0; q < 4; ++q)
+                old[q] = __builtin_nontemporal_load(
+                    reinterpret_cast<const v4f*>(o + 4 * q * (int64_t)k));
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              lds_store<v4f>(own + fr * 256 + (((i * 4 + g) ^ fr) << 4), acc[i0 + i][j]);
+            stage(i0, j);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              v4f v = lds_load<v4f>(own + (4 * q + g) * 256 + ((fr ^ (4 * q + g)) << 4));
+              v4f v = staged(4 * q + g, fr);
               if constexpr (kAdd) v += old[q];
-              store_grad4<kF32>(dw, (row + 4 * q) * k + col, v);
+              v4f* to = reinterpret_cast<v4f*>(o + 4 * q * (int64_t)k);
+              if constexpr (kParts) *to = v;
+              else __builtin_nontemporal_store(v, to);
+            }
+          }
+        } else if constexpr (kAdd) {  // bf16 sums are added in fp32
+#pragma unroll
+          for (int i0 = 0; i0 < FI; i0 += 4) {
+            if (tc + i0 * 16 >= k) break;
+            const int r = lane >> 3, c = (lane & 7) * 2;  // rows 8 q + r
+            uint16_t* o = (uint16_t*)dw + (row0 + r) * k + tc + i0 * 16 + c * 4;
+            u32x4 old[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              old[q] = __builtin_nontemporal_load(
+                  reinterpret_cast<const u32x4*>(o + 8 * q * (int64_t)k));
+            stage(i0, j);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const v4f x = staged(8 * q + r, c), y = staged(8 * q + r, c + 1);
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const u32x4 b = old[q];
+                v[e] = x[e] + __uint_as_float(e & 1 ? b[e / 2] & 0xffff0000u : b[e / 2] << 16);
+                v[4 + e] =
+                    y[e] + __uint_as_float(e & 1 ? b[2 + e / 2] & 0xffff0000u : b[2 + e / 2] << 16);
+              }
+              __builtin_nontemporal_store(pack8(v),
+                                          reinterpret_cast<u32x4*>(o + 8 * q * (int64_t)k));
             }
           }
         } else {  // all 128 columns as bf16
@@ -263,14 +307,12 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
           for (int q = 0; q < 4; ++q) {
             const u32x4 v = lds_load<u32x4>(own + (4 * q + g) * 256 + ((fr ^ (4 * q + g)) << 4));
             if (tc + fr * 8 < k)
-              *reinterpret_cast<u32x4*>((uint16_t*)dw + (row + 4 * q) * k + tc + fr * 8) = v;
+              __builtin_nontemporal_store(
+                  v, reinterpret_cast<u32x4*>((uint16_t*)dw + (row0 + 4 * q + g) * k + tc +
+                                              fr * 8));
           }
         }
       }
-    };
-    if (jc < n) {
-      if (accumulate) store(std::true_type());
-      else store(std::false_type());
     }
   }
   wait_vmcnt<0>();  // no load may land after the workgroup's LDS has been given away
@@ -364,11 +406,14 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
   if (grid > items * splits) grid = items * splits;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   const bool f32 = fmt == MOE_GRAD_F32;
-  // The parts of a split sum are written as fp32 [splits][E][n][k].
-  auto kern = f32 || splits > 1 ? wgrad_kernel<true> : wgrad_kernel<false>;
+  auto kern = splits > 1   ? wgrad_kernel<true, false, true>
+              : f32        ? (accumulate ? wgrad_kernel<true, true, false>
+                                         : wgrad_kernel<true, false, false>)
+              : accumulate ? wgrad_kernel<false, true, false>
+                           : wgrad_kernel<false, false, false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, (const uint8_t*)dy,
                      (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,
-                     splits > 1 ? 0 : accumulate, splits, splits > 1 ? workspace : dw);
+                     splits, splits > 1 ? workspace : dw);
   if (splits > 1) {
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH;
     const int64_t count = (int64_t)num_experts * n * k;

@@ -116,8 +116,8 @@ __device__ __forceinline__ Item decode(uint32_t item, uint32_t whole, int NT, in
 
 // TK: columns of an output tile, 256 or 128.  kW: this wave loads w, else dy.
 template <int TK, bool kW>
-__device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
-                                    bool few_rows, const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
+__device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe, bool few_rows,
+                                    const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
                                     int k, int E, int align, uint16_t* dx, int lane, int wid) {
   constexpr int kRowBytes = TK * 2;                      // a staged row of w
   constexpr int kStageRows = kWBytes / kRowBytes;        // 32 or 64
@@ -154,7 +154,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   const uint8_t* d_src = nullptr;
   // Load q covers rows r + q * (kLoadRows or 8): the offset of row r's chunk
   // (one of two, by the swizzle) plus a uniform q * d_pitch.
-  uint32_t d_off[2];
+  uint32_t d_off[2] = {};
   const int64_t d_pitch = kW ? (int64_t)k * 2 * kLoadRows : (int64_t)n * 16;
   uint32_t d_slot = 0;
   auto d_open = [&]() __attribute__((always_inline)) {

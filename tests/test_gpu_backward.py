@@ -181,6 +181,35 @@ def test_products_past_the_capacity():
     assert torch.count_nonzero(dw[2]) == 0
 
 
+@pytest.mark.parametrize("experts,n,k", [(300, 1024, 1024), (70, 256, 4096), (129, 768, 2560)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_wgrad_few_experts_of_many(accumulate, experts, n, k):
+    """Runs of experts without rows, shorter and longer than the wave that
+    looks at them, at the start, in between and at the end."""
+    print(f"wgrad {experts} experts n {n} k {k} acc {accumulate}", flush=True)
+    g = np.random.default_rng(experts)
+    counts = [0] * experts
+    for e, c in ((1, 3), (2, 40), (4, 1), (experts // 2 + 1, 17), (experts - 3, 70)):
+        counts[e] = c
+    L = dev_layout(counts, 16, 1)
+    dy, x = bf16(g, (L["cap"], n), 0.1), bf16(g, (L["cap"], k))
+    a, b = poisoned(dy, L["lab"]), poisoned(x, L["lab"])
+    dw = torch.full((experts, n, k), 3.0, dtype=BF, device="cuda")
+    M.moe_grouped_wgrad_bf16(a, b, L["psum"], L["status"], 16, dw, workspace(L, n, k),
+                             accumulate=accumulate)
+    base = 3.0 if accumulate else 0.0
+    dw = dw.cpu()
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.all(dw[e] == base), f"expert {e} without rows"
+            continue
+        mine = L["lab"] == e
+        d, v = f64(dy[torch.from_numpy(mine)]), f64(x[torch.from_numpy(mine)])
+        ref, mag = d.T @ v + base, np.abs(d.T) @ np.abs(v) + base
+        check(f64(dw[e]), ref,
+              2.0 ** -8 * np.abs(ref) + (c + 2) * 2.0 ** -23 * mag + TINY, f"dw[{e}]")
+
+
 def test_wgrad_without_rows():
     """Capacity 0: zeros, or unchanged when accumulating."""
     e = torch.empty((0, 128), dtype=BF, device="cuda")

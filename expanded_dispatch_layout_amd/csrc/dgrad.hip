@@ -43,14 +43,26 @@ constexpr int kLds = kABase + kARing;          // 144 KB
 constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
 constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of steps)
 constexpr int FJ = 8;                          // 16-row tiles per wave: 128 rows
-// Which kernel, by the bound on the number of 256 x 256 tiles that the sizes
-// give (the rows of an expert are only known on the device).  Below kMinTiles
-// the narrow one (512 rows, 8 x 2048 x 1024, 56 tiles: 21.5 us against 23.8 with
-// 128 columns and 30.7 with 256; 64 rows, 8 x 4096 x 2048, 96: 54.5, 42, 59).
-// Below kMinWide, where an average expert has one row group, 128 columns
+// Which kernel, by the sizes (the rows of an expert are only known on the
+// device).  Up to two rounds of 64 x 64 tiles, when experts are even, the narrow
+// one; with short sums, whose wide tiles end soon, fewer.  Measured, narrow
+// against the better wide kernel: 64 rows per expert, 8 x 2048 x 1024 (256
+// tiles), 13.0 and 24.0 us; 64 rows, 8 x 2048 x 2048 (512), 23.2 and 24.8; 256
+// rows there (1024), 46 and 34; 512 rows, 2 x 7168 x 2048 (512), 56 and 91; 64
+// rows, 32 x 512 x 512 (512), 13.0 and 12.0; 64 rows, 19 x 640 x 576 (342), 9.5
+// and 12.3.
+constexpr int64_t kMaxNarrow = 512;
+inline bool is_narrow(int64_t capacity, int n, int k, int num_experts) {
+  const int64_t rows = (capacity + num_experts - 1) / num_experts;
+  const int64_t tiles =
+      num_experts * ((rows + kNarrowTile - 1) / kNarrowTile) * (k / kNarrowTile);
+  return tiles <= min(kMaxNarrow, (int64_t)(256 + n / 4));
+}
+// Of the wide ones, by the bound on the number of 256 x 256 tiles: below
+// kMinWide, where an average expert has one row group, 128 columns
 // (300 rows, 32 x 1024 x 512, 98 tiles: 16.3 against 18.9; 8 rows, 8 x 4096 x
 // 7168, 336: 84 against 77; but 20000 rows, 4 x 4096 x 256, 84: 98 against 80).
-constexpr int64_t kMinTiles = 80, kMinWide = 256;
+constexpr int64_t kMinWide = 256;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row so that the 16
 // lanes that a 16-byte LDS read serves at once fall on different banks, whether
@@ -128,7 +140,6 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   const Rounds rounds((uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT, gridDim.x,
                       few_rows);
   const uint32_t whole = rounds.whole, nitems = rounds.count;
-  const uint32_t first = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
   const int steps = n / kStep;  // even: n % 128 == 0
   const int wr = wid >> 2, wc = wid & 3;
 
@@ -149,7 +160,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   const uint32_t a_bytes = few_rows ? kARing / 4 : kARing / 2;  // a stage of dy
   // Waves 6 and 7 load rows 128..255: none where there are few rows.
   const bool loads = kW || !few_rows || wid < kLoadWaves + 2;
-  uint32_t d_item = first;
+  uint32_t d_base = 0;  // the round
   int d_step = 0, d_live = 0;
   const uint8_t* d_src = nullptr;
   // Load q covers rows r + q * (kLoadRows or 8): the offset of row r's chunk
@@ -159,6 +170,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
   uint32_t d_slot = 0;
   auto d_open = [&]() __attribute__((always_inline)) {
     d_live = 0;
+    const uint32_t d_item = round_item(d_base, nitems);
     if (d_item >= nitems) return;
     const Item it = decode<TK>(d_item, whole, NT, E, align, nrows, gp, pe);
     d_live = it.live;
@@ -203,7 +215,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
     }
     if (d_step == steps) {
       d_step = 0;
-      d_item += gridDim.x;
+      d_base += gridDim.x;
       d_open();
     }
   };
@@ -228,7 +240,9 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
     a[h][j] = lds_load<bf16x8>(((fa + slot) ^ (uint32_t)(h << 6)) + j * 16 * 128);
   };
 
-  for (uint32_t item = first; item < nitems; item += gridDim.x) {
+  for (uint32_t base = 0;; base += gridDim.x) {
+    const uint32_t item = round_item(base, nitems);
+    if (item >= nitems) break;
     const Item it = decode<TK>(item, whole, NT, E, align, nrows, gp, pe);
     const bool busy = wr * 128 < it.live;  // uniform: the wave has live rows
 #pragma unroll
@@ -373,7 +387,7 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
   const int64_t groups = (capacity + TM - 1) / TM + num_experts;
   const int64_t wide = groups * ((k + 255) / 256);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (wide < kMinTiles)
+  if (is_narrow(capacity, n, k, num_experts))
     return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx, st);
   const bool half_wide = wide < kMinWide && capacity <= (int64_t)TM * num_experts;
   const int64_t tiles = half_wide ? groups * ((k + 127) / 128) : wide;

@@ -21,6 +21,18 @@ inline moe_status check_backward_sizes(int64_t capacity, int n, int k, int num_e
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// This workgroup's item of the round that starts at item `base` (nitems: none).
+// Neighbouring items go to the workgroups of one XCD, whose L2 they share, and
+// every XCD gets as many: the grid is a bound, and rounds that are not full
+// would otherwise leave whole XCDs idle (64 rows per expert, 8 x 2048 x 1024:
+// 22.4 -> 13.0 us; 1024 rows per expert, in a round and a fifth: 56 -> 51).
+__device__ __forceinline__ uint32_t round_item(uint32_t base, uint32_t nitems) {
+  const uint32_t left = nitems > base ? nitems - base : 0;
+  const uint32_t per = (min(left, gridDim.x) + kXcds - 1) / kXcds;
+  const uint32_t slot = blockIdx.x / kXcds;
+  return slot < per ? min(base + blockIdx.x % kXcds * per + slot, nitems) : nitems;
+}
+
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]),
                pk_bf16(v[6], v[7])};

@@ -33,7 +33,9 @@ static_assert(kWaveBytes == T * T * 4, "a partial tile fills its wave's slots");
 // Row-staged operand (reduction along the rows): 32 rows of 128 bytes.  Four
 // 32-byte pieces per row, XOR-swizzled by row so that the 8 rows that half a
 // wave reads at once fall on different banks (two rows make 256 bytes).
-__device__ __forceinline__ int row_key(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
+__device__ __forceinline__ int row_key(int row) {
+  return ((row >> 1) & 1) | (((row >> 3) & 1) << 1);
+}
 // Column-staged operand (reduction along the columns): 64 rows of 64 bytes,
 // four 16-byte chunks per row, XOR-swizzled by row / 4 -> 0, 2, 3, 1: no bank
 // conflicts between 16 consecutive lanes, nor between lanes 0-3 and 12-15 of
@@ -166,43 +168,40 @@ __global__ __launch_bounds__(kThreads) void dgrad_narrow_kernel(
   }
   __syncthreads();
   const int NT = k / T;
-  const int64_t nitems = (int64_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT;
-  const int per_xcd = gridDim.x / kXcds;
-  for (int64_t item = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-       item < nitems; item += gridDim.x) {
-    const int q = (int)(item / NT);
-    int lo = 0, hi = E - 1;  // last e with gp[e] <= q
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (gp[mid] <= q) lo = mid;
-      else hi = mid - 1;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
-    const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
-    const int local = (int)(item - (int64_t)NT * g0);
-    const int t0 = local / ge * T;
-    int64_t st, en;
-    expert_rows(psum, nrows, align, e, st, en);
-    const int64_t m0 = st + (int64_t)(local % ge) * T;
-    const int live = (int)min((int64_t)T, en - m0);
-    const uint8_t* a = dy + m0 * n * 2;
-    const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
-    v4f acc[4][4] = {};
-    wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
-                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
-                      load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
-                      load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
-                                dst + kOpBytes, lane);
-                    },
-                    acc);
-    float v[8];
-    join_waves(lds0, wid, lane, acc, v);
-    const int row = threadIdx.x >> 3;
-    if (row < live)
-      *reinterpret_cast<u32x4*>(dx + (m0 + row) * k + t0 + (threadIdx.x & 7) * 8) = pack8(v);
-    __syncthreads();  // the partial tiles have been read
+  const uint32_t nitems = (uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * (uint32_t)NT;
+  const uint32_t item = round_item(0, nitems);  // the grid has room for all
+  if (item >= nitems) return;
+  const int q = (int)(item / (uint32_t)NT);
+  int lo = 0, hi = E - 1;  // last e with gp[e] <= q
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gp[mid] <= q) lo = mid;
+    else hi = mid - 1;
   }
+  const int e = __builtin_amdgcn_readfirstlane(lo);
+  const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
+  const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
+  const int local = (int)(item - (uint32_t)NT * (uint32_t)g0);
+  const int t0 = local / ge * T;
+  int64_t st, en;
+  expert_rows(psum, nrows, align, e, st, en);
+  const int64_t m0 = st + (int64_t)(local % ge) * T;
+  const int live = (int)min((int64_t)T, en - m0);
+  const uint8_t* a = dy + m0 * n * 2;
+  const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
+  v4f acc[4][4] = {};
+  wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
+                  [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                    load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
+                    load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
+                              dst + kOpBytes, lane);
+                  },
+                  acc);
+  float v[8];
+  join_waves(lds0, wid, lane, acc, v);
+  const int row = threadIdx.x >> 3;
+  if (row < live)
+    *reinterpret_cast<u32x4*>(dx + (m0 + row) * k + t0 + (threadIdx.x & 7) * 8) = pack8(v);
 }
 
 template <bool kF32>
@@ -216,32 +215,28 @@ __global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
   const uint32_t lds0 = lds_addr(lds);
   const int64_t nrows = min((int64_t)status[0], capacity);
   const int NJ = n / T, NT = k / T;
-  const int64_t nitems = (int64_t)E * NJ * NT;
-  for (int64_t item = blockIdx.x; item < nitems; item += gridDim.x) {
-    const int t0 = (int)(item % NT) * T, j0 = (int)(item / NT % NJ) * T;
-    const int e = (int)(item / ((int64_t)NT * NJ));
-    int64_t st, en;
-    expert_rows(psum, nrows, align, e, st, en);
-    const int live = en > st ? (int)(en - st) : 0;
-    if (live == 0 && accumulate) continue;  // dw[e] stays (uniform)
-    const uint8_t* a = dy + (st * n + j0) * 2;
-    const uint8_t* b = x + (st * k + t0) * 2;
-    v4f acc[4][4] = {};
-    wave_sum<true>(wid, kWaves, (live + kStep - 1) / kStep, lds0 + wid * kWaveBytes, lane,
-                   [&](int s, uint32_t dst) __attribute__((always_inline)) {
-                     const int64_t r = (int64_t)s * kStep;
-                     const int nr = (int)min((int64_t)kStep, live - r);
-                     load_rows(a + r * n * 2, (int64_t)n * 2, nr, dst, lane);
-                     load_rows(b + r * k * 2, (int64_t)k * 2, nr, dst + kOpBytes, lane);
-                   },
-                   acc);
-    float v[8];
-    join_waves(lds0, wid, lane, acc, v);
-    const int64_t at =
-        ((int64_t)e * n + j0 + (threadIdx.x >> 3)) * k + t0 + (threadIdx.x & 7) * 8;
-    store_grad8<kF32>(dw, at, v, accumulate);
-    __syncthreads();  // the partial tiles have been read
-  }
+  const int t0 = blockIdx.x % NT * T, j0 = blockIdx.x / NT % NJ * T;
+  const int e = blockIdx.x / (NT * NJ);
+  int64_t st, en;
+  expert_rows(psum, nrows, align, e, st, en);
+  const int live = en > st ? (int)(en - st) : 0;
+  if (live == 0 && accumulate) return;  // dw[e] stays (uniform)
+  const uint8_t* a = dy + (st * n + j0) * 2;
+  const uint8_t* b = x + (st * k + t0) * 2;
+  v4f acc[4][4] = {};
+  wave_sum<true>(wid, kWaves, (live + kStep - 1) / kStep, lds0 + wid * kWaveBytes, lane,
+                 [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                   const int64_t r = (int64_t)s * kStep;
+                   const int nr = (int)min((int64_t)kStep, live - r);
+                   load_rows(a + r * n * 2, (int64_t)n * 2, nr, dst, lane);
+                   load_rows(b + r * k * 2, (int64_t)k * 2, nr, dst + kOpBytes, lane);
+                 },
+                 acc);
+  float v[8];
+  join_waves(lds0, wid, lane, acc, v);
+  const int64_t at =
+      ((int64_t)e * n + j0 + (threadIdx.x >> 3)) * k + t0 + (threadIdx.x & 7) * 8;
+  store_grad8<kF32>(dw, at, v, accumulate);
 }
 
 }  // namespace
@@ -250,7 +245,6 @@ moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psu
                                const int32_t* status, int64_t capacity, int n, int k,
                                int num_experts, int align, void* dx, hipStream_t s) {
   int64_t grid = ((capacity + T - 1) / T + num_experts) * (int64_t)(k / T);
-  if (grid > 2048) grid = 2048;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   hipLaunchKernelGGL(dgrad_narrow_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
                      (const uint8_t*)dy, (const uint8_t*)w, psum, status, capacity, n, k,
@@ -263,8 +257,7 @@ moe_status launch_wgrad_narrow(const void* dy, const void* x, const int32_t* psu
                                int num_experts, int align, moe_grad_fmt fmt, int accumulate,
                                void* dw, hipStream_t s) {
   const bool f32 = fmt == MOE_GRAD_F32;
-  int64_t grid = (int64_t)num_experts * (n / T) * (k / T);
-  if (grid > 4096) grid = 4096;
+  const int64_t grid = (int64_t)num_experts * (n / T) * (k / T);
   auto kern = f32 ? wgrad_narrow_kernel<true> : wgrad_narrow_kernel<false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, (const uint8_t*)dy,
                      (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,

@@ -45,11 +45,9 @@ constexpr int kRing = kStages * kStageBytes;   // 160 KB, all of the CU's
 constexpr int kLoads = 4;                      // DMA instructions per wave and stage
 constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
 
-// Fewer tiles than this, and short sums (not split): the narrow kernel.  Wide
-// against narrow: 13.0 and 12.7 us at 72 tiles (140 rows, 6 x 896 x 640, before
-// the stores were widened), 25 and 8 at 3 (3000 rows, 3 x 128 x 64), 15 and 24
-// at 128 (64 rows, 2 x 2048 x 2048).
+// Fewer tiles than this and short sums: the narrow kernel.
 constexpr int64_t kMinTiles = 64;
+constexpr int64_t kNarrowRows = 4096;  // rows, times the rounds of narrow tiles
 constexpr int64_t kFullTiles = 256;  // one per CU
 
 struct Tile {
@@ -107,25 +105,24 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   const int NJ = (n + TN - 1) / TN, NT = (k + TK - 1) / TK;
   // At most 2^24 tiles (1024 experts, 128 x 128), and a split sum has few.
   const uint32_t nitems = (uint32_t)E * NJ * NT * splits;
-  const uint32_t first = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
 
-  // The first of this workgroup's items behind `item` whose expert has rows,
-  // expert e having none: 64 experts are looked at at once, since each look is
+  // The first round behind that at `base` that may have an item whose expert
+  // has rows, expert e having none: 64 experts are looked at at once, since each look is
   // a round trip to memory (8 of 256 experts with a row, 4096 x 7168, adding to
   // bf16: 213 us, against 381 tile by tile and 202 for those 8 experts alone).
   // Only where dw is added to: elsewhere every tile of such an expert is
   // written, at the memory's rate (256 experts: 2.7 ms for 15 GB).
-  auto skip_idle = [&](uint32_t item, int e) __attribute__((always_inline)) {
-    for (int base = e + 1; base < E; base += 64) {
-      const int q = base + lane;
+  auto skip_idle = [&](uint32_t base, int e) __attribute__((always_inline)) -> uint32_t {
+    for (int q0 = e + 1; q0 < E; q0 += 64) {
+      const int q = q0 + lane;
       bool live = false;
       if (q < E)
         live = min((int64_t)psum[q], nrows) > (int64_t)max(0, align_up_i(psum[q - 1], align));
       const uint64_t mask = __ballot(live);
       if (mask) {
         const uint32_t at =
-            (uint32_t)(base + __builtin_ctzll(mask)) * (uint32_t)(NJ * NT) * (uint32_t)splits;
-        return item + (at - item + gridDim.x - 1) / gridDim.x * gridDim.x;
+            (uint32_t)(q0 + __builtin_ctzll(mask)) * (uint32_t)(NJ * NT) * (uint32_t)splits;
+        return max(base + gridDim.x, at / gridDim.x * gridDim.x);
       }
     }
     return nitems;
@@ -142,14 +139,16 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   }
 
   // DMA side: the next stage to load.
-  uint32_t d_item = first;
+  uint32_t d_base = 0;  // the round
   int d_left = 0;    // rows left of its tile (<= 0: a stage of zeros)
   int d_stages = 0;  // stages left of its tile
   const uint8_t *d_dy = nullptr, *d_x = nullptr;
   uint32_t d_offa[2] = {}, d_offb[2] = {};  // x, dy: offsets of this lane's chunks
   uint32_t d_slot = 0;            // LDS offset of the next slot
   auto d_open = [&]() __attribute__((always_inline)) {  // next tile that has rows
-    while (d_item < nitems) {
+    while (true) {
+      const uint32_t d_item = round_item(d_base, nitems);
+      if (d_item >= nitems) break;
       const Tile t = decode(d_item, NJ, NT, splits, psum, nrows, align);
       if (t.live > 0) {
         d_left = t.live;
@@ -165,7 +164,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
         }
         return;
       }
-      d_item = kAdd && t.idle ? skip_idle(d_item, t.e) : d_item + gridDim.x;
+      d_base = kAdd && t.idle ? skip_idle(d_base, t.e) : d_base + gridDim.x;
     }
   };
   // Load q (0..3) of the next stage: dy rows first, then x.  Rows past the
@@ -183,8 +182,8 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     d_left -= kStep;
     d_dy += (int64_t)kStep * n * 2;
     d_x += (int64_t)kStep * k * 2;
-    if (--d_stages <= 0 && d_item < nitems) {
-      d_item += gridDim.x;
+    if (--d_stages <= 0 && d_base < nitems) {
+      d_base += gridDim.x;
       d_open();
     }
   };
@@ -199,10 +198,12 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   v4f acc[FI][FJ];
   bf16x8 a[2][FI], b[2][FJ];
 
-  for (uint32_t item = first, next; item < nitems; item = next) {
+  for (uint32_t base = 0, next;; base = next) {
+    const uint32_t item = round_item(base, nitems);
+    if (item >= nitems) break;
     const Tile t = decode(item, NJ, NT, splits, psum, nrows, align);
     const int steps = stages_of(t.live);
-    next = kAdd && t.idle ? skip_idle(item, t.e) : item + gridDim.x;
+    next = kAdd && t.idle ? skip_idle(base, t.e) : base + gridDim.x;
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -375,6 +376,24 @@ int64_t wide_tiles(int n, int k, int num_experts) {
   return (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
 }
 
+// The narrow kernel, where the wide tiles leave CUs idle and an average expert's
+// sum is short.  One of its rounds over the CUs takes about 2.5 us and 1 us per
+// 200 rows; the wide kernel 8 us and 1 us per 64 rows, or, split, at least 16.
+// Measured, narrow against the wide kernel (split or not, whichever
+// wgrad_splits takes), rows per expert: 1024 x 256, one expert, 1024 rows 6.5
+// and 16.2 us, 4096 rows 19.3 and 19.8, 8192 rows 33.4 and 23.6; 1024 x 1024, one
+// expert, 2048 rows 13.2 and 23.8, 8192 rows 37.6 and 37.2; 512 x 512, eight (two
+// rounds), 1024 rows 18.7 and 24.7, 2048 rows 28.9 and 29.1, 4096 rows 51 and 38;
+// 1024 x 1024, three (three rounds), 1024 rows 22 and 26.4, 4096 rows 54.7 and 44.8.
+// With 64 wide tiles (four rounds; 2048 x 512, four experts) 64 rows take 13.7 and
+// 9.2, 1024 rows 32.4 and 26.9.
+bool is_narrow(int64_t capacity, int n, int k, int num_experts) {
+  const int64_t rounds =
+      ((int64_t)num_experts * (n / kNarrowTile) * (k / kNarrowTile) + kFullTiles - 1) / kFullTiles;
+  return wide_tiles(n, k, num_experts) < kMinTiles &&
+         rounds * (capacity / num_experts) <= kNarrowRows;
+}
+
 // Parts that each expert's sum is cut into where the tiles leave CUs idle.  A
 // stage of a tile takes about 0.5 us, so the sum of an average expert's R rows
 // takes R / 64 us / S in S parts; writing and joining them moves 8 S E n k
@@ -384,6 +403,7 @@ int64_t wide_tiles(int n, int k, int num_experts) {
 // 16384 rows of two, 2048 x 1024, 170 / 79 / 79; 20000 rows of four, 2048 x 256,
 // 109 / 43 / 46.
 int wgrad_splits(int64_t capacity, int n, int k, int num_experts) {
+  if (is_narrow(capacity, n, k, num_experts)) return 1;
   const int64_t tiles = wide_tiles(n, k, num_experts), rows = capacity / num_experts;
   if (tiles * 2 > kFullTiles) return 1;
   const double best =
@@ -423,7 +443,7 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
   }
   const int64_t items = wide_tiles(n, k, num_experts);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (splits == 1 && items < kMinTiles)
+  if (is_narrow(capacity, n, k, num_experts))
     return launch_wgrad_narrow(dy, x, psum, status, capacity, n, k, num_experts, align, fmt,
                                accumulate, dw, st);
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD

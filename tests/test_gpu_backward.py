@@ -210,6 +210,41 @@ def test_wgrad_few_experts_of_many(accumulate, experts, n, k):
               2.0 ** -8 * np.abs(ref) + (c + 2) * 2.0 ** -23 * mag + TINY, f"dw[{e}]")
 
 
+LONG_SUMS = [
+    ([9000, 0, 4500, 8200], 256, 320, 16),   # each expert's sum in parts of uneven length
+    ([12001, 11000], 384, 576, 64),
+    ([70, 0, 16000, 1, 9000], 128, 64, 128),
+]
+
+
+@pytest.mark.parametrize("f32,accumulate", [(False, False), (True, False), (True, True),
+                                            (False, True)])
+@pytest.mark.parametrize("counts,n,k,align", LONG_SUMS)
+def test_wgrad_long_sums(counts, n, k, align, f32, accumulate):
+    cap = sum(-(-c // align) * align for c in counts) + align
+    assert M.moe_grouped_wgrad_workspace_bytes(cap, n, k, len(counts)) > 0
+    test_wgrad(counts, n, k, align, 1, f32, accumulate)
+
+
+# Numbers of 64 x 64, 256 x 128 and 256 x 256 tiles just below and above whole
+# rounds of the CUs, and far fewer than the sizes allow.
+ROUNDS = [
+    ([65] * 8, 2048, 1024, 16),
+    ([64] * 8, 1024, 2048, 16),
+    ([1, 0, 0, 0, 0, 0, 0, 900], 1024, 1024, 16),
+    ([256] * 7 + [257], 256, 2176, 16),
+    ([300] * 9, 384, 4096, 16),
+    ([2000, 0, 300, 2300], 256, 4160, 64),
+]
+
+
+@pytest.mark.parametrize("counts,n,k,align", ROUNDS)
+def test_rounds_of_tiles(counts, n, k, align):
+    test_dgrad(counts, n, k, align, 1)
+    test_wgrad(counts, n, k, align, 1, False, False)
+    test_wgrad(counts, n, k, align, 1, True, True)
+
+
 def test_wgrad_without_rows():
     """Capacity 0: zeros, or unchanged when accumulating."""
     e = torch.empty((0, 128), dtype=BF, device="cuda")

@@ -36,7 +36,9 @@ constexpr int kPart = kThreads * kVec;
 // Parts per workgroup.  With 8-bit states two, whose loads are asked for
 // together (354M values: 1015 us against 1100 with one), with fp32 ones one
 // (100M: 463 against 492 with two).
-__host__ __device__ constexpr int parts(int state_fmt) { return state_fmt == MOE_STATE_FP8 ? 2 : 1; }
+__host__ __device__ constexpr int parts(int state_fmt) {
+  return state_fmt == MOE_STATE_FP8 ? 2 : 1;
+}
 __host__ __device__ constexpr int chunk(int state_fmt) { return kPart * parts(state_fmt); }
 // Values of a tensor: a launch has fewer than 2^32 threads.
 constexpr int64_t kMaxNumel = 1LL << 33;

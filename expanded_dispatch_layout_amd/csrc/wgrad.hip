@@ -107,11 +107,11 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   const uint32_t nitems = (uint32_t)E * NJ * NT * splits;
 
   // The first round behind that at `base` that may have an item whose expert
-  // has rows, expert e having none: 64 experts are looked at at once, since each look is
-  // a round trip to memory (8 of 256 experts with a row, 4096 x 7168, adding to
-  // bf16: 213 us, against 381 tile by tile and 202 for those 8 experts alone).
-  // Only where dw is added to: elsewhere every tile of such an expert is
-  // written, at the memory's rate (256 experts: 2.7 ms for 15 GB).
+  // has rows, expert e having none: 64 experts are looked at at once, since each
+  // look is a round trip to memory (8 of 256 experts with a row, 4096 x 7168,
+  // adding to bf16: 213 us, against 381 tile by tile and 202 for those 8 experts
+  // alone).  Only where dw is added to: elsewhere every tile of such an expert
+  // is written, at the memory's rate (256 experts: 2.7 ms for 15 GB).
   auto skip_idle = [&](uint32_t base, int e) __attribute__((always_inline)) -> uint32_t {
     for (int q0 = e + 1; q0 < E; q0 += 64) {
       const int q = q0 + lane;

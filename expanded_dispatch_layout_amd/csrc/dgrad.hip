@@ -7,16 +7,17 @@
 //  - One persistent workgroup per CU, tiles of 256 rows x 256 columns, eight
 //    waves (two per SIMD) of 128 rows x 64 columns, v_mfma_f32_16x16x32_bf16
 //    with w as the first operand, so that a lane ends up with neighbouring
-//    columns of a row.
+//    columns of a row.  128 x 128 tiles (waves of 64 x 32) where the larger
+//    ones leave CUs idle, 64 x 64 (grad_narrow.hip) where those do.
 //  - The sum runs over w's rows, so w is staged as rows and read through
 //    ds_read_b64_tr_b16 (lds_dma.hpp); dy's rows hold the sum's axis and are
 //    read as they are.
 //  - Operands go HBM -> LDS directly: waves 0-3 load w (32 rows a stage, five
 //    stages, four steps ahead), waves 4-7 dy (64 columns of 256 rows, whole
 //    128-byte lines, two stages).  The load counter is per wave, so each
-//    stream keeps its own depth.  Both run ahead across tiles.  Rows that are
-//    not live are loaded from a chunk of zeros and cost no traffic; a wave
-//    whose 128 rows hold none skips its MFMAs.
+//    stream keeps its own depth (128 x 128: four stages of dy).  Both run ahead
+//    across tiles.  Rows that are not live are loaded from a chunk of zeros
+//    and cost no traffic; a wave whose rows hold none skips its MFMAs.
 //  - What it reaches: 106 us at one rank's share (1024 rows, 8 x 4096 x 7168:
 //    4.7 TB/s), 420 us at 18432 uneven rows of 6144 x 2048 (1.10 PFLOP/s) and
 //    800 at 4096 x 6144 (1.16; with zeros as inputs 649: power, as in
@@ -29,40 +30,40 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;                  // 8 waves, two per SIMD
-constexpr int TM = 256;                        // rows of an output tile
 constexpr int kStep = 32;                      // reduction per step
 constexpr int kWBytes = 16384;                 // a stage of w: 32 x 256 or 64 x 128 values
 constexpr int kWStages = 5;
-// dy: 64 values of each row (two steps) per stage, two stages of 256 rows or,
-// in the 128-column tiles where no expert has more than 128, four of 128: few
-// rows leave little to compute while the loads are under way (64 rows, 8 x
-// 4096 x 2048: 42 against 57 us).
-constexpr int kARing = 2 * TM * 128;           // 64 KB
+constexpr int kARing = 65536;                  // dy: 64 values (two steps) of a tile's rows a stage
 constexpr int kABase = kWStages * kWBytes;
 constexpr int kLds = kABase + kARing;          // 144 KB
 constexpr int kLoadWaves = 4;                  // waves 0-3 load w, 4-7 dy
-constexpr int kWLoads = 4, kALoads = 8;        // per loading wave and stage (dy: pair of steps)
-constexpr int FJ = 8;                          // 16-row tiles per wave: 128 rows
-// Which kernel, by the sizes (the rows of an expert are only known on the
-// device).  Up to two rounds of 64 x 64 tiles, when experts are even, the narrow
-// one; with short sums, whose wide tiles end soon, fewer.  Measured, narrow
-// against the better wide kernel: 64 rows per expert, 8 x 2048 x 1024 (256
-// tiles), 13.0 and 24.0 us; 64 rows, 8 x 2048 x 2048 (512), 23.2 and 24.8; 256
-// rows there (1024), 46 and 34; 512 rows, 2 x 7168 x 2048 (512), 56 and 91; 64
-// rows, 32 x 512 x 512 (512), 13.0 and 12.0; 64 rows, 19 x 640 x 576 (342), 9.5
-// and 12.3.
-constexpr int64_t kMaxNarrow = 512;
-inline bool is_narrow(int64_t capacity, int n, int k, int num_experts) {
-  const int64_t rows = (capacity + num_experts - 1) / num_experts;
-  const int64_t tiles =
-      num_experts * ((rows + kNarrowTile - 1) / kNarrowTile) * (k / kNarrowTile);
-  return tiles <= min(kMaxNarrow, (int64_t)(256 + n / 4));
+constexpr int kWLoads = 4;                     // per loading wave and stage
+// Few rows leave little to compute while the loads are under way: the smaller
+// tiles have four stages of dy instead of two.
+template <int TK>
+struct Shape {
+  static constexpr int kRows = TK;
+  static constexpr int kABytes = kRows * 128;         // a stage of dy
+  static constexpr int kAStages = kARing / kABytes;   // 2 or 4
+  static constexpr int kALoads = kRows / 32;          // per loading wave and stage
+  static constexpr int FI = TK / 64, FJ = kRows / 32;  // 16-wide tiles per wave: columns, rows
+};
+
+// Square tiles of t rows and columns to expect.  The rows of an expert are only
+// known on the device: as many live ones as fit the capacity with the worst
+// alignment, evenly spread, half a tile lost by each expert.
+inline int64_t expected_tiles(int64_t capacity, int k, int num_experts, int align, int t) {
+  const int64_t experts = min((int64_t)num_experts, capacity / align);  // with rows
+  const int64_t live = capacity - experts * (align - 1);
+  return max(experts, live / t + experts / 2) * ((k + t - 1) / t);
 }
-// Of the wide ones, by the bound on the number of 256 x 256 tiles: below
-// kMinWide, where an average expert has one row group, 128 columns
-// (300 rows, 32 x 1024 x 512, 98 tiles: 16.3 against 18.9; 8 rows, 8 x 4096 x
-// 7168, 336: 84 against 77; but 20000 rows, 4 x 4096 x 256, 84: 98 against 80).
-constexpr int64_t kMinWide = 256;
+// Which kernel: the smallest tiles that the CUs hold at once, since each step of
+// a tile takes its loads' latency or longer.  Measured with 64 / 128 / 256, rows
+// per expert: 64 rows, 8 x 2048 x 1024, 13 / 19 / 32 us; 256 rows there, 27 / 21 /
+// 32; 512 rows, 2 x 7168 x 2048, 74 / 53 / 94; 8 rows, 8 x 4096 x 2048, 26 / 28 /
+// 59; more than one round of 128 x 128 tiles: 512 rows, 8 x 2048 x 1024, 43 / 36 /
+// 33; 128 rows, 8 x 4096 x 7168, 179 / 128 / 104.
+constexpr int64_t kFull = 256;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row so that the 16
 // lanes that a 16-byte LDS read serves at once fall on different banks, whether
@@ -77,16 +78,16 @@ struct Item {
 };
 
 // The workgroups take the items in rounds.  Where the last round leaves half
-// of them idle, its items are cut into their upper and lower 128 rows, which
+// of them idle, its items (256 x 256 ones) are cut into their upper and lower 128 rows, which
 // waves 0-3 compute in about half the time (18432 rows, 6144 x 2048: 454 ->
 // 420 us; 16384 rows, 2 x 2048 x 1024: 97 -> 83).  `whole` items come
 // first, then `count - whole` halves.
 // Items fit 32 bits: at most 2^22 + 2^10 row groups and 2^8 column tiles.
 struct Rounds {
   uint32_t whole, count;
-  __device__ __forceinline__ Rounds(uint32_t items, uint32_t grid, bool few_rows) {
+  __device__ __forceinline__ Rounds(uint32_t items, uint32_t grid, bool halves) {
     const uint32_t left = items % grid;
-    const bool cut = 2 * left <= grid && !few_rows;
+    const bool cut = 2 * left <= grid && halves;
     whole = cut ? items - left : items;
     count = cut ? items + left : items;
   }
@@ -107,6 +108,7 @@ __device__ __forceinline__ Item decode(uint32_t item, uint32_t whole, int NT, in
     if (gp[mid] <= q) lo = mid;
     else hi = mid - 1;
   }
+  constexpr int TM = Shape<TK>::kRows;
   Item it;
   it.e = __builtin_amdgcn_readfirstlane(lo);
   const int g0 = __builtin_amdgcn_readfirstlane(gp[it.e]);
@@ -128,17 +130,19 @@ __device__ __forceinline__ Item decode(uint32_t item, uint32_t whole, int NT, in
 
 // TK: columns of an output tile, 256 or 128.  kW: this wave loads w, else dy.
 template <int TK, bool kW>
-__device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe, bool few_rows,
+__device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
                                     const uint8_t* dy, const uint8_t* w, int64_t nrows, int n,
                                     int k, int E, int align, uint16_t* dx, int lane, int wid) {
   constexpr int kRowBytes = TK * 2;                      // a staged row of w
   constexpr int kStageRows = kWBytes / kRowBytes;        // 32 or 64
   constexpr int kStageSteps = kStageRows / kStep;        // steps per stage of w: 1 or 2
   constexpr int kLoadRows = 1024 / kRowBytes;            // rows of w per load: 2 or 4
-  constexpr int FI = TK / 64;                            // 16-column tiles per wave
+  using S = Shape<TK>;
+  constexpr int FI = S::FI, FJ = S::FJ, kALoads = S::kALoads;
+  constexpr int kWaveRows = S::kRows / 2;
   const int NT = (k + TK - 1) / TK;
   const Rounds rounds((uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * NT, gridDim.x,
-                      few_rows);
+                      TK == 256);
   const uint32_t whole = rounds.whole, nitems = rounds.count;
   const int steps = n / kStep;  // even: n % 128 == 0
   const int wr = wid >> 2, wc = wid & 3;
@@ -151,15 +155,12 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
     const int piece = wc * FI;  // 32-byte pieces, eight to 256 bytes
     fw = (lds0 + tr_lane_offset<kRowBytes>(lane) + (piece >> 3) * 256) ^
          (uint32_t)((piece & 7) << 5);
-    const int row = wr * 128 + (lane & 15);
+    const int row = wr * kWaveRows + (lane & 15);
     fa = lds0 + kABase + (uint32_t)(row * 128 + ((g ^ a_key(row)) << 4));
   }
 
   // Loading side: this wave's stream of stages, running ahead of the
   // computation across items.
-  const uint32_t a_bytes = few_rows ? kARing / 4 : kARing / 2;  // a stage of dy
-  // Waves 6 and 7 load rows 128..255: none where there are few rows.
-  const bool loads = kW || !few_rows || wid < kLoadWaves + 2;
   uint32_t d_base = 0;  // the round
   int d_step = 0, d_live = 0;
   const uint8_t* d_src = nullptr;
@@ -209,7 +210,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
       d_src += (int64_t)kStageRows * k * 2;
       d_step += kStageSteps;
     } else {
-      d_slot = d_slot + a_bytes == kARing ? 0 : d_slot + a_bytes;
+      d_slot = d_slot + S::kABytes == kARing ? 0 : d_slot + S::kABytes;
       d_src += 128;
       d_step += 2;
     }
@@ -222,10 +223,9 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
 
   d_open();
 #pragma unroll 1
-  for (int g = 0; g < (kW ? kWStages : few_rows ? 4 : 2); ++g) {
-    if (loads)
+  for (int g = 0; g < (kW ? kWStages : S::kAStages); ++g) {
 #pragma unroll
-      for (int q = 0; q < (kW ? kWLoads : kALoads); ++q) d_load(q);
+    for (int q = 0; q < (kW ? kWLoads : kALoads); ++q) d_load(q);
     d_advance();
   }
 
@@ -244,7 +244,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
     const uint32_t item = round_item(base, nitems);
     if (item >= nitems) break;
     const Item it = decode<TK>(item, whole, NT, E, align, nrows, gp, pe);
-    const bool busy = wr * 128 < it.live;  // uniform: the wave has live rows
+    const bool busy = wr * kWaveRows < it.live;  // uniform: the wave has live rows
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -261,11 +261,10 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
       const uint32_t nw = !kNewW ? w_slot : w_slot + kWBytes == kWStages * kWBytes
                                                 ? 0
                                                 : w_slot + kWBytes;
-      const uint32_t na = !kNewA ? a_slot : a_slot + a_bytes == kARing ? 0 : a_slot + a_bytes;
+      const uint32_t na = !kNewA ? a_slot : a_slot + S::kABytes == kARing ? 0 : a_slot + S::kABytes;
       if constexpr (kNewW) {
         if constexpr (kW) wait_vmcnt<(kWStages - 2) * kWLoads>();
-        else if (kNewA && few_rows) wait_vmcnt<2 * kALoads>();
-        else if (kNewA) wait_vmcnt<0>();
+        else if (kNewA) wait_vmcnt<(S::kAStages - 2) * kALoads>();
         wait_lgkm0();
         barrier();
       }
@@ -278,7 +277,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
           acc[i][j] =
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[h][i], a[h][j], acc[i][j], 0, 0, 0);
           sched_fence();
-          if (TK == 128 && u < FI + FJ) {  // 16 MFMAs: a read beside each
+          if (TK == 128 && u < FI + FJ) {  // 8 MFMAs: a read beside all but two
             if (u < FI) read_w(h ^ 1, u, nw);
             else read_a(h ^ 1, u - FI, na);
           } else if (TK == 256 && u % 2 == 0 && u / 2 < FI + FJ) {
@@ -286,7 +285,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
             else read_a(h ^ 1, u / 2 - FI, na);
           }
         }
-        if (u % 2 == 1 && u / 2 < kL && loads) d_load(u / 2);
+        if (u % 2 == 1 && u / 2 < kL) d_load(u / 2);
         sched_fence();
       }
       w_slot = nw;
@@ -309,7 +308,7 @@ __device__ __forceinline__ void run(uint32_t lds0, const int* gp, const int* pe,
       if (tc < k) {
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
-          const int m = wr * 128 + j * 16 + (lane & 15);
+          const int m = wr * kWaveRows + j * 16 + (lane & 15);
           uint16_t* row = dx + (it.m0 + m) * k + tc + hf * 16 + r1 * 8;
 #pragma unroll
           for (int i = 0; i < FI; i += 2) {
@@ -336,12 +335,12 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
   __shared__ int gp[MOE_MAX_EXPERTS + 1];  // prefix of row groups per expert
   __shared__ int pe[MOE_MAX_EXPERTS];      // end of each expert's live rows
-  __shared__ int few;                      // no expert has more than 128 of them
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nrows = min((int64_t)status[0], capacity);
   if (wid == 0) {
-    int sum = 0, most = 0;
+    constexpr int TM = Shape<TK>::kRows;
+    int sum = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
       int ng = 0;
@@ -349,7 +348,6 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
         const int64_t st = e ? max(0, align_up_i(psum[e - 1], align)) : 0;
         const int64_t en = min((int64_t)psum[e], nrows);
         ng = en > st ? (int)((en - st + TM - 1) / TM) : 0;
-        most = max(most, (int)max((int64_t)0, en - st));
         pe[e] = psum[e];
       }
       const int incl = wave_incl_scan_i(ng);
@@ -357,14 +355,12 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(
       sum += __shfl(incl, 63, 64);
     }
     if (lane == 0) gp[E] = sum;
-    few = __any(most > TM / 2) ? 0 : 1;
   }
   __syncthreads();
-  const bool few_rows = TK == 128 && __builtin_amdgcn_readfirstlane(few);
   if (wid < kLoadWaves)
-    run<TK, true>(lds_addr(lds), gp, pe, few_rows, dy, w, nrows, n, k, E, align, dx, lane, wid);
+    run<TK, true>(lds_addr(lds), gp, pe, dy, w, nrows, n, k, E, align, dx, lane, wid);
   else
-    run<TK, false>(lds_addr(lds), gp, pe, few_rows, dy, w, nrows, n, k, E, align, dx, lane, wid);
+    run<TK, false>(lds_addr(lds), gp, pe, dy, w, nrows, n, k, E, align, dx, lane, wid);
 }
 
 }  // namespace
@@ -383,16 +379,14 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
   if (((uintptr_t)dy % 16) || ((uintptr_t)w % 16) || ((uintptr_t)dx % 16))
     return MOE_ERR_ALIGNMENT;
   if (capacity == 0) return MOE_OK;
-  // Bounds on the tiles: the rows of an expert are only known on the device.
-  const int64_t groups = (capacity + TM - 1) / TM + num_experts;
-  const int64_t wide = groups * ((k + 255) / 256);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (is_narrow(capacity, n, k, num_experts))
+  if (expected_tiles(capacity, k, num_experts, align, kNarrowTile) <= kFull)
     return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx, st);
-  const bool half_wide = wide < kMinWide && capacity <= (int64_t)TM * num_experts;
-  const int64_t tiles = half_wide ? groups * ((k + 127) / 128) : wide;
+  const bool half_wide = expected_tiles(capacity, k, num_experts, align, 128) <= kFull;
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
-  if (grid > 2 * tiles) grid = 2 * tiles;
+  const int t = half_wide ? 128 : 256;
+  const int64_t most = 2 * ((capacity + t - 1) / t + num_experts) * ((k + t - 1) / t);  // halves
+  if (grid > most) grid = most;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   auto kern = half_wide ? dgrad_kernel<128> : dgrad_kernel<256>;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, (const uint8_t*)dy,

@@ -169,39 +169,42 @@ __global__ __launch_bounds__(kThreads) void dgrad_narrow_kernel(
   __syncthreads();
   const int NT = k / T;
   const uint32_t nitems = (uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * (uint32_t)NT;
-  const uint32_t item = round_item(0, nitems);  // the grid has room for all
-  if (item >= nitems) return;
-  const int q = (int)(item / (uint32_t)NT);
-  int lo = 0, hi = E - 1;  // last e with gp[e] <= q
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (gp[mid] <= q) lo = mid;
-    else hi = mid - 1;
+  for (uint32_t base = 0;; base += gridDim.x) {
+    const uint32_t item = round_item(base, nitems);
+    if (item >= nitems) break;
+    const int q = (int)(item / (uint32_t)NT);
+    int lo = 0, hi = E - 1;  // last e with gp[e] <= q
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (gp[mid] <= q) lo = mid;
+      else hi = mid - 1;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
+    const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
+    const int local = (int)(item - (uint32_t)NT * (uint32_t)g0);
+    const int t0 = local / ge * T;
+    int64_t st, en;
+    expert_rows(psum, nrows, align, e, st, en);
+    const int64_t m0 = st + (int64_t)(local % ge) * T;
+    const int live = (int)min((int64_t)T, en - m0);
+    const uint8_t* a = dy + m0 * n * 2;
+    const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
+    v4f acc[4][4] = {};
+    wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
+                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                      load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
+                      load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
+                                dst + kOpBytes, lane);
+                    },
+                    acc);
+    float v[8];
+    join_waves(lds0, wid, lane, acc, v);
+    const int row = threadIdx.x >> 3;
+    if (row < live)
+      *reinterpret_cast<u32x4*>(dx + (m0 + row) * k + t0 + (threadIdx.x & 7) * 8) = pack8(v);
+    __syncthreads();  // the partial tiles have been read
   }
-  const int e = __builtin_amdgcn_readfirstlane(lo);
-  const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
-  const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
-  const int local = (int)(item - (uint32_t)NT * (uint32_t)g0);
-  const int t0 = local / ge * T;
-  int64_t st, en;
-  expert_rows(psum, nrows, align, e, st, en);
-  const int64_t m0 = st + (int64_t)(local % ge) * T;
-  const int live = (int)min((int64_t)T, en - m0);
-  const uint8_t* a = dy + m0 * n * 2;
-  const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
-  v4f acc[4][4] = {};
-  wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
-                  [&](int s, uint32_t dst) __attribute__((always_inline)) {
-                    load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
-                    load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
-                              dst + kOpBytes, lane);
-                  },
-                  acc);
-  float v[8];
-  join_waves(lds0, wid, lane, acc, v);
-  const int row = threadIdx.x >> 3;
-  if (row < live)
-    *reinterpret_cast<u32x4*>(dx + (m0 + row) * k + t0 + (threadIdx.x & 7) * 8) = pack8(v);
 }
 
 template <bool kF32>
@@ -244,7 +247,9 @@ __global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
 moe_status launch_dgrad_narrow(const void* dy, const void* w, const int32_t* psum,
                                const int32_t* status, int64_t capacity, int n, int k,
                                int num_experts, int align, void* dx, hipStream_t s) {
+  // A workgroup per CU (its LDS): more would only look at the layout and end.
   int64_t grid = ((capacity + T - 1) / T + num_experts) * (int64_t)(k / T);
+  if (grid > device_cus()) grid = device_cus();
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   hipLaunchKernelGGL(dgrad_narrow_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
                      (const uint8_t*)dy, (const uint8_t*)w, psum, status, capacity, n, k,

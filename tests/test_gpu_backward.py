@@ -235,6 +235,9 @@ ROUNDS = [
     ([256] * 7 + [257], 256, 2176, 16),
     ([300] * 9, 384, 4096, 16),
     ([2000, 0, 300, 2300], 256, 4160, 64),
+    ([127, 128, 129, 0, 1, 255, 256, 257], 512, 1088, 128),   # 128 x 128 ones
+    ([64, 1, 0, 65, 191, 192, 193, 700], 1152, 960, 32),
+    ([1500], 128, 2048, 16),
 ]
 
 

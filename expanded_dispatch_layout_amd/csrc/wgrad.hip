@@ -7,7 +7,8 @@
 //
 //  - One persistent workgroup per CU, 256 x 256 outputs, eight waves (two per
 //    SIMD) of 64 dy columns x 128 x columns: 8 x 4 v_mfma_f32_16x16x32_bf16
-//    per 32 rows.  (Measured at 18432 rows, 4096 x 6144: four waves of 128 x
+//    per 32 rows.  128 x 128 outputs (waves of 32 x 64, a ring of eight stages)
+//    where those leave CUs idle, 64 x 64 where these do.  (Measured at 18432 rows, 4096 x 6144: four waves of 128 x
 //    128 are bound by issue, 850 us against 808 then; 32x32x16 MFMAs draw more
 //    power, 879.)
 //  - The sum runs over the rows, along which neither operand is contiguous:
@@ -27,6 +28,8 @@
 //    the same instructions take 612 us.
 #include <math.h>
 
+#include <type_traits>
+
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -35,19 +38,21 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512;
-constexpr int TN = 256, TK = 256;            // output tile: dy columns x x columns
-constexpr int kStep = 32;                    // rows per stage
-constexpr int kRowBytes = 512;               // 256 bf16
-constexpr int kOpBytes = kStep * kRowBytes;  // 16 KB: one operand of a stage
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kStages = 5;
-constexpr int kRing = kStages * kStageBytes;   // 160 KB, all of the CU's
-constexpr int kLoads = 4;                      // DMA instructions per wave and stage
-constexpr int FI = 8, FJ = 4;                  // 16-wide tiles per wave: 128 x columns, 64 dy ones
+constexpr int kStep = 32;         // rows per stage
+constexpr int kLds = 160 * 1024;  // all of the CU's
 
-// Fewer tiles than this and short sums: the narrow kernel.
-constexpr int64_t kMinTiles = 64;
-constexpr int64_t kNarrowRows = 4096;  // rows, times the rounds of narrow tiles
+// Output tiles are T x T, 256 or 128.
+template <int T>
+struct Shape {
+  static constexpr int kRowBytes = T * 2;
+  static constexpr int kOpBytes = kStep * kRowBytes;  // one operand of a stage
+  static constexpr int kStageBytes = 2 * kOpBytes;    // 32 or 16 KB
+  static constexpr int kStages = T == 256 ? 5 : 8;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kLoads = T / 64;               // DMA instructions per wave and stage
+  static constexpr int FI = T / 32, FJ = T / 64;      // 16-wide tiles per wave: x, dy columns
+};
+
 constexpr int64_t kFullTiles = 256;  // one per CU
 
 struct Tile {
@@ -65,6 +70,7 @@ __device__ __forceinline__ int stages_of(int live) {
 // Items of one expert: panels of 8 tiles along t, j-major inside a panel, so
 // that the 32 neighbouring items of an XCD's CUs are a 4 x 8 block and share
 // their operands in its L2.
+template <int T>
 __device__ __forceinline__ Tile decode(uint32_t item, int NJ, int NT, int splits,
                                        const int32_t* psum, int64_t nrows, int align) {
   Tile t;
@@ -76,8 +82,8 @@ __device__ __forceinline__ Tile decode(uint32_t item, int NJ, int NT, int splits
   const int panel = local / (8 * NJ);
   const int rem = local - panel * 8 * NJ;
   const int w = min(8, NT - panel * 8);
-  t.j0 = rem / w * TN;
-  t.t0 = (panel * 8 + rem % w) * TK;
+  t.j0 = rem / w * T;
+  t.t0 = (panel * 8 + rem % w) * T;
   t.st = t.e ? max(0, align_up_i(psum[t.e - 1], align)) : 0;
   const int64_t en = min((int64_t)psum[t.e], nrows);
   t.live = en > t.st ? (int)(en - t.st) : 0;
@@ -92,17 +98,21 @@ __device__ __forceinline__ Tile decode(uint32_t item, int NJ, int NT, int splits
 
 // kF32: dw is fp32, else bf16.  kAdd: the sums are added to it.  kParts: part z
 // of a split sum goes to dw[z][E][n][k].
-template <bool kF32, bool kAdd, bool kParts>
+template <int T, bool kF32, bool kAdd, bool kParts>
 __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     const uint8_t* __restrict__ dy, const uint8_t* __restrict__ x,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
     int k, int E, int align, int splits, void* __restrict__ dw) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing];  // addresses are XORed
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];  // addresses are XORed
+  using S = Shape<T>;
+  constexpr int kRowBytes = S::kRowBytes, kOpBytes = S::kOpBytes, kStageBytes = S::kStageBytes;
+  constexpr int kStages = S::kStages, kRing = S::kRing, kLoads = S::kLoads;
+  constexpr int FI = S::FI, FJ = S::FJ;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_addr(lds);
   const int64_t nrows = min((int64_t)status[0], capacity);
-  const int NJ = (n + TN - 1) / TN, NT = (k + TK - 1) / TK;
+  const int NJ = (n + T - 1) / T, NT = (k + T - 1) / T;
   // At most 2^24 tiles (1024 experts, 128 x 128), and a split sum has few.
   const uint32_t nitems = (uint32_t)E * NJ * NT * splits;
 
@@ -134,8 +144,9 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   uint32_t fx, fy;  // x, dy
   {
     const uint32_t base = lds0 + tr_lane_offset<kRowBytes>(lane);
-    fx = base + kOpBytes + wt * 256;
-    fy = (base + (wj >> 1) * 256) ^ (uint32_t)((wj & 1) * FJ * 32);
+    const int px = wt * FI, py = wj * FJ;  // 32-byte pieces, eight to 256 bytes
+    fx = (base + kOpBytes + (px >> 3) * 256) ^ (uint32_t)((px & 7) << 5);
+    fy = (base + (py >> 3) * 256) ^ (uint32_t)((py & 7) << 5);
   }
 
   // DMA side: the next stage to load.
@@ -143,22 +154,25 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   int d_left = 0;    // rows left of its tile (<= 0: a stage of zeros)
   int d_stages = 0;  // stages left of its tile
   const uint8_t *d_dy = nullptr, *d_x = nullptr;
-  uint32_t d_offa[2] = {}, d_offb[2] = {};  // x, dy: offsets of this lane's chunks
+  constexpr int kHalf = kLoads / 2;            // of each operand: 2 or 1
+  constexpr int kLoadRows = 1024 / kRowBytes;  // 2 or 4
+  constexpr int kLanes = 64 / kLoadRows;       // per row
+  uint32_t d_offa[kHalf] = {}, d_offb[kHalf] = {};  // x, dy: offsets of this lane's chunks
   uint32_t d_slot = 0;            // LDS offset of the next slot
   auto d_open = [&]() __attribute__((always_inline)) {  // next tile that has rows
     while (true) {
       const uint32_t d_item = round_item(d_base, nitems);
       if (d_item >= nitems) break;
-      const Tile t = decode(d_item, NJ, NT, splits, psum, nrows, align);
+      const Tile t = decode<T>(d_item, NJ, NT, splits, psum, nrows, align);
       if (t.live > 0) {
         d_left = t.live;
         d_stages = stages_of(t.live);
         d_dy = dy + (t.st * n + t.j0) * 2;
         d_x = x + (t.st * k + t.t0) * 2;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = (wid * 2 + j) * 2 + (lane >> 5);
-          const int col = ((lane & 31) ^ (tr_key(row) << 1)) * 8;
+        for (int j = 0; j < kHalf; ++j) {
+          const int row = wid * 4 + j * kLoadRows + lane / kLanes;
+          const int col = ((lane % kLanes) ^ (tr_key(row) << 1)) * 8;
           d_offb[j] = (uint32_t)(row * n + min(col, n - 8 - t.j0)) * 2u;
           d_offa[j] = (uint32_t)(row * k + min(col, k - 8 - t.t0)) * 2u;
         }
@@ -167,15 +181,15 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
       d_base = kAdd && t.idle ? skip_idle(d_base, t.e) : d_base + gridDim.x;
     }
   };
-  // Load q (0..3) of the next stage: dy rows first, then x.  Rows past the
+  // Load q of the next stage: dy rows first, then x.  Rows past the
   // tile's last live one, and every row once there is no tile left, read
   // zeros, so that each step issues the same loads without a branch.
-  const int d_row = wid * 4 + (lane >> 5);  // this lane's row in load 0; 2 more per load
+  const int d_row = wid * 4 + lane / kLanes;  // this lane's row in load 0
   auto d_load = [&](int q) __attribute__((always_inline)) {
-    const int j = q & 1;
-    const uint8_t* p = q < 2 ? d_dy + d_offb[j] : d_x + d_offa[j];
-    p = d_row + 2 * j < d_left ? p : zero_chunk();
-    dma16_ptr(p, lds0 + d_slot + wid * 2048 + (q < 2 ? 0 : kOpBytes) + j * 1024);
+    const int j = q % kHalf;
+    const uint8_t* p = q < kHalf ? d_dy + d_offb[j] : d_x + d_offa[j];
+    p = d_row + kLoadRows * j < d_left ? p : zero_chunk();
+    dma16_ptr(p, lds0 + d_slot + (wid * kHalf + j) * 1024 + (q < kHalf ? 0 : kOpBytes));
   };
   auto d_advance = [&]() __attribute__((always_inline)) {
     d_slot = d_slot + kStageBytes == kRing ? 0 : d_slot + kStageBytes;
@@ -201,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
   for (uint32_t base = 0, next;; base = next) {
     const uint32_t item = round_item(base, nitems);
     if (item >= nitems) break;
-    const Tile t = decode(item, NJ, NT, splits, psum, nrows, align);
+    const Tile t = decode<T>(item, NJ, NT, splits, psum, nrows, align);
     const int steps = stages_of(t.live);
     next = kAdd && t.idle ? skip_idle(base, t.e) : base + gridDim.x;
 #pragma unroll
@@ -229,7 +243,11 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
             acc[i][j] =
                 __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
             sched_fence();
-            if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr<kRowBytes>(ny ^ ((u / 2) << 5));
+            if (T == 128) {  // 8 MFMAs: a read or a load beside each
+              if (u < FJ) b[h ^ 1][u] = frag_tr<kRowBytes>(ny ^ (u << 5));
+              else if (u < FJ + FI) a[h ^ 1][u - FJ] = frag_tr<kRowBytes>(nx ^ ((u - FJ) << 5));
+              else d_load(u - FJ - FI);
+            } else if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr<kRowBytes>(ny ^ ((u / 2) << 5));
             else if (u % 2 == 0 && u / 2 < FJ + FI)
               a[h ^ 1][u / 2 - FJ] = frag_tr<kRowBytes>(nx ^ ((u / 2 - FJ) << 5));
             else if (u % 4 == 1 && u / 4 < kLoads) d_load(u / 4);
@@ -249,10 +267,10 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
     // of 64 bytes of 16 (one rank's share, 1024 rows of 8 x 4096 x 7168, through
     // the caches: 137 us against 160 in bf16, 394 against 432 accumulating in
     // fp32).
-    barrier();  // every wave has read that slot
-    const uint32_t own =
-        lds0 + (c_slot == 0 ? kRing : c_slot) - kStageBytes + (uint32_t)wid * 4096u;
-    const int jc = t.j0 + wj * 64, tc = t.t0 + wt * 128;
+    if constexpr (T == 256) barrier();  // every wave has read that slot
+    const uint32_t own = lds0 + (uint32_t)wid * 4096u +
+                         (T == 256 ? (c_slot == 0 ? kRing : c_slot) - kStageBytes : kRing);
+    const int jc = t.j0 + wj * FJ * 16, tc = t.t0 + wt * FI * 16;
     const int fr = lane & 15, g = lane >> 4;
     // 64 columns (tiles i0..) of 16 rows into LDS as fp32.
     auto stage = [&](int i0, int j) __attribute__((always_inline)) {
@@ -320,21 +338,22 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
                                           reinterpret_cast<u32x4*>(o + 8 * q * (int64_t)k));
             }
           }
-        } else {  // all 128 columns as bf16
+        } else {  // all columns as bf16, kC chunks a row
+          constexpr int kC = 2 * FI, kPass = 64 / kC;
 #pragma unroll
           for (int i = 0; i < FI; ++i) {
             typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-            lds_store<u32x2>(own + fr * 256 + (((2 * i + (g >> 1)) ^ fr) << 4) + (g & 1) * 8,
-                             u32x2{pk_bf16(acc[i][j][0], acc[i][j][1]),
-                                   pk_bf16(acc[i][j][2], acc[i][j][3])});
+            lds_store<u32x2>(
+                own + fr * kC * 16 + (((2 * i + (g >> 1)) ^ (fr % kC)) << 4) + (g & 1) * 8,
+                u32x2{pk_bf16(acc[i][j][0], acc[i][j][1]), pk_bf16(acc[i][j][2], acc[i][j][3])});
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x4 v = lds_load<u32x4>(own + (4 * q + g) * 256 + ((fr ^ (4 * q + g)) << 4));
-            if (tc + fr * 8 < k)
+          for (int q = 0; q < 16 / kPass; ++q) {
+            const int r = q * kPass + lane / kC, c = lane % kC;
+            const u32x4 v = lds_load<u32x4>(own + r * kC * 16 + ((c ^ (r % kC)) << 4));
+            if (tc + c * 8 < k)
               __builtin_nontemporal_store(
-                  v, reinterpret_cast<u32x4*>((uint16_t*)dw + (row0 + 4 * q + g) * k + tc +
-                                              fr * 8));
+                  v, reinterpret_cast<u32x4*>((uint16_t*)dw + (row0 + r) * k + tc + c * 8));
           }
         }
       }
@@ -372,26 +391,24 @@ using namespace moe;
 namespace moe {
 namespace {
 
-int64_t wide_tiles(int n, int k, int num_experts) {
-  return (int64_t)num_experts * ((n + TN - 1) / TN) * ((k + TK - 1) / TK);
+int64_t tiles_of(int n, int k, int num_experts, int t) {
+  return (int64_t)num_experts * ((n + t - 1) / t) * ((k + t - 1) / t);
 }
 
-// The narrow kernel, where the wide tiles leave CUs idle and an average expert's
-// sum is short.  One of its rounds over the CUs takes about 2.5 us and 1 us per
-// 200 rows; the wide kernel 8 us and 1 us per 64 rows, or, split, at least 16.
-// Measured, narrow against the wide kernel (split or not, whichever
-// wgrad_splits takes), rows per expert: 1024 x 256, one expert, 1024 rows 6.5
-// and 16.2 us, 4096 rows 19.3 and 19.8, 8192 rows 33.4 and 23.6; 1024 x 1024, one
-// expert, 2048 rows 13.2 and 23.8, 8192 rows 37.6 and 37.2; 512 x 512, eight (two
-// rounds), 1024 rows 18.7 and 24.7, 2048 rows 28.9 and 29.1, 4096 rows 51 and 38;
-// 1024 x 1024, three (three rounds), 1024 rows 22 and 26.4, 4096 rows 54.7 and 44.8.
-// With 64 wide tiles (four rounds; 2048 x 512, four experts) 64 rows take 13.7 and
-// 9.2, 1024 rows 32.4 and 26.9.
-bool is_narrow(int64_t capacity, int n, int k, int num_experts) {
-  const int64_t rounds =
-      ((int64_t)num_experts * (n / kNarrowTile) * (k / kNarrowTile) + kFullTiles - 1) / kFullTiles;
-  return wide_tiles(n, k, num_experts) < kMinTiles &&
-         rounds * (capacity / num_experts) <= kNarrowRows;
+// Which tiles: the smallest that the CUs hold at once, since a step of a tile
+// takes its loads' latency or longer.  With long sums the 256 x 256 ones, split
+// over workgroups (wgrad_splits).  Measured with 64 (grad_narrow.hip) / 128 /
+// 256, rows per expert: 1024 x 1024, one expert (256 tiles of 64), 16 rows 4.0 /
+// 5.5 / 7.4 us, 1024 rows 8.4 / 14.4 / 19.9, 4096 rows 20 / 42 / 29, 8192 rows 36 /
+// 78 / 38; 1024 x 1024, four (256 tiles of 128), 16 rows 11.9 / 6.5 / 8.3, 512 rows
+// 20 / 11 / 17, 2048 rows 40 / 26 / 38, 4096 rows 70 / 46 / 50; 4096 x 1024, one,
+// 8192 rows 137 / 85 / 78; 1024 x 1024, eight, 512 rows 36 / 18 / 18.
+constexpr int64_t kShortRows = 4096;
+int tile_of(int64_t capacity, int n, int k, int num_experts) {
+  const int64_t rows = capacity / num_experts;
+  if (tiles_of(n, k, num_experts, 64) <= kFullTiles && rows <= kShortRows) return 64;
+  if (tiles_of(n, k, num_experts, 128) <= kFullTiles && rows <= kShortRows) return 128;
+  return 256;
 }
 
 // Parts that each expert's sum is cut into where the tiles leave CUs idle.  A
@@ -403,8 +420,8 @@ bool is_narrow(int64_t capacity, int n, int k, int num_experts) {
 // 16384 rows of two, 2048 x 1024, 170 / 79 / 79; 20000 rows of four, 2048 x 256,
 // 109 / 43 / 46.
 int wgrad_splits(int64_t capacity, int n, int k, int num_experts) {
-  if (is_narrow(capacity, n, k, num_experts)) return 1;
-  const int64_t tiles = wide_tiles(n, k, num_experts), rows = capacity / num_experts;
+  if (tile_of(capacity, n, k, num_experts) < 256) return 1;
+  const int64_t tiles = tiles_of(n, k, num_experts, 256), rows = capacity / num_experts;
   if (tiles * 2 > kFullTiles) return 1;
   const double best =
       sqrt((double)rows / 64.0 * 0.75e6 / ((double)num_experts * (double)n * (double)k));
@@ -441,20 +458,26 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
       return MOE_ERR_WORKSPACE;
     if ((uintptr_t)workspace % 256) return MOE_ERR_ALIGNMENT;
   }
-  const int64_t items = wide_tiles(n, k, num_experts);
+  const int tile = tile_of(capacity, n, k, num_experts);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (is_narrow(capacity, n, k, num_experts))
+  if (tile == 64)
     return launch_wgrad_narrow(dy, x, psum, status, capacity, n, k, num_experts, align, fmt,
                                accumulate, dw, st);
+  const int64_t items = tiles_of(n, k, num_experts, tile) * splits;
   int64_t grid = device_cus();  // one workgroup per CU, a whole number per XCD
-  if (grid > items * splits) grid = items * splits;
+  if (grid > items) grid = items;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   const bool f32 = fmt == MOE_GRAD_F32;
-  auto kern = splits > 1   ? wgrad_kernel<true, false, true>
-              : f32        ? (accumulate ? wgrad_kernel<true, true, false>
-                                         : wgrad_kernel<true, false, false>)
-              : accumulate ? wgrad_kernel<false, true, false>
-                           : wgrad_kernel<false, false, false>;
+  auto pick = [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    return f32 ? (accumulate ? wgrad_kernel<T, true, true, false>
+                             : wgrad_kernel<T, true, false, false>)
+               : (accumulate ? wgrad_kernel<T, false, true, false>
+                             : wgrad_kernel<T, false, false, false>);
+  };
+  auto kern = splits > 1    ? wgrad_kernel<256, true, false, true>
+              : tile == 128 ? pick(std::integral_constant<int, 128>())
+                            : pick(std::integral_constant<int, 256>());
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, (const uint8_t*)dy,
                      (const uint8_t*)x, psum, status, capacity, n, k, num_experts, align,
                      splits, splits > 1 ? workspace : dw);

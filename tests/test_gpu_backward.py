@@ -226,7 +226,23 @@ def test_wgrad_long_sums(counts, n, k, align, f32, accumulate):
     test_wgrad(counts, n, k, align, 1, f32, accumulate)
 
 
-# Numbers of 64 x 64, 256 x 128 and 256 x 256 tiles just below and above whole
+# Weight gradients too large for one round of 64 x 64 tiles, not of 128 x 128.
+MIDDLE = [
+    ([200, 0, 77, 1], 640, 832, 16),
+    ([33], 2048, 1024, 64),
+    ([1, 31, 32, 33, 63, 64, 65, 0, 700], 384, 704, 32),
+    ([0, 900, 0, 2, 0, 129], 512, 960, 256),
+]
+
+
+@pytest.mark.parametrize("f32,accumulate", [(False, False), (True, False), (True, True),
+                                            (False, True)])
+@pytest.mark.parametrize("counts,n,k,align", MIDDLE)
+def test_wgrad_middle(counts, n, k, align, f32, accumulate):
+    test_wgrad(counts, n, k, align, 1, f32, accumulate)
+
+
+# Numbers of 64 x 64, 128 x 128 and 256 x 256 tiles just below and above whole
 # rounds of the CUs, and far fewer than the sizes allow.
 ROUNDS = [
     ([65] * 8, 2048, 1024, 16),

@@ -1,11 +1,11 @@
 // The grouped products' gradients where the 256 x 256 tiles of dgrad.hip and
 // wgrad.hip are too few to fill the CUs: 64 x 64 tiles, the reduction split
 // over the eight waves of a workgroup.  Bound by latency: launch, layout, a few
-// rounds of loads, the joining of the waves (140 rows, 6 x 896 x 640: below the
-// 7.4 us that a call takes to issue, against 16.6 with the wide tiles).
+// rounds of loads, the joining of the waves (140 rows, 6 x 896 x 640: 6.8 us,
+// below the 7.4 that a call takes to issue).
 //
 //  - A wave takes every eighth 32-deep stage of the reduction.  Its stages are
-//    its own: it loads them HBM -> LDS into its own two slots of 8 KB and
+//    its own: it loads them HBM -> LDS into its own 16 KB, two stages or three, and
 //    waits for its own loads only, so there is no barrier in the loop.
 //  - The eight partial tiles (fp32) meet in LDS, each in its wave's own slots,
 //    and are summed in the waves' order: equal calls give equal bits.
@@ -14,6 +14,8 @@
 //    where the reduction runs along the staged rows (w, and both operands of
 //    the weight gradient), and as 16-byte pieces where it runs along the
 //    columns (dy of the input gradient).
+#include <type_traits>
+
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -25,10 +27,7 @@ constexpr int kThreads = 512, kWaves = 8;
 constexpr int T = kNarrowTile;            // 64
 constexpr int kStep = 32;
 constexpr int kOpBytes = 4096;            // one operand of a stage: 32 x 64 bf16
-constexpr int kSlotBytes = 2 * kOpBytes;
-constexpr int kWaveBytes = 2 * kSlotBytes;  // two slots; later one fp32 64 x 64 tile
-constexpr int kLoads = 8;                 // per stage
-static_assert(kWaveBytes == T * T * 4, "a partial tile fills its wave's slots");
+constexpr int kWaveBytes = T * T * 4;     // slots of stages; later one fp32 64 x 64 tile
 
 // Row-staged operand (reduction along the rows): 32 rows of 128 bytes.  Four
 // 32-byte pieces per row, XOR-swizzled by row so that the 8 rows that half a
@@ -64,11 +63,12 @@ __device__ __forceinline__ void load_rows(const uint8_t* src, int64_t ld, int nr
     dma16_ptr(row < nr ? p : zero_chunk(), lds + q * 1024);
   }
 }
-// The same of a column-staged operand: rows 16 q + lane / 4.
+// Loads q < kQ of a column-staged operand: rows 16 q + lane / 4.
+template <int kQ>
 __device__ __forceinline__ void load_cols(const uint8_t* src, int64_t ld, int nr, uint32_t lds,
                                           int lane) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < kQ; ++q) {
     const int row = 16 * q + (lane >> 2);
     const uint8_t* p = src + row * ld + (((lane & 3) ^ col_key(row)) << 4);
     dma16_ptr(row < nr ? p : zero_chunk(), lds + q * 1024);
@@ -76,35 +76,42 @@ __device__ __forceinline__ void load_cols(const uint8_t* src, int64_t ld, int nr
 }
 
 // Sum over this wave's stages s = s0, s0 + ds, .. < ns: load(s, lds) issues a
-// stage's loads; x's fragments (the tile's columns) are row-staged, y's (its
-// rows) row- or column-staged.
-template <bool kYRows, typename Load>
+// stage's loads, of x (the tile's columns, row-staged) and y (kQ tiles of 16 of
+// its rows, row- or column-staged).  A slot holds x's, then y's; there are two,
+// or three of the smallest.
+template <bool kYRows, int kQ, typename Load>
 __device__ __forceinline__ void wave_sum(int s0, int ds, int ns, uint32_t base, int lane,
                                          Load&& load, v4f (&acc)[4][4]) {
-  const uint32_t fx = base + kOpBytes + row_lane(lane);
-  const uint32_t fy = base + (kYRows ? row_lane(lane) : col_lane(lane));
-  if (s0 < ns) load(s0, base);
-  if (s0 + ds < ns) load(s0 + ds, base + kSlotBytes);
+  constexpr uint32_t kSlotBytes = kOpBytes + kQ * 1024;
+  constexpr int kSlots = kWaveBytes / kSlotBytes, kLoads = 4 + kQ;
+  static_assert(kSlots == 2 || kSlots == 3);
+  const uint32_t fx = base + row_lane(lane);
+  const uint32_t fy = base + kOpBytes + (kYRows ? row_lane(lane) : col_lane(lane));
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (s0 + i * ds < ns) load(s0 + i * ds, base + i * kSlotBytes);
   uint32_t slot = 0;
   for (int s = s0; s < ns; s += ds) {
-    if (s + ds < ns) wait_vmcnt<kLoads>();
+    if (kSlots == 3 && s + 2 * ds < ns) wait_vmcnt<2 * kLoads>();
+    else if (s + ds < ns) wait_vmcnt<kLoads>();
     else wait_vmcnt<0>();
-    bf16x8 x[4], y[4];
+    bf16x8 x[4], y[kQ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = frag_tr<128>((fx + slot) ^ (uint32_t)(i << 5));
+    for (int i = 0; i < 4; ++i) x[i] = frag_tr<128>((fx + slot) ^ (uint32_t)(i << 5));
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
       if constexpr (kYRows) y[i] = frag_tr<128>((fy + slot) ^ (uint32_t)(i << 5));
       else y[i] = lds_load<bf16x8>(fy + slot + i * 1024);
     }
     wait_lgkm0();  // the slot has been read: it may be loaded anew
     sched_fence();
-    if (s + 2 * ds < ns) load(s + 2 * ds, base + slot);
+    if (s + kSlots * ds < ns) load(s + kSlots * ds, base + slot);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kQ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
-    slot ^= kSlotBytes;
+    slot = slot + kSlotBytes == kSlots * kSlotBytes ? 0 : slot + kSlotBytes;
   }
 }
 
@@ -191,13 +198,23 @@ __global__ __launch_bounds__(kThreads) void dgrad_narrow_kernel(
     const uint8_t* a = dy + m0 * n * 2;
     const uint8_t* b = w + ((int64_t)e * n * k + t0) * 2;
     v4f acc[4][4] = {};
-    wave_sum<false>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
-                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
-                      load_cols(a + s * kStep * 2, (int64_t)n * 2, live, dst, lane);
-                      load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep,
-                                dst + kOpBytes, lane);
-                    },
-                    acc);
+    // Only 16-row tiles that hold live rows are loaded and computed (two rows,
+    // 5 x 5376 x 576: 12.0 us, 14.7 with all four; 24 rows, 2 x 4224 x 128: 9.2
+    // and 12.2).  dy first: the weights first take 4 % longer at 64 rows.
+    auto sum = [&](auto q) __attribute__((always_inline)) {
+      constexpr int kQ = decltype(q)::value;
+      wave_sum<false, kQ>(wid, kWaves, n / kStep, lds0 + wid * kWaveBytes, lane,
+                          [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                            load_cols<kQ>(a + s * kStep * 2, (int64_t)n * 2, live,
+                                          dst + kOpBytes, lane);
+                            load_rows(b + (int64_t)s * kStep * k * 2, (int64_t)k * 2, kStep, dst,
+                                      lane);
+                          },
+                          acc);
+    };
+    if (live <= 16) sum(std::integral_constant<int, 1>());
+    else if (live <= 32) sum(std::integral_constant<int, 2>());
+    else sum(std::integral_constant<int, 4>());
     float v[8];
     join_waves(lds0, wid, lane, acc, v);
     const int row = threadIdx.x >> 3;
@@ -227,14 +244,14 @@ __global__ __launch_bounds__(kThreads) void wgrad_narrow_kernel(
   const uint8_t* a = dy + (st * n + j0) * 2;
   const uint8_t* b = x + (st * k + t0) * 2;
   v4f acc[4][4] = {};
-  wave_sum<true>(wid, kWaves, (live + kStep - 1) / kStep, lds0 + wid * kWaveBytes, lane,
-                 [&](int s, uint32_t dst) __attribute__((always_inline)) {
-                   const int64_t r = (int64_t)s * kStep;
-                   const int nr = (int)min((int64_t)kStep, live - r);
-                   load_rows(a + r * n * 2, (int64_t)n * 2, nr, dst, lane);
-                   load_rows(b + r * k * 2, (int64_t)k * 2, nr, dst + kOpBytes, lane);
-                 },
-                 acc);
+  wave_sum<true, 4>(wid, kWaves, (live + kStep - 1) / kStep, lds0 + wid * kWaveBytes, lane,
+                    [&](int s, uint32_t dst) __attribute__((always_inline)) {
+                      const int64_t r = (int64_t)s * kStep;
+                      const int nr = (int)min((int64_t)kStep, live - r);
+                      load_rows(b + r * k * 2, (int64_t)k * 2, nr, dst, lane);
+                      load_rows(a + r * n * 2, (int64_t)n * 2, nr, dst + kOpBytes, lane);
+                    },
+                    acc);
   float v[8];
   join_waves(lds0, wid, lane, acc, v);
   const int64_t at =

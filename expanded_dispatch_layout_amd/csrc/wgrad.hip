@@ -8,9 +8,9 @@
 //  - One persistent workgroup per CU, 256 x 256 outputs, eight waves (two per
 //    SIMD) of 64 dy columns x 128 x columns: 8 x 4 v_mfma_f32_16x16x32_bf16
 //    per 32 rows.  128 x 128 outputs (waves of 32 x 64, a ring of eight stages)
-//    where those leave CUs idle, 64 x 64 where these do.  (Measured at 18432 rows, 4096 x 6144: four waves of 128 x
-//    128 are bound by issue, 850 us against 808 then; 32x32x16 MFMAs draw more
-//    power, 879.)
+//    where those leave CUs idle, 64 x 64 where these do.  (Measured at 18432
+//    rows, 4096 x 6144: four waves of 128 x 128 are bound by issue, 850 us
+//    against 808 then; 32x32x16 MFMAs draw more power, 879.)
 //  - The sum runs over the rows, along which neither operand is contiguous:
 //    both are staged as rows (coalesced loads) and read through
 //    ds_read_b64_tr_b16 (lds_dma.hpp).
@@ -247,7 +247,8 @@ __global__ __launch_bounds__(kThreads, 1) void wgrad_kernel(
               if (u < FJ) b[h ^ 1][u] = frag_tr<kRowBytes>(ny ^ (u << 5));
               else if (u < FJ + FI) a[h ^ 1][u - FJ] = frag_tr<kRowBytes>(nx ^ ((u - FJ) << 5));
               else d_load(u - FJ - FI);
-            } else if (u % 2 == 0 && u / 2 < FJ) b[h ^ 1][u / 2] = frag_tr<kRowBytes>(ny ^ ((u / 2) << 5));
+            } else if (u % 2 == 0 && u / 2 < FJ)
+              b[h ^ 1][u / 2] = frag_tr<kRowBytes>(ny ^ ((u / 2) << 5));
             else if (u % 2 == 0 && u / 2 < FJ + FI)
               a[h ^ 1][u / 2 - FJ] = frag_tr<kRowBytes>(nx ^ ((u / 2 - FJ) << 5));
             else if (u % 4 == 1 && u / 4 < kLoads) d_load(u / 4);

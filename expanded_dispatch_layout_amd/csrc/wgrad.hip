@@ -403,12 +403,17 @@ int64_t tiles_of(int n, int k, int num_experts, int t) {
 // 5.5 / 7.4 us, 1024 rows 8.4 / 14.4 / 19.9, 4096 rows 20 / 42 / 29, 8192 rows 36 /
 // 78 / 38; 1024 x 1024, four (256 tiles of 128), 16 rows 11.9 / 6.5 / 8.3, 512 rows
 // 20 / 11 / 17, 2048 rows 40 / 26 / 38, 4096 rows 70 / 46 / 50; 4096 x 1024, one,
-// 8192 rows 137 / 85 / 78; 1024 x 1024, eight, 512 rows 36 / 18 / 18.
-constexpr int64_t kShortRows = 4096;
+// 8192 rows 137 / 85 / 78.
+// Two rounds of 128 take as long as one of 256 where experts are even, and less
+// where they are not, since fewer CUs wait for the longest: 1024 x 1024, eight,
+// 4096 rows even 17.9 / 18.4 us, 6400 rows of which 43 % are one expert's 40 / 62;
+// three rounds lose more (384 x 1728, fourteen, 5473 rows even 21.2 / 16.3).
+constexpr int64_t kShortRows = 4608;
 int tile_of(int64_t capacity, int n, int k, int num_experts) {
   const int64_t rows = capacity / num_experts;
   if (tiles_of(n, k, num_experts, 64) <= kFullTiles && rows <= kShortRows) return 64;
-  if (tiles_of(n, k, num_experts, 128) <= kFullTiles && rows <= kShortRows) return 128;
+  const int64_t rounds = (tiles_of(n, k, num_experts, 128) + kFullTiles - 1) / kFullTiles;
+  if (rounds <= 2 && rounds * rows <= kShortRows) return 128;
   return 256;
 }
 

@@ -144,6 +144,20 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _on(stream):
+    """A context in which torch's own work goes to the stream of that handle
+    (None: the current one).  Handle 0 is the default stream:
+    torch.cuda.ExternalStream(0) would be some stream of torch's pool."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    handle = int(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle
+                             else torch.cuda.default_stream())
+
+
 def _check(fn, code):
     if code != MOE_OK:
         raise MoeError(fn, code)
@@ -727,11 +741,7 @@ class TrainableBf16MoE(StandardBf16MoE):
                stream=None):
         """One AdamW step on both weights with the gradients in dw13 and dw2 and
         the learning rate in the lr tensor; counts step up first."""
-        import torch
-        if stream is None:
+        with _on(stream):
             self.step.add_(1)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(int(stream))):
-                self.step.add_(1)
         moe_adamw(self.tensors, self.step, self.lr, beta1, beta2, eps, weight_decay, grad_scale,
                   stream)

@@ -1,0 +1,51 @@
+"""TrainableBf16MoE on streams other than the current one, by handle."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import expanded_dispatch_layout_amd as M  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+BF = torch.bfloat16
+ROWS, TOPK, E, H, I = 96, 2, 4, 256, 128
+
+
+def weights(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    normal = lambda *s: torch.empty(s, device="cuda").normal_(0, 0.1, generator=g).to(BF)  # noqa: E731
+    ids = torch.from_numpy(np.random.default_rng(seed).integers(0, E, (ROWS, TOPK))
+                           .astype(np.int32)).cuda()
+    return (normal(E, 2 * I, H), normal(E, H, I), normal(ROWS, H), normal(ROWS, H), ids,
+            torch.rand((ROWS, TOPK), generator=g, device="cuda"))
+
+
+def step(mod, x, dout, ids, w, stream=None):
+    out = mod(x, ids, w, stream=stream)
+    dx, dc = mod.backward(dout, w, stream=stream)
+    mod.update(stream=stream)
+    return [out, dx, dc, mod.master13, mod.master2, mod.w13, mod.w2, mod.step]
+
+
+def test_the_default_stream_by_its_handle():
+    """Handle 0 is the default stream, whatever stream is current."""
+    w13, w2, *rest = weights(5)
+    mod = M.TrainableBf16MoE(ROWS, TOPK, w13.clone(), w2.clone(), align=16)
+    want = [t.clone() for _ in range(2) for t in step(mod, *rest)]
+    mod = M.TrainableBf16MoE(ROWS, TOPK, w13.clone(), w2.clone(), align=16)
+    torch.cuda.synchronize()
+    got = []
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(2):
+            res = step(mod, *rest, stream=0)
+            torch.cuda.synchronize()
+            got += [t.clone() for t in res]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

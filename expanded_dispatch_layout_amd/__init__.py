@@ -158,6 +158,20 @@ def _on(stream):
                              else torch.cuda.default_stream())
 
 
+def _output(stream, shape, dtype, device):
+    """A new tensor for a call on the stream of that handle to write.  Its memory
+    belongs to that stream: no other one can still be at work on an earlier
+    tensor there.  The current stream counts as a user, so a tensor that is
+    dropped after it was used there is not handed out again too early."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _check(fn, code):
     if code != MOE_OK:
         raise MoeError(fn, code)
@@ -525,7 +539,7 @@ class ExpandedMoE:
                  out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty((self.rows, self.H), dtype=torch.bfloat16, device=x.device)
+            out = _output(stream, (self.rows, self.H), torch.bfloat16, x.device)
         self.layout(x, x_scale, topk_ids, topk_weights, psum_recv_per_rank, stream)
         self.experts(stream)
         self.gather(topk_weights, psum_recv_per_rank, out, stream)
@@ -565,7 +579,7 @@ class StandardMoE(ExpandedMoE):
                  stream=None):
         import torch
         if out is None:
-            out = torch.empty((self.rows, self.H), dtype=torch.bfloat16, device=x.device)
+            out = _output(stream, (self.rows, self.H), torch.bfloat16, x.device)
         self.layout(x, topk_ids, topk_weights, psum_recv_per_rank, stream)
         self.experts(stream)
         self.gather(topk_weights, psum_recv_per_rank, out, stream)
@@ -663,7 +677,7 @@ class StandardBf16MoE:
                  stream=None):
         import torch
         if out is None:
-            out = torch.empty((self.rows, self.H), dtype=torch.bfloat16, device=x.device)
+            out = _output(stream, (self.rows, self.H), torch.bfloat16, x.device)
         self.layout(x, topk_ids, topk_weights, psum_recv_per_rank, stream)
         self.experts(stream)
         self.gather(topk_weights, psum_recv_per_rank, out, stream)
@@ -718,10 +732,9 @@ class TrainableBf16MoE(StandardBf16MoE):
         what they hold with accumulate."""
         import torch
         if dx is None:
-            dx = torch.empty((self.rows, self.H), dtype=torch.bfloat16, device=dout.device)
+            dx = _output(stream, (self.rows, self.H), torch.bfloat16, dout.device)
         if d_topk_weights is None:
-            d_topk_weights = torch.empty((self.rows, self.topk), dtype=torch.float32,
-                                         device=dout.device)
+            d_topk_weights = _output(stream, (self.rows, self.topk), torch.float32, dout.device)
         lay = (self.psum, self.status, self.align)
         moe_gather_backward(dout, self.down, self.src2dst, topk_weights, psum_recv_per_rank,
                             self.d_rows, d_topk_weights, stream,

@@ -49,3 +49,26 @@ def test_the_default_stream_by_its_handle():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def pool_of(t):
+    """The stream whose memory a tensor has."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_outputs_on_another_stream():
+    """Outputs that the calls allocate are memory of the stream that writes them."""
+    w13, w2, *rest = weights(6)
+    mod = M.TrainableBf16MoE(ROWS, TOPK, w13.clone(), w2.clone(), align=16)
+    want = [t.clone() for t in step(mod, *rest)]
+    mod = M.TrainableBf16MoE(ROWS, TOPK, w13.clone(), w2.clone(), align=16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = step(mod, *rest, stream=s.cuda_stream)
+    for t in got[:3]:
+        assert pool_of(t) == s.cuda_stream
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -26,6 +26,7 @@ def streams(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", enter)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle or POOL)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
     return now
 
 
@@ -57,3 +58,44 @@ def test_update_counts_on_the_stream_of_its_step(streams, monkeypatch, stream, w
     mod.update(stream=stream)
     assert calls == [stream] and mod.step.value == 1
     assert mod.step.on == [where]
+
+
+class Output:
+    """Stands in for a tensor: the stream whose memory it has, and its users."""
+
+    def __init__(self, on):
+        self.on, self.users = on, [on]
+
+    def record_stream(self, stream):
+        self.users.append(stream)
+
+
+class Tokens:
+    device = "cuda"
+
+
+@pytest.mark.parametrize("stream", [None, 0, 7, 4096])
+@pytest.mark.parametrize("cls", [M.ExpandedMoE, M.StandardMoE, M.MaskedMoE, M.StandardBf16MoE,
+                                 M.TrainableBf16MoE])
+def test_outputs_are_of_the_stream_that_writes_them(streams, monkeypatch, cls, stream):
+    """What a class allocates for a call on another stream is that stream's
+    memory, and the current stream is a user of it."""
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: Output(streams[-1]))
+    for name in dir(M):
+        if name.startswith("moe_") and callable(getattr(M, name)):
+            monkeypatch.setattr(M, name, lambda *a, **kw: None)
+    mod = object.__new__(cls)
+    mod.rows, mod.H, mod.topk, mod.fmt = 4, 128, 2, "f32"
+    for step in ("layout", "experts", "gather"):
+        monkeypatch.setattr(cls, step, lambda self, *a: None)
+    streams.append(7)                                       # the current one
+    args = (None,) * (3 if issubclass(cls, M.ExpandedMoE) and cls is not M.StandardMoE else 2)
+    got = [mod(Tokens, *args, stream=stream)]
+    if cls is M.TrainableBf16MoE:
+        for name in ("psum status align src2dst down d_rows y dw2 wgrad_workspace w2 d_y gate_up "
+                     "m_indices E d_gate_up ex dw13 w13 routed_scaling_factor").split():
+            setattr(mod, name, None)
+        got += mod.backward(Tokens, None, stream=stream)
+    for t in got:
+        assert t.on == (7 if stream is None else stream)
+        assert 7 in t.users

@@ -307,7 +307,7 @@ extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors
     const uintptr_t a = (uintptr_t)tensors[i].master, an = (uintptr_t)tensors[i].numel * 4;
     for (int j = 0; j < i && a < hi && lo < a + an; ++j) {
       const uintptr_t c = (uintptr_t)tensors[j].master, cn = (uintptr_t)tensors[j].numel * 4;
-      if (a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
+      if (cn && a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
     }
     lo = a < lo ? a : lo;
     hi = a + an > hi ? a + an : hi;

@@ -150,6 +150,30 @@ def test_adamw_rejects_bad_arguments():
     assert _adamw(tensors=[dict(t, numel=0) for t in far]) == M.MOE_OK
 
 
+# A list that passes every check is launched, and without a GPU the launch fails.
+PASSES = M.MOE_ERR_LAUNCH
+
+
+def _entry(i, **kw):
+    """Tensor i of 1000 values, with arrays of its own."""
+    at = lambda j: 0x10000000 * (i + 1) + 0x100000 * j  # noqa: E731
+    a = dict(master=at(0), grad=at(1), m=at(2), v=at(3), param=None, m_scale=None, v_scale=None,
+             numel=1000, grad_fmt=0, state_fmt=0)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: never launched")
+def test_adamw_passes_over_empty_tensors():
+    """An empty tensor overlaps nothing, wherever its pointer lies."""
+    last = _entry(1)
+    empty = _entry(7, master=last["master"] + 16, numel=0)
+    far = [_entry(0), _entry(5)]
+    assert _adamw(tensors=far + [empty, last]) == PASSES
+    assert _adamw(tensors=far + [last, empty]) == PASSES
+    assert _adamw(tensors=far + [last]) == PASSES
+
+
 def test_header_matches_the_struct():
     assert ctypes.sizeof(M._AdamWTensor) == 72
 

@@ -21,6 +21,10 @@
 // of 128 is 32 lanes.  354M values with 8-bit states take 1015 us, 5.6 TB/s;
 // 100M with fp32 states 463 us, 6.0 TB/s (with accesses through the caches
 // 1110 and 527).
+#include <stdlib.h>
+
+#include <algorithm>
+
 #include "lds_dma.hpp"
 
 // Each operation rounded by itself: plain operators under this pragma (the
@@ -280,6 +284,62 @@ moe_status check_tensor(const moe_adamw_tensor& t) {
   return MOE_OK;
 }
 
+// Memory that a call reads or writes.
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+
+// MOE_OK if no array that the call writes shares memory with another that it
+// reads or writes: two updates of one value would race.  Sorted by their
+// begins, a range overlaps an earlier one if it begins below the furthest end
+// so far.  (On the host, per call: 0.25 us for six tensors with fp32 states, 4 us
+// for 75 with 8-bit ones.)
+moe_status check_apart(const moe_adamw_tensor* tensors, int num_tensors, const int64_t* step,
+                       const float* lr, const float* grad_scale) {
+  constexpr int kScalars = 3, kArrays = 7, kFew = 32;
+  Range few[kScalars + kArrays * kFew];
+  Range* all = few;
+  if (num_tensors > kFew) {
+    all = (Range*)malloc((kScalars + kArrays * (size_t)num_tensors) * sizeof(Range));
+    if (!all) return MOE_ERR_LAUNCH;
+  }
+  size_t n = 0;
+  auto add = [&](const void* p, int64_t bytes, bool written) {
+    if (p) all[n++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written};
+  };
+  add(step, 8, false);
+  add(lr, 4, false);
+  add(grad_scale, 4, false);
+  for (int i = 0; i < num_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.numel == 0) continue;
+    const bool fp8 = t.state_fmt == MOE_STATE_FP8;
+    const int64_t state = t.numel * (fp8 ? 1 : 4);
+    add(t.master, t.numel * 4, true);
+    add(t.grad, t.numel * (t.grad_fmt == MOE_GRAD_F32 ? 4 : 2), false);
+    add(t.m, state, true);
+    add(t.v, state, true);
+    add(t.param, t.numel * 2, true);
+    if (fp8) {
+      const int64_t scales = (t.numel + MOE_STATE_GROUP - 1) / MOE_STATE_GROUP * 4;
+      add(t.m_scale, scales, true);
+      add(t.v_scale, scales, true);
+    }
+  }
+  std::sort(all, all + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end = 0, end_written = 0;  // the furthest of all, of the written ones
+  bool apart = true;
+  for (size_t i = 0; i < n && apart; ++i) {
+    const Range& r = all[i];
+    apart = r.begin >= (r.written ? end : end_written);
+    end = std::max(end, r.end);
+    if (r.written) end_written = std::max(end_written, r.end);
+  }
+  if (all != few) free(all);
+  return apart ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -297,21 +357,12 @@ extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors
   if (!step || !lr || (num_tensors > 0 && !tensors)) return MOE_ERR_NULL;
   if (((uintptr_t)step % 8) || ((uintptr_t)lr % 4) || ((uintptr_t)grad_scale % 4))
     return MOE_ERR_ALIGNMENT;
-  // Two updates of one value would race.  A tensor beyond the range of all
-  // earlier ones (the usual order of allocations) needs no look at each.
-  uintptr_t lo = UINTPTR_MAX, hi = 0;
   for (int i = 0; i < num_tensors; ++i) {
     const moe_status s = check_tensor(tensors[i]);
     if (s != MOE_OK) return s;
-    if (tensors[i].numel == 0) continue;
-    const uintptr_t a = (uintptr_t)tensors[i].master, an = (uintptr_t)tensors[i].numel * 4;
-    for (int j = 0; j < i && a < hi && lo < a + an; ++j) {
-      const uintptr_t c = (uintptr_t)tensors[j].master, cn = (uintptr_t)tensors[j].numel * 4;
-      if (cn && a < c + cn && c < a + an) return MOE_ERR_UNSUPPORTED;
-    }
-    lo = a < lo ? a : lo;
-    hi = a + an > hi ? a + an : hi;
   }
+  const moe_status apart = check_apart(tensors, num_tensors, step, lr, grad_scale);
+  if (apart != MOE_OK) return apart;
   const Hyper h = {beta1, beta2, (float)beta1, (float)(1.0 - beta1), (float)beta2,
                    (float)(1.0 - beta2), (float)eps, (float)weight_decay};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

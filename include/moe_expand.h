@@ -603,8 +603,10 @@ typedef struct {
  * The last group of a tensor may be short.
  * Errors: numel < 0 or > 2^33, num_tensors < 0, hyperparameters
  * out of range (beta in [0, 1), eps >= 0, weight_decay >= 0, all finite):
- * MOE_ERR_SHAPE; unknown formats, or masters that overlap:
- * MOE_ERR_UNSUPPORTED.  Tensors with numel 0 are skipped.
+ * MOE_ERR_SHAPE; unknown formats, or an array that is written (master, m, v,
+ * param, the scales) and shares memory with any other of the call's arrays or
+ * scalars: MOE_ERR_UNSUPPORTED.  Gradients may be shared.  Tensors with numel
+ * 0 are skipped.
  */
 moe_status moe_adamw(
     const moe_adamw_tensor* tensors, int num_tensors, const int64_t* step,

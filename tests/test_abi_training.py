@@ -174,6 +174,46 @@ def test_adamw_passes_over_empty_tensors():
     assert _adamw(tensors=far + [last]) == PASSES
 
 
+def _coded(i, **kw):
+    """The same with a bf16 copy and 8-bit states: 1000 codes, 8 scales each."""
+    base = 0x10000000 * (i + 1)
+    a = dict(param=base + 0x400000, m_scale=base + 0x500000, v_scale=base + 0x600000, state_fmt=1)
+    a.update(kw)
+    return _entry(i, **a)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: never launched")
+def test_adamw_keeps_written_arrays_apart():
+    """Any two arrays of a call of which one is written, within a tensor and
+    between two, by their last byte and by their first."""
+    assert _adamw(tensors=[_coded(0), _entry(1), _coded(2)]) == PASSES
+    size = dict(master=4000, grad=2000, m=1000, v=1000, param=2000, m_scale=32, v_scale=32)
+    for a in size:
+        for b in size:
+            for other in (0, 1):
+                if (a, 0) == (b, other):
+                    continue
+                one = _coded(0)
+                # Arrays begin at multiples of 16.
+                for at in (one[a], (one[a] + size[a] - 1) // 16 * 16):
+                    two = [dict(one), _coded(1)]
+                    two[other][b] = at
+                    want = PASSES if a == b == "grad" else M.MOE_ERR_UNSUPPORTED
+                    assert _adamw(tensors=two) == want, (a, b, other)
+                two = [dict(one), _coded(1)]
+                two[other][b] = -(-(one[a] + size[a]) // 16) * 16       # right behind it
+                assert _adamw(tensors=two) == PASSES, (a, b, other)
+    one = _entry(0)
+    for scalar in ("step", "lr", "gs"):
+        for a in ("master", "m", "v"):
+            assert _adamw(tensors=[one], **{scalar: one[a] + 8}) == M.MOE_ERR_UNSUPPORTED
+        assert _adamw(tensors=[one], **{scalar: one["grad"] + 8}) == PASSES
+    many = [_coded(i) for i in range(90)]
+    assert _adamw(tensors=many) == PASSES
+    many[80]["v_scale"] = many[3]["param"] + 16
+    assert _adamw(tensors=many) == M.MOE_ERR_UNSUPPORTED
+
+
 def test_header_matches_the_struct():
     assert ctypes.sizeof(M._AdamWTensor) == 72
 

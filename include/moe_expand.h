@@ -600,6 +600,15 @@ typedef struct {
  * a positive r gets at least the smallest positive code (2^-9), since a second
  * moment of 0 would let the step divide by eps alone.  The step itself uses m and v
  * before they are coded.  An infinite value spoils its group.
+ * A state whose beta is above 31/32 moves by far less than the codes' distance
+ * (6 to 12 %) in a step and would keep its nearest code for good.  It gets one
+ * of its two neighbouring codes instead, the expected one being its value: with
+ * 32-bit h = (m_bits ^ rotl(r_bits, 11)) * 0x9e3779b9 + t * 0xbb67ae85,
+ * h = (h ^ h >> 16) * 0x9e3779b9, h = (h ^ h >> 15) * 0x6a09e667, h ^= h >> 16,
+ * the upper (m) or lower (r) 20 bits of h, as a fraction of the distance, are
+ * added to the magnitude before it is cut off to a code.  Equal calls give equal
+ * codes.  A single root is then off by 15 to 20 % in the mean square (nearest
+ * codes at smaller betas: 8 %), without a bias.
  * The last group of a tensor may be short.
  * Errors: numel < 0 or > 2^33, num_tensors < 0, hyperparameters
  * out of range (beta in [0, 1), eps >= 0, weight_decay >= 0, all finite):

@@ -106,9 +106,32 @@ def layer_backward(x, ids, w, w13, w2, f, num_valid, dout):
     return dx, dw, dw13, dw2
 
 
-def encode_state(x, positive):
+def dither_bits(m, r, t):
+    """(20 bits for m's codes, 20 bits for r's) of each element at step t."""
+    u = lambda a: np.ascontiguousarray(a, F32).view(np.uint32)  # noqa: E731
+    c = np.uint32
+    step = np.array([t], np.int64).astype(np.uint32)
+    h = (u(m) ^ (u(r) << c(11) | u(r) >> c(21))) * c(0x9e3779b9) + step * c(0xbb67ae85)
+    h = (h ^ h >> c(16)) * c(0x9e3779b9)
+    h = (h ^ h >> c(15)) * c(0x6a09e667)
+    h = h ^ h >> c(16)
+    return h >> c(12), h & c(0xfffff)
+
+
+def to_neighbour(q, bits):
+    """fp32 q to one of its two neighbouring e4m3 values, by 20 bits each."""
+    a = np.abs(q)
+    low = a < F32(2.0 ** -6)
+    t = np.where(low, a + F32(2.0 ** -6), a).astype(F32)
+    t = ((t.view(np.uint32) + bits) & np.uint32(0xfff00000)).view(F32)
+    t = np.where(low, t - F32(2.0 ** -6), t)
+    return np.where(a <= F32(448), np.copysign(t, q), q).astype(F32)
+
+
+def encode_state(x, positive, bits=None):
     """Codes and scales of fp32 values x, in the order of the fp32 operations:
-    scale = amax * fl(1/448), code = rne(x * (fl(1/amax) * 448))."""
+    scale = amax * fl(1/448), code = rne(x * (fl(1/amax) * 448)), or one of the
+    neighbouring codes by `bits`."""
     n = x.size
     g = np.zeros(-(-n // 128) * 128, F32)
     g[:n] = x
@@ -118,7 +141,8 @@ def encode_state(x, positive):
     q = g * inv[:, None]
     if positive:
         q = np.where(g > 0, np.maximum(q, F32(2.0 ** -9)), q)
-    codes = fp8.encode_e4m3(q.astype(F32).reshape(-1)[:n])
+    q = q.astype(F32).reshape(-1)[:n]
+    codes = fp8.encode_e4m3(q if bits is None else to_neighbour(q, bits))
     return codes, (amax * (F32(1.0) / F32(448.0))).astype(F32)
 
 

@@ -36,6 +36,7 @@
 // of 128 is 32 lanes.  354M values with 8-bit states take 1015 us, 5.6 TB/s;
 // 100M with fp32 states 463 us, 6.0 TB/s (with accesses through the caches
 // 1110 and 527).
+#include <float.h>
 #include <stdlib.h>
 
 #include <algorithm>
@@ -97,7 +98,9 @@ struct Step {
 // takes them with one reciprocal and two products where the formula has three
 // quotients and another root: a few fp32 steps off the update, which moves
 // the master by far less than its own last rounding does.  (The reciprocal's
-// argument is normal: the root of any positive fp32 value is at least 2^-75.)
+// argument is normal or 0: the root of any positive fp32 value is at least 2^-75,
+// and an eps below the normal range is refused; the reciprocal of one would be
+// infinite.)
 __device__ __forceinline__ void update(const Hyper& h, const Step& st, float grad, float& p,
                                        float& m, float& v, float& r) {
   const float g = grad * st.gs;
@@ -416,6 +419,7 @@ extern "C" moe_status moe_adamw(const moe_adamw_tensor* tensors, int num_tensors
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
       !(eps >= 0.0 && eps <= 3.4e38) || !(weight_decay >= 0.0 && weight_decay <= 3.4e38))
     return MOE_ERR_SHAPE;
+  if (eps > 0.0 && (float)eps < FLT_MIN) return MOE_ERR_SHAPE;
   if (!step || !lr || (num_tensors > 0 && !tensors)) return MOE_ERR_NULL;
   if (((uintptr_t)step % 8) || ((uintptr_t)lr % 4) || ((uintptr_t)grad_scale % 4))
     return MOE_ERR_ALIGNMENT;

@@ -611,7 +611,8 @@ typedef struct {
  * codes at smaller betas: 8 %), without a bias.
  * The last group of a tensor may be short.
  * Errors: numel < 0 or > 2^33, num_tensors < 0, hyperparameters
- * out of range (beta in [0, 1), eps >= 0, weight_decay >= 0, all finite):
+ * out of range (beta in [0, 1), eps 0 or at least 2^-126, weight_decay >= 0,
+ * all finite):
  * MOE_ERR_SHAPE; unknown formats, or an array that is written (master, m, v,
  * param, the scales) and shares memory with any other of the call's arrays or
  * scalars: MOE_ERR_UNSUPPORTED.  Gradients may be shared.  Tensors with numel

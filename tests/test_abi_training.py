@@ -214,6 +214,16 @@ def test_adamw_keeps_written_arrays_apart():
     assert _adamw(tensors=many) == M.MOE_ERR_UNSUPPORTED
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: never launched")
+def test_adamw_takes_no_eps_below_the_normal_range():
+    """The step divides by eps alone where v is 0: 0 gives what 0 gives, and any
+    other eps is a normal fp32 number."""
+    for eps in (5e-324, 1e-46, 1e-45, 1e-40, 2.0 ** -126 * (1 - 2.0 ** -20)):
+        assert _adamw(tensors=[_entry(0)], eps=eps) == M.MOE_ERR_SHAPE, eps
+    for eps in (0.0, 2.0 ** -126, 1e-30, 1.0):
+        assert _adamw(tensors=[_entry(0)], eps=eps) == PASSES, eps
+
+
 def test_header_matches_the_struct():
     assert ctypes.sizeof(M._AdamWTensor) == 72
 

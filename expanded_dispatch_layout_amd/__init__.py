@@ -436,13 +436,15 @@ class AdamWTensors:
     fp32; grad bf16 or fp32; param a bf16 copy of master, or None; m and v
     fp32 with scales None, or 8-bit codes (torch.float8_e4m3fn or uint8) with
     fp32 scales, one per group of MOE_STATE_GROUP values.  All contiguous, of
-    one size.  The list keeps the tensors alive."""
+    one size, on the GPU that is current now and at every step.  The list keeps
+    the tensors alive; it does not see one whose storage is exchanged."""
 
     def __init__(self, entries):
         import torch
         fn, f32, bf = "AdamWTensors", torch.float32, torch.bfloat16
         codes = (torch.float8_e4m3fn, torch.uint8)
         self.entries = [tuple(e) for e in entries]
+        self.device = self.entries[0][0].get_device() if self.entries else None
         self.array = (_AdamWTensor * max(len(self.entries), 1))()
         for i, (master, grad, m, v, param, ms, vs) in enumerate(self.entries):
             shape, n = master.shape, master.numel()
@@ -470,6 +472,9 @@ def moe_adamw(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=
     fn = "moe_adamw"
     _need(fn, ("step", step, torch.int64, (1,)), ("lr", lr, torch.float32, (1,)),
           ("grad_scale", grad_scale, torch.float32, (1,)))
+    if tensors.device not in (None, step.get_device()):
+        raise ValueError(f"{fn}: the list's tensors are on GPU {tensors.device}, "
+                         f"not on the current GPU")
     code = lib().moe_adamw(tensors.array, len(tensors.entries), _ptr(step), _ptr(lr),
                            _ptr(grad_scale), beta1, beta2, eps, weight_decay, _stream(stream))
     _check(fn, code)

@@ -99,3 +99,41 @@ def test_outputs_are_of_the_stream_that_writes_them(streams, monkeypatch, cls, s
     for t in got:
         assert t.on == (7 if stream is None else stream)
         assert 7 in t.users
+
+
+class OnGpu:
+    """Stands in for a contiguous tensor on a GPU."""
+
+    def __init__(self, gpu, dtype, *shape):
+        self.gpu, self.dtype, self.shape = gpu, dtype, torch.Size(shape)
+
+    def get_device(self):
+        return self.gpu
+
+    device = property(lambda self: f"cuda:{self.gpu}")
+    numel = lambda self: self.shape.numel()  # noqa: E731
+    is_contiguous = lambda self: True  # noqa: E731
+    data_ptr = lambda self: 0x1000  # noqa: E731
+
+
+def test_adamw_refuses_a_list_of_another_gpu(monkeypatch):
+    """Made while GPU 0 was current and used while GPU 1 is, with that one's step
+    and rate: the kernel would run on GPU 1 on memory that is not its own."""
+    current, calls = [0], []
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[-1], raising=False)
+
+    class Library:
+        moe_adamw = staticmethod(lambda *a: calls.append(a) or M.MOE_OK)
+
+    monkeypatch.setattr(M, "lib", lambda: Library)
+    f32 = lambda gpu, n: OnGpu(gpu, torch.float32, n)  # noqa: E731
+    ts = M.AdamWTensors([(f32(0, 5), f32(0, 5), f32(0, 5), f32(0, 5), None, None, None)])
+    scalars = lambda gpu: (OnGpu(gpu, torch.int64, 1), f32(gpu, 1))  # noqa: E731
+    M.moe_adamw(ts, *scalars(0), stream=4096)
+    assert len(calls) == 1
+    current.append(1)
+    with pytest.raises(ValueError, match="not on the current GPU"):
+        M.moe_adamw(ts, *scalars(1), stream=4096)
+    assert len(calls) == 1
+    M.moe_adamw(M.AdamWTensors([]), *scalars(1), stream=4096)      # nothing to be elsewhere

@@ -758,8 +758,14 @@ class TrainableBf16MoE(StandardBf16MoE):
     def update(self, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=None,
                stream=None):
         """One AdamW step on both weights with the gradients in dw13 and dw2 and
-        the learning rate in the lr tensor; counts step up first."""
+        the learning rate in the lr tensor; counts step up first.  A call that is
+        refused leaves the count as it was."""
         with _on(stream):
             self.step.add_(1)
-        moe_adamw(self.tensors, self.step, self.lr, beta1, beta2, eps, weight_decay, grad_scale,
-                  stream)
+        try:
+            moe_adamw(self.tensors, self.step, self.lr, beta1, beta2, eps, weight_decay,
+                      grad_scale, stream)
+        except Exception:
+            with _on(stream):
+                self.step.sub_(1)
+            raise

@@ -72,3 +72,46 @@ def test_outputs_on_another_stream():
     torch.cuda.current_stream().wait_stream(s)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_a_refused_update_does_not_count():
+    w13, w2, *rest = weights(7)
+    mod = M.TrainableBf16MoE(ROWS, TOPK, w13, w2, align=16)
+    step(mod, *rest)
+    before = [t.clone() for t in (mod.step, mod.master13, mod.master2)]
+    with pytest.raises(M.MoeError):
+        mod.update(beta1=1.0)
+    with pytest.raises(ValueError):
+        mod.update(grad_scale=torch.ones(2, device="cuda"))
+    with pytest.raises(M.MoeError):
+        mod.update(eps=1e-40, stream=0)
+    for a, b in zip((mod.step, mod.master13, mod.master2), before):
+        assert torch.equal(a, b)
+
+
+def test_captured_with_the_handle_of_its_stream():
+    """The outputs that the calls allocate lie in the graph's memory; replays
+    with eager steps of the program between them equal eager steps."""
+    w13, w2, *rest = weights(8)
+    new = lambda: M.TrainableBf16MoE(ROWS, TOPK, w13.clone(), w2.clone(), align=16)  # noqa: E731
+    eager, want = new(), []
+    for _ in range(4):
+        want.append([t.clone() for t in step(eager, *rest)])
+    mod, s, g = new(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        first = [t.clone() for t in step(mod, *rest, stream=s.cuda_stream)]     # eager
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            res = step(mod, *rest, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(first, want[0]):
+        assert torch.equal(a, b)
+    for rep in (1, 2, 3):
+        junk = [torch.full_like(t, 9) for t in res[:3]]                  # other work
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, want[rep]):
+            assert torch.equal(a, b), rep
+        del junk

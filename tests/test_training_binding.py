@@ -40,6 +40,9 @@ class Counter:
         self.value += n
         self.on.append(self.now[-1])
 
+    def sub_(self, n):
+        self.add_(-n)
+
 
 def trainable(now):
     mod = object.__new__(M.TrainableBf16MoE)
@@ -137,3 +140,16 @@ def test_adamw_refuses_a_list_of_another_gpu(monkeypatch):
         M.moe_adamw(ts, *scalars(1), stream=4096)
     assert len(calls) == 1
     M.moe_adamw(M.AdamWTensors([]), *scalars(1), stream=4096)      # nothing to be elsewhere
+
+
+@pytest.mark.parametrize("stream", [None, 0, 4096])
+def test_a_refused_update_does_not_count(streams, monkeypatch, stream):
+    def refuse(*a):
+        raise M.MoeError("moe_adamw", M.MOE_ERR_SHAPE)
+
+    monkeypatch.setattr(M, "moe_adamw", refuse)
+    mod = trainable(streams)
+    with pytest.raises(M.MoeError):
+        mod.update(beta1=1.0, stream=stream)
+    assert mod.step.value == 0
+    assert set(mod.step.on) == {stream or 0}

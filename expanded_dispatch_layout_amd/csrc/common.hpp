@@ -78,6 +78,12 @@ __device__ __forceinline__ uint32_t e8m0_round_up(float s) {
   return ex + (bump ? 1u : 0u);
 }
 
+// Do n bytes at p and m bytes at q share memory?  (Nothing lies at NULL.)
+inline bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
+}
+
 // Compute units of the current device (256 if it cannot be asked).
 inline int device_cus() {
   static int cus[64] = {0};

@@ -379,6 +379,10 @@ extern "C" moe_status moe_grouped_dgrad_bf16(const void* dy, const void* w, cons
   if (((uintptr_t)dy % 16) || ((uintptr_t)w % 16) || ((uintptr_t)dx % 16))
     return MOE_ERR_ALIGNMENT;
   if (capacity == 0) return MOE_OK;
+  const int64_t out = capacity * k * 2;
+  if (overlap(dx, out, dy, capacity * n * 2) ||
+      overlap(dx, out, w, (int64_t)num_experts * n * k * 2))
+    return MOE_ERR_UNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (expected_tiles(capacity, k, num_experts, align, kNarrowTile) <= kFull)
     return launch_dgrad_narrow(dy, w, psum, status, capacity, n, k, num_experts, align, dx, st);

@@ -96,6 +96,17 @@ extern "C" moe_status moe_gather_backward(const void* dout, const void* expert_o
     return MOE_ERR_ALIGNMENT;
   if (hidden > 8192) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
+  const int64_t out = capacity * hidden * 2, weights = rows * topk * 4;
+  if (overlap(d_expert_out, out, dout, rows * hidden * 2) ||
+      overlap(d_expert_out, out, d_topk_weights ? expert_out : nullptr, out) ||
+      overlap(d_expert_out, out, src2dst, weights) ||
+      overlap(d_expert_out, out, topk_weights, weights) ||
+      overlap(d_topk_weights, weights, dout, rows * hidden * 2) ||
+      overlap(d_topk_weights, weights, expert_out, out) ||
+      overlap(d_topk_weights, weights, d_expert_out, out) ||
+      overlap(d_topk_weights, weights, src2dst, weights) ||
+      overlap(d_topk_weights, weights, topk_weights, weights))
+    return MOE_ERR_UNSUPPORTED;
   const int64_t blocks = (rows * topk + kWaves - 1) / kWaves;
   const int64_t grid = blocks < 65536 ? blocks : 65536;  // grid-stride over the rest
   auto kern = d_topk_weights ? gather_backward_kernel<true> : gather_backward_kernel<false>;

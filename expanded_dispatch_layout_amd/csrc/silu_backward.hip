@@ -93,6 +93,10 @@ extern "C" moe_status moe_silu_mul_bf16_backward(const void* gate_up, const void
   if (((uintptr_t)gate_up % 16) || ((uintptr_t)dy % 16) || ((uintptr_t)d_gate_up % 16))
     return MOE_ERR_ALIGNMENT;
   if (capacity == 0) return MOE_OK;
+  const int64_t row = capacity * (int64_t)inter * 2;
+  if ((d_gate_up != gate_up && overlap(d_gate_up, 2 * row, gate_up, 2 * row)) ||
+      overlap(d_gate_up, 2 * row, dy, row))
+    return MOE_ERR_UNSUPPORTED;
   int row_shift = 0;  // threads per row: a power of two that covers the row, at most all
   while ((8 << row_shift) < inter && (1 << row_shift) < kThreads) ++row_shift;
   const int64_t rows_per_block = kThreads >> row_shift;

@@ -464,6 +464,12 @@ extern "C" moe_status moe_grouped_wgrad_bf16(const void* dy, const void* x, cons
       return MOE_ERR_WORKSPACE;
     if ((uintptr_t)workspace % 256) return MOE_ERR_ALIGNMENT;
   }
+  const int64_t a = capacity * n * 2, b = capacity * k * 2;
+  const int64_t out = (int64_t)num_experts * n * k * (fmt == MOE_GRAD_F32 ? 4 : 2);
+  const int64_t part = splits > 1 ? (int64_t)splits * num_experts * n * k * 4 : 0;
+  if (overlap(dw, out, dy, a) || overlap(dw, out, x, b) || overlap(dw, out, workspace, part) ||
+      overlap(workspace, part, dy, a) || overlap(workspace, part, x, b))
+    return MOE_ERR_UNSUPPORTED;
   const int tile = tile_of(capacity, n, k, num_experts);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (tile == 64)

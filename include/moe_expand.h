@@ -79,9 +79,9 @@
  *
  * Conventions for every call:
  *  - Pointers named as device buffers are device memory the caller owns
- *    (allocated, e.g., by PyTorch).  The library never allocates, frees,
- *    copies between host and device, synchronises, or reads device data on
- *    the host.  `stream` is a hipStream_t (NULL = the default stream); work
+ *    (allocated, e.g., by PyTorch).  The library never allocates or frees
+ *    device memory, copies between host and device, synchronises, or reads
+ *    device data on the host.  `stream` is a hipStream_t (NULL = the default stream); work
  *    is enqueued asynchronously on it.
  *  - Host-detectable errors (null pointers, bad sizes, misaligned buffers,
  *    unsupported combinations) are returned as a moe_status before anything
@@ -103,6 +103,9 @@
  *    Weight scales are [E, N/128, K/128].
  *  - Calls are stateless and reentrant; calls that share output buffers
  *    must be ordered by the caller's streams.
+ *  - A buffer that a call writes shares no memory with another of its buffers
+ *    unless the call's comment allows it.  The training calls refuse it
+ *    (MOE_ERR_UNSUPPORTED).
  */
 #ifndef MOE_EXPAND_H
 #define MOE_EXPAND_H

@@ -224,6 +224,49 @@ def test_adamw_takes_no_eps_below_the_normal_range():
         assert _adamw(tensors=[_entry(0)], eps=eps) == PASSES, eps
 
 
+def _apart(call, size, outputs, allowed=()):
+    """Every output on every other buffer, at its first 16 bytes and at its last."""
+    base = {name: 0x10000000 * (i + 1) for i, name in enumerate(size)}
+    assert call(base) == PASSES
+    for out in outputs:
+        for other in size:
+            if other == out:
+                continue
+            for at in (base[other], base[other] + (size[other] - 1) // 256 * 256):
+                same = at == base[other]
+                want = PASSES if same and (out, other) in allowed else M.MOE_ERR_UNSUPPORTED
+                assert call({**base, out: at}) == want, (out, other, same)
+            behind = base[other] + -(-size[other] // 256) * 256
+            assert call({**base, out: behind}) == PASSES, (out, other)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: never launched")
+def test_outputs_share_no_memory_with_other_buffers():
+    L, ints = M.lib(), FAKE
+    cap, n, k, E, rows, topk = 320, 256, 256, 4, 64, 2
+    _apart(lambda p: L.moe_grouped_dgrad_bf16(p["dy"], p["w"], ints, ints, cap, n, k, E, 64,
+                                              p["dx"], None),
+           dict(dy=cap * n * 2, w=E * n * k * 2, dx=cap * k * 2), ["dx"])
+    cap, E = 20480, 1                                       # sums in parts: a workspace
+    for fmt, bytes_ in ((0, 2), (1, 4)):
+        need = M.moe_grouped_wgrad_workspace_bytes(cap, n, k, E)
+        assert need > 0
+        _apart(lambda p: L.moe_grouped_wgrad_bf16(p["dy"], p["x"], ints, ints, cap, n, k, E, 64,
+                                                  fmt, 0, p["dw"], p["ws"], need, None),
+               dict(dy=cap * n * 2, x=cap * k * 2, dw=E * n * k * bytes_, ws=need), ["dw", "ws"])
+    cap, E = 320, 4
+    _apart(lambda p: L.moe_silu_mul_bf16_backward(p["gu"], p["dy"], ints, ints, ints, cap, 128, E,
+                                                  64, p["out"], None),
+           dict(gu=cap * 512, dy=cap * 256, out=cap * 512), ["out"], [("out", "gu")])
+    _apart(lambda p: L.moe_gather_backward(p["dout"], p["eo"], p["s2d"], p["w"], 1.0, None, 0,
+                                           rows, n, topk, cap, p["deo"], p["dw"], None),
+           dict(dout=rows * n * 2, eo=cap * n * 2, s2d=rows * topk * 4, w=rows * topk * 4,
+                deo=cap * n * 2, dw=rows * topk * 4), ["deo", "dw"])
+    # Without d_topk_weights expert_out is not read: its place may be written.
+    assert L.moe_gather_backward(0x10000000, 0x20000000, 0x30000000, None, 1.0, None, 0, rows, n,
+                                 topk, cap, 0x20000000, None, None) == PASSES
+
+
 def test_header_matches_the_struct():
     assert ctypes.sizeof(M._AdamWTensor) == 72
 

@@ -696,7 +696,8 @@ class TrainableBf16MoE(StandardBf16MoE):
     rows, SiLU*up and the down rows in the object's buffers, and backward()
     reads them.  w13 and w2 are the bf16 copies that update() rewrites from
     the fp32 masters master13 and master2.  grad: 'f32' or 'bf16' weight
-    gradients (dw13, dw2); state: 'f32' or 'fp8' optimiser states."""
+    gradients (dw13, dw2); state: 'f32' or 'fp8' optimiser states.  The buffers
+    are made on the current stream: order a call on another one behind it."""
 
     def __init__(self, rows, topk, w13, w2, align=128, routed_scaling_factor=1.0,
                  grad="f32", state="f32", lr=1e-4, device="cuda"):
@@ -734,7 +735,8 @@ class TrainableBf16MoE(StandardBf16MoE):
         """Gradients of the last forward call (its topk_weights and
         psum_recv_per_rank): returns (dx [rows, H] bf16, d_topk_weights
         [rows, topk] fp32) and leaves the weights' in dw13 and dw2, added to
-        what they hold with accumulate."""
+        what they hold with accumulate.  Rows of dx and d_topk_weights at or past
+        the received ones are not written."""
         import torch
         if dx is None:
             dx = _output(stream, (self.rows, self.H), torch.bfloat16, dout.device)

@@ -63,6 +63,11 @@ inline int64_t expected_tiles(int64_t capacity, int k, int num_experts, int alig
 // 32; 512 rows, 2 x 7168 x 2048, 74 / 53 / 94; 8 rows, 8 x 4096 x 2048, 26 / 28 /
 // 59; more than one round of 128 x 128 tiles: 512 rows, 8 x 2048 x 1024, 43 / 36 /
 // 33; 128 rows, 8 x 4096 x 7168, 179 / 128 / 104.
+// A capacity far above the live rows (a layer class allocates topk rows for every
+// row received, of which an expert-parallel rank uses few) makes the rule expect
+// tiles that are not there, and take larger ones than the live rows want: 1024
+// rows, 8 x 2048 x 1024, 19.5 us in a buffer of 1920 rows, 32 in one of 33664; 8 x
+// 7168 x 2048, 81 and 121; 8 x 4096 x 7168, 106 in both.
 constexpr int64_t kFull = 256;
 
 // A row of dy is 8 chunks of 16 bytes, XOR-swizzled by row so that the 16
@@ -82,7 +87,8 @@ struct Item {
 // waves 0-3 compute in about half the time (18432 rows, 6144 x 2048: 454 ->
 // 420 us; 16384 rows, 2 x 2048 x 1024: 97 -> 83).  `whole` items come
 // first, then `count - whole` halves.
-// Items fit 32 bits: at most 2^22 + 2^10 row groups and 2^8 column tiles.
+// Items fit 32 bits: at most 2^22 + 2^10 row groups of 2^7 column tiles, twice that
+// many halves (256 x 256); 2^23 + 2^10 groups of 2^8 (128 x 128).
 struct Rounds {
   uint32_t whole, count;
   __device__ __forceinline__ Rounds(uint32_t items, uint32_t grid, bool halves) {

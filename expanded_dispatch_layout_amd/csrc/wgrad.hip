@@ -408,6 +408,9 @@ int64_t tiles_of(int n, int k, int num_experts, int t) {
 // where they are not, since fewer CUs wait for the longest: 1024 x 1024, eight,
 // 4096 rows even 17.9 / 18.4 us, 6400 rows of which 43 % are one expert's 40 / 62;
 // three rounds lose more (384 x 1728, fourteen, 5473 rows even 21.2 / 16.3).
+// The border in rows serves both; between it and about 8192 rows of one expert 64
+// would still be a little ahead.  Rows are those of a full buffer: see
+// wgrad_splits.
 constexpr int64_t kShortRows = 4608;
 int tile_of(int64_t capacity, int n, int k, int num_experts) {
   const int64_t rows = capacity / num_experts;
@@ -424,7 +427,9 @@ int tile_of(int64_t capacity, int n, int k, int num_experts) {
 // smallest is the root of their ratio.  Measured, one part against the rule's
 // choice and twice it: 20000 rows of one expert, 1024 x 1024, 390 / 60 / 62 us;
 // 16384 rows of two, 2048 x 1024, 170 / 79 / 79; 20000 rows of four, 2048 x 256,
-// 109 / 43 / 46.
+// 109 / 43 / 46.  The rows are the capacity's: sums are cut for rows that a larger
+// buffer does not hold (1024 live rows, 8 x 1024 x 1024, 12.9 us in a buffer of
+// 1920 rows, 32.5 with 64 MB of parts in one of 33664).
 int wgrad_splits(int64_t capacity, int n, int k, int num_experts) {
   if (tile_of(capacity, n, k, num_experts) < 256) return 1;
   const int64_t tiles = tiles_of(n, k, num_experts, 256), rows = capacity / num_experts;

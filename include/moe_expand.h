@@ -48,8 +48,10 @@
  *   moe_grouped_dgrad_bf16       d of the expanded rows
  *   moe_gather                   (weights NULL, factor 1) d of the tokens
  *   moe_adamw                    AdamW over all the weights at once
- * None of these reads or writes alignment pad rows or rows past the total,
- * so they may hold anything.  A captured sequence may be replayed on new
+ * Alignment pad rows and rows past the total may hold anything: they are
+ * never written, and what they hold enters no result.  Pad rows may be read
+ * (moe_silu_mul_bf16_backward loads every row below min(status[0], capacity)
+ * before it knows which ones are live).  A captured sequence may be replayed on new
  * routings: every row count, the step number and the learning rate are read
  * on the device.
  *

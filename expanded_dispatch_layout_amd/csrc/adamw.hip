@@ -24,8 +24,8 @@
 // nearest codes, 0.96 with these; 0.99, 7.7 and 0.99; 0.98, 1.8 and 0.99.  Up to
 // 0.97 the gradients' own noise carries states from code to code, and the
 // nearest ones stay closer: 0.96, 5th to 95th percentile 0.87 to 1.12 against
-// 0.83 to 1.21.  The hash costs 8 % with one state's codes chosen by it, 13 % with
-// both (354M values: 990, 1080 and 1135 us).
+// 0.83 to 1.21.  The hash costs 10 % with one state's codes chosen by it, 15 % with
+// both (354M values: 1000, 1100 and 1150 us).
 //
 // HBM-bound: everything is read once and written once, past the caches.  A
 // workgroup takes 1024 or 2048 values of one tensor; the list of tensors
@@ -33,8 +33,8 @@
 // kMaxTensors per launch.  Each lane owns 4 consecutive values, so that every
 // access of a wave is one contiguous run (8 per lane, in two pieces for the
 // fp32 arrays: 566 us against 527 at 100M values with fp32 states), and a group
-// of 128 is 32 lanes.  354M values with 8-bit states take 1015 us, 5.6 TB/s;
-// 100M with fp32 states 463 us, 6.0 TB/s (with accesses through the caches
+// of 128 is 32 lanes.  354M values with 8-bit states take 1000 us, 5.7 TB/s;
+// 100M with fp32 states 460 us, 6.1 TB/s (with accesses through the caches
 // 1110 and 527).
 #include <float.h>
 #include <stdlib.h>

@@ -18,9 +18,9 @@
 //    stream keeps its own depth (128 x 128: four stages of dy).  Both run ahead
 //    across tiles.  Rows that are not live are loaded from a chunk of zeros
 //    and cost no traffic; a wave whose rows hold none skips its MFMAs.
-//  - What it reaches: 106 us at one rank's share (1024 rows, 8 x 4096 x 7168:
-//    4.7 TB/s), 420 us at 18432 uneven rows of 6144 x 2048 (1.10 PFLOP/s) and
-//    800 at 4096 x 6144 (1.16; with zeros as inputs 649: power, as in
+//  - What it reaches: 105 us at one rank's share (1024 rows, 8 x 4096 x 7168:
+//    4.7 TB/s), 418 us at 18432 uneven rows of 6144 x 2048 (1.11 PFLOP/s) and
+//    806 at 4096 x 6144 (1.15; with zeros as inputs 649: power, as in
 //    wgrad.hip).
 #include "gemm_backward.hpp"
 

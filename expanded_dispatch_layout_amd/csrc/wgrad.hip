@@ -21,10 +21,10 @@
 //    enter a product, whatever they hold.
 //  - Fragments are double-buffered in registers: a step's 32 MFMAs run while
 //    the next one's 24 reads are under way, with one barrier per step.
-//  - What it reaches: 765 us at 18432 rows of 4096 x 6144 (1.21 PFLOP/s; the
-//    library's plain product of that layout and size takes 890), 114 us at one
-//    rank's share in bf16 and 378 accumulating in fp32 (1024 rows, 8 x 4096 x
-//    7168; 4.3 and 5.0 TB/s).  The large one is bound by power: with zeros as inputs
+//  - What it reaches: 766 us at 18432 rows of 4096 x 6144 (1.21 PFLOP/s; the
+//    library's plain product of that layout and size takes 890); at one rank's
+//    share (1024 rows, 8 x 4096 x 7168) 116 us writing bf16 and 211 adding to it,
+//    189 and 381 in fp32 (4.2 to 5.1 TB/s).  The large one is bound by power: with zeros as inputs
 //    the same instructions take 612 us.
 #include <math.h>
 

@@ -14,17 +14,22 @@ Functions mirror the C ABI in ``include/moe_expand.h``:
     moe_grouped_gemm_bf16, moe_silu_mul_bf16,
     moe_grouped_dgrad_bf16, moe_grouped_wgrad_bf16, moe_silu_mul_bf16_backward,
     moe_gather_backward, moe_adamw,
+    moe_layer_norm, moe_layer_norm_backward, moe_router, moe_router_backward,
+    moe_grouped_gemm_w4,
     moe_expand_capacity, moe_expand_workspace_bytes,
-    moe_grouped_wgrad_workspace_bytes, moe_status_string
+    moe_grouped_wgrad_workspace_bytes, moe_layer_norm_backward_workspace_bytes,
+    moe_status_string
 
 plus :class:`ExpandedMoE`, which allocates the buffers once for a given
 receive-buffer size and runs the five calls of a layer in order, and
 :class:`StandardMoE`, the same for the standard (non-EP) path: bf16 token
 rows in, top-k weights and the routed scaling factor applied in the gather,
 :class:`MaskedMoE`, the decode path on a fixed-height masked slab,
-:class:`StandardBf16MoE`, the standard path with bf16 weights, and
-:class:`TrainableBf16MoE`, that path with its backward pass and an AdamW step
-(:class:`AdamWTensors` lists the tensors of one).
+:class:`StandardBf16MoE`, the standard path with bf16 weights,
+:class:`StandardW4MoE`, the same with 4-bit weights,
+:class:`TrainableBf16MoE`, the bf16 path with its backward pass and an AdamW step
+(:class:`AdamWTensors` lists the tensors of one), and :class:`MoEBlock`, the
+norm, the gate and the router around one of the standard paths.
 """
 
 import ctypes
@@ -43,6 +48,13 @@ MOE_FLAG_CAPACITY_OVERFLOW, MOE_FLAG_EXPERT_ID_RANGE, MOE_FLAG_SLAB_OVERFLOW = 1
 MOE_GRAD_BF16, MOE_GRAD_F32 = 0, 1
 MOE_STATE_F32, MOE_STATE_FP8 = 0, 1
 MOE_STATE_GROUP = 128
+MOE_FLOAT_BF16, MOE_FLOAT_F32 = 0, 1
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_W4_INT4, MOE_W4_MXFP4 = 0, 1
+NORM = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
+SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+W4 = {"int4": MOE_W4_INT4, "mxfp4": MOE_W4_MXFP4}
 FMT = {"f32": MOE_SCALE_F32, "ue8m0": MOE_SCALE_UE8M0, "none": MOE_SCALE_NONE,
        "mxfp8": MOE_SCALE_MXFP8}
 
@@ -82,6 +94,15 @@ _SIGNATURES = {
     "moe_gather_backward": (_I, [_P, _P, _P, _P, ctypes.c_float, _P, _I, _I64, _I, _I, _I64,
                                  _P, _P, _P]),
     "moe_adamw": (_I, [_P, _I, _P, _P, _P, _D, _D, _D, _D, _P]),
+    "moe_layer_norm": (_I, [_P, _I64, _I, _P, _P, _P, _I, _I, ctypes.c_float, _P, _I, _I64, _I,
+                            _P, _P, _P, _P, _P]),
+    "moe_layer_norm_backward_workspace_bytes": (_SZ, [_I64, _I]),
+    "moe_layer_norm_backward": (_I, [_P, _P, _P, _I64, _I, _P, _I, _I, _P, _P, _P, _P, _I, _I64,
+                                     _I, _P, _P, _P, _I, _I, _P, _SZ, _P]),
+    "moe_router": (_I, [_P, _I64, _I, _P, _I, _I, _I, _I, _P, _I, _I64, _I, _I, _P, _P, _P]),
+    "moe_router_backward": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _I, _I64, _I, _I, _P, _I64,
+                                 _P]),
+    "moe_grouped_gemm_w4": (_I, [_P, _P, _P, _I, _I, _P, _P, _I64, _I, _I, _I, _I, _P, _P]),
 }
 
 _lib = None
@@ -480,6 +501,146 @@ def moe_adamw(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=
     _check(fn, code)
 
 
+def _need_rows(fn, name, t, dtypes, shape):
+    """A matrix of one of those types and that shape on the current GPU, whose
+    columns are contiguous (its rows may be apart).  Returns whether it is fp32,
+    and the elements from row to row."""
+    import torch
+    if t.dtype not in dtypes or t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be {' or '.join(map(str, dtypes))} of shape "
+                         f"{tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}")
+    row, col = t.stride()
+    if t.shape[1] > 1 and col != 1 and t.shape[0] > 0:
+        raise ValueError(f"{fn}: {name} must have contiguous rows")
+    if t.get_device() != (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2):
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
+    if t.shape[0] <= 1:
+        row = max(row, t.shape[1])   # the distance to a row that is not there
+    elif row < t.shape[1]:
+        raise ValueError(f"{fn}: {name} has rows that overlap")
+    return t.dtype == torch.float32, row
+
+
+def moe_layer_norm(x, weight, y, bias=None, branch=None, sum=None, mean=None, rstd=None,
+                   kind="layer", eps=1e-5, psum_recv_per_rank=None, stream=None):
+    """x [rows, H] bf16 or fp32 (rows may be apart), branch [rows, H] bf16 or None
+    -> sum [rows, H] of x's type (x + branch; may be x), y [rows, H] bf16, mean and
+    rstd [rows] fp32 (each may be None).  weight, bias [H] bf16 or fp32.  kind
+    'layer' or 'rms'."""
+    import torch
+    fn, bf, f32 = "moe_layer_norm", torch.bfloat16, torch.float32
+    rows, H = x.shape
+    x_f32, stride = _need_rows(fn, "x", x, (bf, f32), (rows, H))
+    nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
+    wdt = f32 if weight.dtype == f32 else bf
+    _need(fn, ("weight", weight, wdt, (H,)), ("bias", bias, wdt, (H,)), ("y", y, bf, (rows, H)),
+          ("branch", branch, bf, (rows, H)), ("sum", sum, x.dtype, (rows, H)),
+          ("mean", mean, f32, (rows,)), ("rstd", rstd, f32, (rows,)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+    code = lib().moe_layer_norm(
+        _ptr(x), stride, x_f32, _ptr(branch), _ptr(weight), _ptr(bias), wdt == f32, NORM[kind],
+        eps, _ptr(psum_recv_per_rank), nsrc, rows, H, _ptr(sum), _ptr(y), _ptr(mean), _ptr(rstd),
+        _stream(stream))
+    _check(fn, code)
+
+
+def moe_layer_norm_backward_workspace_bytes(rows, hidden) -> int:
+    return int(lib().moe_layer_norm_backward_workspace_bytes(rows, hidden))
+
+
+def moe_layer_norm_backward(dy, x, weight, rstd, dx, mean=None, dy2=None, dsum=None,
+                            dweight=None, dbias=None, accumulate=False, kind="layer",
+                            psum_recv_per_rank=None, workspace=None, stream=None):
+    """dy (and dy2) [rows, H] bf16, x [rows, H] as the forward call kept it (its sum)
+    -> dx [rows, H] of x's type, with dsum of that type added (dx may be dsum);
+    dweight, dbias [H] bf16 or fp32, added to what they hold with accumulate.
+    workspace: a uint8 tensor of at least moe_layer_norm_backward_workspace_bytes
+    (None without dweight and dbias)."""
+    import torch
+    fn, bf, f32 = "moe_layer_norm_backward", torch.bfloat16, torch.float32
+    rows, H = x.shape
+    x_f32, stride = _need_rows(fn, "x", x, (bf, f32), (rows, H))
+    nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
+    size = 0 if workspace is None else workspace.numel()
+    wdt = f32 if weight.dtype == f32 else bf
+    grad = dweight if dweight is not None else dbias
+    gdt = bf if grad is not None and grad.dtype == bf else f32
+    _need(fn, ("dy", dy, bf, (rows, H)), ("dy2", dy2, bf, (rows, H)),
+          ("weight", weight, wdt, (H,)), ("mean", mean, f32, (rows,)),
+          ("rstd", rstd, f32, (rows,)), ("dsum", dsum, x.dtype, (rows, H)),
+          ("dx", dx, x.dtype, (rows, H)), ("dweight", dweight, gdt, (H,)),
+          ("dbias", dbias, gdt, (H,)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)),
+          ("workspace", workspace, torch.uint8, (size,)))
+    code = lib().moe_layer_norm_backward(
+        _ptr(dy), _ptr(dy2), _ptr(x), stride, x_f32, _ptr(weight), wdt == f32, NORM[kind],
+        _ptr(mean), _ptr(rstd), _ptr(dsum), _ptr(psum_recv_per_rank), nsrc, rows, H, _ptr(dx),
+        _ptr(dweight), _ptr(dbias), MOE_GRAD_BF16 if gdt == bf else MOE_GRAD_F32,
+        bool(accumulate), _ptr(workspace), size, _stream(stream))
+    _check(fn, code)
+
+
+def moe_router(logits, topk_ids, topk_weights, bias=None, score="softmax", num_groups=1,
+               topk_groups=1, normalize=True, psum_recv_per_rank=None, stream=None):
+    """logits [rows, E] bf16 or fp32 (rows may be apart) -> topk_ids [rows, topk] int32 and
+    topk_weights [rows, topk] fp32; bias [E] fp32 or None.  score 'softmax' or
+    'sigmoid'."""
+    import torch
+    fn, f32 = "moe_router", torch.float32
+    rows, E = logits.shape
+    is_f32, stride = _need_rows(fn, "logits", logits, (torch.bfloat16, f32), (rows, E))
+    topk = topk_ids.shape[1]
+    nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
+    _need(fn, ("topk_ids", topk_ids, torch.int32, (rows, topk)),
+          ("topk_weights", topk_weights, f32, (rows, topk)), ("bias", bias, f32, (E,)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+    code = lib().moe_router(
+        _ptr(logits), stride, is_f32, _ptr(bias), SCORE[score], num_groups, topk_groups,
+        bool(normalize), _ptr(psum_recv_per_rank), nsrc, rows, E, topk, _ptr(topk_ids),
+        _ptr(topk_weights), _stream(stream))
+    _check(fn, code)
+
+
+def moe_router_backward(logits, topk_ids, d_topk_weights, d_logits, score="softmax",
+                        normalize=True, psum_recv_per_rank=None, stream=None):
+    """logits [rows, E] and topk_ids [rows, topk] of moe_router, d_topk_weights
+    [rows, topk] fp32 -> d_logits [rows, E] of the logits' type (rows may be apart)."""
+    import torch
+    fn = "moe_router_backward"
+    rows, E = logits.shape
+    is_f32, stride = _need_rows(fn, "logits", logits, (torch.bfloat16, torch.float32), (rows, E))
+    _, d_stride = _need_rows(fn, "d_logits", d_logits, (logits.dtype,), (rows, E))
+    topk = topk_ids.shape[1]
+    nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
+    _need(fn, ("topk_ids", topk_ids, torch.int32, (rows, topk)),
+          ("d_topk_weights", d_topk_weights, torch.float32, (rows, topk)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+    code = lib().moe_router_backward(
+        _ptr(logits), stride, is_f32, SCORE[score], bool(normalize), _ptr(topk_ids),
+        _ptr(d_topk_weights), _ptr(psum_recv_per_rank), nsrc, rows, E, topk, _ptr(d_logits),
+        d_stride, _stream(stream))
+    _check(fn, code)
+
+
+def moe_grouped_gemm_w4(a, w, w_scale, fmt, psum, status, align, out, stream=None):
+    """a [capacity, k] bf16, w [E, n, k/2] uint8 (two codes a byte, the lower k in the
+    low half), w_scale [E, n, k/group] -> out [capacity, n] bf16 (live rows).  fmt
+    'int4' (bf16 scales, group 32, 64 or 128) or 'mxfp4' (UE8M0 bytes, group 32)."""
+    import torch
+    fn, bf = "moe_grouped_gemm_w4", torch.bfloat16
+    (capacity, k), (E, n, _), groups = a.shape, w.shape, w_scale.shape[-1]
+    if groups < 1 or k % groups:
+        raise ValueError(f"{fn}: w_scale has {groups} groups along k = {k}")
+    _need(fn, ("a", a, bf, (capacity, k)), ("w", w, torch.uint8, (E, n, k // 2)),
+          ("w_scale", w_scale, bf if W4[fmt] == MOE_W4_INT4 else torch.uint8, (E, n, groups)),
+          ("psum", psum, torch.int32, (E,)), ("status", status, torch.int32, (2,)),
+          ("out", out, bf, (capacity, n)))
+    code = lib().moe_grouped_gemm_w4(
+        _ptr(a), _ptr(w), _ptr(w_scale), W4[fmt], k // groups, _ptr(psum), _ptr(status), capacity,
+        n, k, E, align, _ptr(out), _stream(stream))
+    _check(fn, code)
+
+
 class ExpandedMoE:
     """Buffers for one receive-buffer size, and the layer's five calls.
 
@@ -771,3 +932,133 @@ class TrainableBf16MoE(StandardBf16MoE):
             with _on(stream):
                 self.step.sub_(1)
             raise
+
+
+class StandardW4MoE(StandardBf16MoE):
+    """The standard path with 4-bit weights: as StandardBf16MoE, the products
+    from w13 [E, 2I, H/2] and w2 [E, H, I/2] uint8 (two codes a byte) with
+    w13_scale [E, 2I, H/group] and w2_scale [E, H, I/group].  fmt 'int4' (bf16
+    scales, group 32, 64 or 128) or 'mxfp4' (UE8M0 bytes, group 32)."""
+
+    def __init__(self, rows, topk, w13, w13_scale, w2, w2_scale, fmt, align=128,
+                 routed_scaling_factor=1.0, device="cuda"):
+        (E, two_i, half), (E2, H, half_i) = w13.shape, w2.shape
+        if E2 != E or H != 2 * half or two_i != 4 * half_i:
+            raise ValueError(f"StandardW4MoE: w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} "
+                             "are not [E, 2I, H/2] and [E, H, I/2]")
+        W4[fmt]
+        # The buffers are the bf16 path's, sized by w13's shape alone.
+        sizes = w13[:, :, :1].expand(E, two_i, H)
+        super().__init__(rows, topk, sizes, None, align, routed_scaling_factor, device)
+        self.fmt = fmt
+        self.w13, self.w13_scale, self.w2, self.w2_scale = w13, w13_scale, w2, w2_scale
+
+    def experts(self, stream=None):
+        moe_grouped_gemm_w4(self.ex, self.w13, self.w13_scale, self.fmt, self.psum, self.status,
+                            self.align, self.gate_up, stream)
+        moe_silu_mul_bf16(self.gate_up, self.m_indices, self.psum, self.status, self.E,
+                          self.align, self.y, stream)
+        moe_grouped_gemm_w4(self.y, self.w2, self.w2_scale, self.fmt, self.psum, self.status,
+                            self.align, self.down, stream)
+
+
+class MoEBlock:
+    """What stands around the experts of a layer: the norm of the residual
+    stream (with the branch before it added), the gate's product and the router.
+
+    experts: a StandardMoE, StandardBf16MoE, StandardW4MoE or TrainableBf16MoE.  gate
+    [E, H] bf16: a copy, padded to a multiple of 128 experts, is kept in self.gate
+    [1, >=E, H]; the logits are bf16.  weight, bias [H]: the norm's, bf16 or fp32;
+    select_bias [E] fp32: added to the scores for the choice only.  stream_dtype: the
+    residual stream's type (bf16 or fp32).  The choice is described at moe_router.
+
+    With a TrainableBf16MoE, backward() leaves the gradients of gate, weight and
+    bias in d_gate, d_weight and d_bias (grad: 'f32' or 'bf16').  The buffers are
+    made on the current stream: order a call on another one behind it."""
+
+    def __init__(self, experts, gate, weight, bias=None, select_bias=None, kind="rms", eps=1e-5,
+                 score="softmax", num_groups=1, topk_groups=1, normalize=True,
+                 stream_dtype=None, grad="f32"):
+        import torch
+        bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        E, H, rows, topk = experts.E, experts.H, experts.rows, experts.topk
+        if gate.shape != (E, H) or gate.dtype != bf:
+            raise ValueError(f"MoEBlock: gate must be bf16 of shape {(E, H)}, got {gate.dtype} of "
+                             f"shape {tuple(gate.shape)}")
+        if grad not in ("f32", "bf16"):
+            raise ValueError("MoEBlock: grad is 'f32' or 'bf16'")
+        dev = gate.device
+        self.moe, self.weight, self.bias, self.select_bias = experts, weight, bias, select_bias
+        self.kind, self.eps = kind, eps
+        self.route = dict(score=score, normalize=normalize)
+        self.groups = dict(num_groups=num_groups, topk_groups=topk_groups)
+        self.E, self.H, self.rows, self.topk = E, H, rows, topk
+        # The gate's product is a grouped one with a single group: all rows.
+        cap, n = -(-rows // 16) * 16, -(-E // 128) * 128
+        self.gate = torch.zeros((1, n, H), dtype=bf, device=dev)
+        self.gate[0, :E] = gate
+        self.all_rows = torch.full((1,), rows, dtype=i32, device=dev)
+        self.status = torch.tensor([cap, 0], dtype=i32, device=dev)
+        self.sum = torch.empty((rows, H), dtype=stream_dtype or bf, device=dev)
+        self.y = torch.zeros((cap, H), dtype=bf, device=dev)
+        self.mean = torch.empty(rows, dtype=f32, device=dev) if kind == "layer" else None
+        self.rstd = torch.empty(rows, dtype=f32, device=dev)
+        self.logits = torch.empty((cap, n), dtype=bf, device=dev)
+        self.topk_ids = torch.empty((rows, topk), dtype=i32, device=dev)
+        self.topk_weights = torch.empty((rows, topk), dtype=f32, device=dev)
+        self.h = None
+        if isinstance(experts, TrainableBf16MoE):
+            gdt = f32 if grad == "f32" else bf
+            self.d_logits = torch.zeros((cap, n), dtype=bf, device=dev)
+            self.d_y = torch.empty((cap, H), dtype=bf, device=dev)
+            self.d_gate = torch.zeros((1, n, H), dtype=gdt, device=dev)
+            self.d_weight = torch.zeros(H, dtype=gdt, device=dev)
+            self.d_bias = None if bias is None else torch.zeros(H, dtype=gdt, device=dev)
+            need = max(moe_grouped_wgrad_workspace_bytes(cap, n, H, 1),
+                       moe_layer_norm_backward_workspace_bytes(rows, H), 256)
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+
+    def _received(self, psum_recv_per_rank):
+        return self.all_rows if psum_recv_per_rank is None else psum_recv_per_rank[-1:]
+
+    def __call__(self, x, branch=None, psum_recv_per_rank=None, out=None, stream=None):
+        """Returns (the experts' output [rows, H] bf16, the residual stream: x, or
+        x + branch in self.sum).  A next block takes the stream as its x and the
+        output as its branch."""
+        self.h = x if branch is None else self.sum
+        y, logits = self.y[:self.rows], self.logits[:self.rows, :self.E]
+        moe_layer_norm(x, self.weight, y, self.bias, branch, None if branch is None else self.sum,
+                       self.mean, self.rstd, self.kind, self.eps, psum_recv_per_rank, stream)
+        moe_grouped_gemm_bf16(self.y, self.gate, self._received(psum_recv_per_rank), self.status,
+                              16, self.logits, stream)
+        moe_router(logits, self.topk_ids, self.topk_weights, self.select_bias,
+                   psum_recv_per_rank=psum_recv_per_rank, stream=stream, **self.route,
+                   **self.groups)
+        return self.moe(y, self.topk_ids, self.topk_weights, psum_recv_per_rank, out,
+                        stream), self.h
+
+    def backward(self, dout, dsum=None, psum_recv_per_rank=None, dx=None, accumulate=False,
+                 stream=None):
+        """Gradient of the last forward call with respect to its residual stream (x,
+        and the branch, if it had one), from the output's (dout) and the stream's
+        own (dsum, or None).  Returns dx [rows, H] of the stream's type."""
+        if not isinstance(self.moe, TrainableBf16MoE):
+            raise TypeError("MoEBlock: backward() needs a TrainableBf16MoE")
+        if self.h is None:
+            raise RuntimeError("MoEBlock: backward() before a forward call")
+        if dx is None:
+            dx = _output(stream, (self.rows, self.H), self.h.dtype, dout.device)
+        rows, received = slice(0, self.rows), self._received(psum_recv_per_rank)
+        d_y, d_topk = self.moe.backward(dout, self.topk_weights, psum_recv_per_rank,
+                                        accumulate=accumulate, stream=stream)
+        moe_router_backward(self.logits[rows, :self.E], self.topk_ids, d_topk,
+                            self.d_logits[rows, :self.E], psum_recv_per_rank=psum_recv_per_rank,
+                            stream=stream, **self.route)
+        moe_grouped_wgrad_bf16(self.d_logits, self.y, received, self.status, 16, self.d_gate,
+                               self.workspace, accumulate, stream)
+        moe_grouped_dgrad_bf16(self.d_logits, self.gate, received, self.status, 16, self.d_y,
+                               stream)
+        moe_layer_norm_backward(d_y, self.h, self.weight, self.rstd, dx, self.mean,
+                                self.d_y[rows], dsum, self.d_weight, self.d_bias, accumulate,
+                                self.kind, psum_recv_per_rank, self.workspace, stream)
+        return dx

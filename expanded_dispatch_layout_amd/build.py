@@ -13,7 +13,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["abi.cpp", "layout.hip", "gemm.hip", "act_quant.hip", "gather.hip", "masked.hip",
            "dgrad.hip", "wgrad.hip", "grad_narrow.hip", "silu_backward.hip",
-           "gather_backward.hip", "adamw.hip"]
+           "gather_backward.hip", "adamw.hip", "norm.hip", "router.hip", "w4.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

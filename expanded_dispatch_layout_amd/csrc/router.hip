@@ -1,0 +1,369 @@
+// moe_router, moe_router_backward: the choice of each token's experts from the
+// gate's logits, and its gradient.
+//
+//   s = softmax(x) or 1 / (1 + exp(-x));  the topk largest s + bias, the lowest
+//   expert first among equals;  w_k = s_k, or s_k / sum of the chosen s
+//
+// -inf and NaN logits are experts that are not available: score 0, never
+// chosen.  +inf counts as the largest finite value.
+//
+// The choice.  Without a bias and groups the scores' order is the logits' own,
+// and no exponential is needed to choose.  Otherwise the keys s + bias, and the
+// groups' sums of two, are compared in fp64: fp32 scores are off by a few
+// 2^-24, and neighbouring keys of 256 experts are nearer than that in one row
+// out of some thousands, which would then go to another expert.
+//
+// The weights.  Normalised weights are formed without the common factor that
+// can underflow: exp(x - max) over the chosen for softmax, and for the sigmoid,
+// which is exp(min(x, 0)) / (1 + exp(-|x|)), the same with min(x, 0).
+//
+// One wave per row; lane l holds experts l, l + 64, ...
+#include <float.h>
+#include <math.h>
+
+#include "common.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kMaxGroups = 64;
+
+__device__ __forceinline__ float load_logit(const void* x, bool f32, int64_t at) {
+  const float v = f32 ? ((const float*)x)[at] : bf16_to_f32(((const uint16_t*)x)[at]);
+  return v != v ? -INFINITY : fminf(v, FLT_MAX);
+}
+__device__ __forceinline__ float wave_max_f(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum_x(T v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+// The largest key of the wave and its expert, the lowest among equals; -1 where
+// every key is -inf.
+template <typename T>
+__device__ __forceinline__ void wave_best(T& key, int& at) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const T k = __shfl_xor(key, o, kWave);
+    const int a = __shfl_xor(at, o, kWave);
+    if (k > key || (k == key && a < at)) {
+      key = k;
+      at = a;
+    }
+  }
+}
+
+struct Sizes {
+  int E, topk, groups, topk_groups;
+  bool f32, sigmoid, normalize;
+};
+
+// Scores' common factor of a row: maximum and sum of softmax.
+template <int kPer>
+__device__ __forceinline__ void softmax_stats(const float (&x)[kPer], float& top, float& total) {
+  top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) top = fmaxf(top, x[i]);
+  top = wave_max_f(top);
+  total = 0.f;
+  if (top == -INFINITY) return;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) total += expf(x[i] - top);
+  total = wave_sum_x(total);
+}
+
+// Weight of the expert this lane holds the id of (logit v, id < 0: none).
+__device__ __forceinline__ float weight_of(float v, int id, const Sizes& z, float top,
+                                           float total) {
+  const bool here = id >= 0;
+  if (!z.normalize) {
+    if (!here) return 0.f;
+    return z.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top) / total;
+  }
+  const float low = here ? (z.sigmoid ? fminf(v, 0.f) : v) : -INFINITY;
+  const float m = wave_max_f(low);
+  float w = here ? expf(low - m) : 0.f;
+  if (z.sigmoid && here) w /= 1.0f + expf(-fabsf(v));
+  const float sum = wave_sum_x(w);
+  return here ? w / sum : 0.f;
+}
+
+template <typename T, int kPer>
+__device__ __forceinline__ int choose(T (&key)[kPer], const Sizes& z, int lane) {
+  int mine = -1;
+  for (int k = 0; k < z.topk; ++k) {
+    T best = -INFINITY;
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 64 * i;
+      }
+    wave_best(best, at);
+    if (best == (T)-INFINITY) break;
+    if (lane == k) mine = at;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 64 * i == at) key[i] = -INFINITY;
+  }
+  return mine;
+}
+
+template <int kPer>
+__global__ __launch_bounds__(kThreads) void router_kernel(
+    const void* __restrict__ logits, int64_t stride, const float* __restrict__ bias, Sizes z,
+    const int32_t* __restrict__ psum_rank, int nsrc, int64_t rows, int32_t* __restrict__ ids,
+    float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t nv = valid_rows(psum_rank, nsrc, rows);
+  for (int64_t r = (int64_t)blockIdx.x * kWaves + wid; r < nv;
+       r += (int64_t)gridDim.x * kWaves) {
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = lane + 64 * i;
+      x[i] = e < z.E ? load_logit(logits, z.f32, r * stride + e) : -INFINITY;
+    }
+    float top = 0.f, total = 1.f;
+    int id;
+    if (!bias && z.groups == 1) {
+      if (!z.sigmoid && !z.normalize) softmax_stats<kPer>(x, top, total);
+      id = choose<float, kPer>(x, z, lane);
+    } else {
+      double key[kPer];
+      if (!z.sigmoid) softmax_stats<kPer>(x, top, total);
+      double sum = 1.0;
+      if (!z.sigmoid) {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (top > -INFINITY) sum += exp((double)x[i] - (double)top);
+        sum = wave_sum_x(sum);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 64 * i;
+        key[i] = -INFINITY;
+        if (x[i] == -INFINITY) continue;
+        key[i] = z.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i]))
+                           : exp((double)x[i] - (double)top) / sum;
+        if (bias) {
+          const float b = bias[e];
+          key[i] = b != b ? -INFINITY : key[i] + (double)fminf(b, FLT_MAX);
+        }
+      }
+      if (z.groups > 1) {
+        const int per = z.E / z.groups;
+        double group = -INFINITY;  // lane g: the sum of group g's two largest keys
+        for (int g = 0; g < z.groups; ++g) {
+          double first = -INFINITY, second = -INFINITY;
+          int at = 0x7fffffff;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 64 * i;
+            if (e / per != g || !(key[i] > -INFINITY)) continue;
+            if (key[i] > first) {
+              second = first;
+              first = key[i];
+              at = e;
+            } else if (key[i] > second) {
+              second = key[i];
+            }
+          }
+          double best = first;
+          int best_at = at;
+          wave_best(best, best_at);
+          if (best == -INFINITY) continue;
+          double rest = best_at == at ? second : first;
+          int none = 0;
+          wave_best(rest, none);
+          if (lane == g) group = rest > -INFINITY ? best + rest : best;
+        }
+        uint64_t chosen = 0;
+        for (int k = 0; k < z.topk_groups; ++k) {
+          double best = group;
+          int at = group > -INFINITY ? lane : 0x7fffffff;
+          wave_best(best, at);
+          if (best == -INFINITY) break;
+          chosen |= 1ull << at;
+          if (lane == at) group = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (!(chosen >> ((lane + 64 * i) / per & 63) & 1)) key[i] = -INFINITY;
+      }
+      id = choose<double, kPer>(key, z, lane);
+    }
+    float v = 0.f;
+    if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
+    const float w = weight_of(v, id, z, top, total);
+    if (lane < z.topk) {
+      ids[r * z.topk + lane] = id;
+      weights[r * z.topk + lane] = w;
+    }
+  }
+}
+
+template <int kPer>
+__global__ __launch_bounds__(kThreads) void router_backward_kernel(
+    const void* __restrict__ logits, int64_t stride, const int32_t* __restrict__ ids,
+    const float* __restrict__ dw, Sizes z, const int32_t* __restrict__ psum_rank, int nsrc,
+    int64_t rows, void* __restrict__ dx, int64_t dx_stride) {
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t nv = valid_rows(psum_rank, nsrc, rows);
+  const bool dense = !z.sigmoid && !z.normalize;  // every available expert has a gradient
+  for (int64_t r = (int64_t)blockIdx.x * kWaves + wid; r < nv;
+       r += (int64_t)gridDim.x * kWaves) {
+    float x[kPer], d[kPer];
+    float top = 0.f, total = 1.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) d[i] = 0.f;
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 64 * i;
+        x[i] = e < z.E ? load_logit(logits, z.f32, r * stride + e) : -INFINITY;
+      }
+      softmax_stats<kPer>(x, top, total);
+    }
+    int id = -1;
+    float g = 0.f, v = 0.f;
+    if (lane < z.topk) {
+      id = ids[r * z.topk + lane];
+      if (id < 0 || id >= z.E) id = -1;
+      if (id >= 0) {
+        v = load_logit(logits, z.f32, r * stride + id);
+        if (v == -INFINITY) id = -1;
+        else g = dw[r * z.topk + lane];
+      }
+    }
+    const float w = weight_of(v, id, z, top, total);
+    const float dot = wave_sum_x(w * g);
+    float own;  // what the chosen experts get by themselves
+    if (z.sigmoid) own = w * (1.0f / (1.0f + expf(v))) * (z.normalize ? g - dot : g);
+    else own = w * (z.normalize ? g - dot : g);
+    for (int k = 0; k < z.topk; ++k) {
+      const int e = __shfl(id, k, kWave);
+      const float o = __shfl(own, k, kWave);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (e == lane + 64 * i) d[i] += o;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = lane + 64 * i;
+      if (e >= z.E) continue;
+      if (dense && x[i] > -INFINITY) d[i] -= expf(x[i] - top) / total * dot;
+      if (z.f32) ((float*)dx)[r * dx_stride + e] = d[i];
+      else ((uint16_t*)dx)[r * dx_stride + e] = f32_to_bf16_rne(d[i]);
+    }
+  }
+}
+
+moe_status check(const void* logits, int64_t stride, moe_float_fmt fmt, moe_score score,
+                 const int32_t* psum_recv_per_rank, int num_src_ranks, int64_t rows,
+                 int num_experts, int topk) {
+  if (rows < 0 || rows > (1LL << 30) || num_experts < 1 || num_experts > MOE_MAX_EXPERTS ||
+      topk < 1 || topk > MOE_MAX_TOPK || topk > num_experts || stride < num_experts ||
+      stride > (1LL << 30))
+    return MOE_ERR_SHAPE;
+  if (num_src_ranks < 0 || (psum_recv_per_rank && num_src_ranks == 0)) return MOE_ERR_SHAPE;
+  if ((fmt != MOE_FLOAT_BF16 && fmt != MOE_FLOAT_F32) ||
+      (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && !logits) return MOE_ERR_NULL;
+  if ((uintptr_t)logits % (fmt == MOE_FLOAT_F32 ? 4 : 2)) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int64_t matrix_bytes(int64_t rows, int cols, int64_t stride, moe_float_fmt fmt) {
+  return rows > 0 ? ((rows - 1) * stride + cols) * (fmt == MOE_FLOAT_F32 ? 4 : 2) : 0;
+}
+
+int64_t grid_of(int64_t rows) {
+  const int64_t blocks = (rows + kWaves - 1) / kWaves;
+  return blocks < 65536 ? blocks : 65536;  // grid-stride over the rest
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_router(const void* logits, int64_t logits_stride, moe_float_fmt fmt,
+                                 const float* bias, moe_score score, int num_groups,
+                                 int topk_groups, int normalize,
+                                 const int32_t* psum_recv_per_rank, int num_src_ranks,
+                                 int64_t rows, int num_experts, int topk, int32_t* topk_ids,
+                                 float* topk_weights, void* stream) {
+  const moe_status bad = check(logits, logits_stride, fmt, score, psum_recv_per_rank,
+                               num_src_ranks, rows, num_experts, topk);
+  if (bad != MOE_OK) return bad;
+  if (num_groups < 1 || num_groups > kMaxGroups || num_experts % num_groups || topk_groups < 1 ||
+      topk_groups > num_groups)
+    return MOE_ERR_SHAPE;
+  if (rows > 0 && (!topk_ids || !topk_weights)) return MOE_ERR_NULL;
+  if ((uintptr_t)bias % 4 || (uintptr_t)topk_ids % 4 || (uintptr_t)topk_weights % 4)
+    return MOE_ERR_ALIGNMENT;
+  const int64_t in = matrix_bytes(rows, num_experts, logits_stride, fmt), out = rows * topk * 4;
+  for (const void* o : {(const void*)topk_ids, (const void*)topk_weights})
+    if (overlap(o, out, logits, in) || overlap(o, out, bias, num_experts * 4LL) ||
+        overlap(o, out, psum_recv_per_rank, num_src_ranks * 4LL))
+      return MOE_ERR_UNSUPPORTED;
+  if (overlap(topk_ids, out, topk_weights, out)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const Sizes z = {num_experts,          topk, num_groups, topk_groups, fmt == MOE_FLOAT_F32,
+                   score == MOE_SCORE_SIGMOID, normalize != 0};
+  auto kern = num_experts <= 64    ? router_kernel<1>
+              : num_experts <= 128 ? router_kernel<2>
+              : num_experts <= 256 ? router_kernel<4>
+              : num_experts <= 512 ? router_kernel<8>
+                                   : router_kernel<16>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(rows)), dim3(kThreads), 0,
+                     reinterpret_cast<hipStream_t>(stream), logits, logits_stride, bias, z,
+                     psum_recv_per_rank, num_src_ranks, rows, topk_ids, topk_weights);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+extern "C" moe_status moe_router_backward(
+    const void* logits, int64_t logits_stride, moe_float_fmt fmt, moe_score score, int normalize,
+    const int32_t* topk_ids, const float* d_topk_weights, const int32_t* psum_recv_per_rank,
+    int num_src_ranks, int64_t rows, int num_experts, int topk, void* d_logits,
+    int64_t d_logits_stride, void* stream) {
+  const moe_status bad = check(logits, logits_stride, fmt, score, psum_recv_per_rank,
+                               num_src_ranks, rows, num_experts, topk);
+  if (bad != MOE_OK) return bad;
+  if (d_logits_stride < num_experts || d_logits_stride > (1LL << 30)) return MOE_ERR_SHAPE;
+  if (rows > 0 && (!topk_ids || !d_topk_weights || !d_logits)) return MOE_ERR_NULL;
+  if ((uintptr_t)d_logits % (fmt == MOE_FLOAT_F32 ? 4 : 2) || (uintptr_t)topk_ids % 4 ||
+      (uintptr_t)d_topk_weights % 4)
+    return MOE_ERR_ALIGNMENT;
+  const int64_t in = matrix_bytes(rows, num_experts, logits_stride, fmt), slots = rows * topk * 4;
+  const int64_t out = matrix_bytes(rows, num_experts, d_logits_stride, fmt);
+  if (overlap(d_logits, out, logits, in) || overlap(d_logits, out, topk_ids, slots) ||
+      overlap(d_logits, out, d_topk_weights, slots) ||
+      overlap(d_logits, out, psum_recv_per_rank, num_src_ranks * 4LL))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const Sizes z = {num_experts, topk, 1, 1, fmt == MOE_FLOAT_F32, score == MOE_SCORE_SIGMOID,
+                   normalize != 0};
+  auto kern = num_experts <= 64    ? router_backward_kernel<1>
+              : num_experts <= 128 ? router_backward_kernel<2>
+              : num_experts <= 256 ? router_backward_kernel<4>
+              : num_experts <= 512 ? router_backward_kernel<8>
+                                   : router_backward_kernel<16>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(rows)), dim3(kThreads), 0,
+                     reinterpret_cast<hipStream_t>(stream), logits, logits_stride, topk_ids,
+                     d_topk_weights, z, psum_recv_per_rank, num_src_ranks, rows, d_logits,
+                     d_logits_stride);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}

@@ -164,6 +164,28 @@ typedef enum {
                                scale per group of MOE_STATE_GROUP values  */
 } moe_state_fmt;
 
+typedef enum {
+  MOE_FLOAT_BF16 = 0,       /* bf16 values                                */
+  MOE_FLOAT_F32 = 1         /* fp32 values                                */
+} moe_float_fmt;
+
+typedef enum {
+  MOE_NORM_LAYER = 0,       /* about the mean                             */
+  MOE_NORM_RMS = 1          /* about zero                                 */
+} moe_norm_kind;
+
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+typedef enum {
+  MOE_W4_INT4 = 0,          /* two's complement codes -8..7, a bf16 scale
+                               per group of 32, 64 or 128 along K         */
+  MOE_W4_MXFP4 = 1          /* MXFP4: E2M1 codes (bit 3 the sign; 0, 0.5, 1,
+                               1.5, 2, 3, 4, 6), a UE8M0 byte per 32      */
+} moe_w4_fmt;
+
 /* Bits of status[1] written by moe_expand_layout. */
 #define MOE_FLAG_CAPACITY_OVERFLOW 1 /* total rows > capacity: rows at or past
                                         the capacity were dropped (their slots
@@ -627,6 +649,155 @@ moe_status moe_adamw(
     const moe_adamw_tensor* tensors, int num_tensors, const int64_t* step,
     const float* lr, const float* grad_scale, double beta1, double beta2, double eps,
     double weight_decay, void* stream);
+
+/*
+ * The norm of the residual stream in front of a layer, with the branch before
+ * it (attention's, or the last layer's output) added on the way:
+ *   h = x + branch                      (branch NULL: h = x)
+ *   mu = mean(h), rstd = 1 / sqrt(mean((h - mu)^2) + eps)
+ *                                       (MOE_NORM_RMS: mu = 0)
+ *   y = (h - mu) * rstd * weight + bias (bias NULL: none)
+ * in fp32, the variance about the mean.  With a branch, h is first rounded to
+ * the stream's type x_fmt: the norm is of the stream as it is kept.
+ *   x       [rows, x_stride] bf16 or fp32 (x_fmt), hidden columns used
+ *   branch  [rows, hidden] bf16 or NULL
+ *   weight, bias  [hidden] in w_fmt; bias may be NULL
+ *   sum     [rows, hidden] in x_fmt: h; may be NULL, and must be without a
+ *           branch; may be x itself where x_stride is hidden
+ *   y       [rows, hidden] bf16
+ *   mean, rstd  [rows] fp32, what the backward pass takes; may be NULL (mean:
+ *           0 for MOE_NORM_RMS)
+ *   psum_recv_per_rank / num_src_ranks  as for the layout (R_v)
+ * Rows >= R_v are neither read nor written.  A row whose h holds an infinity
+ * or a NaN gets NaN throughout.
+ * Sizes: hidden % 8 == 0 and hidden <= 8192 (else MOE_ERR_UNSUPPORTED);
+ * x_stride >= hidden, rows of x 16-byte aligned; 0 <= eps < infinity; buffers
+ * 16-byte aligned, mean and rstd 4-byte.  A buffer that is written and shares
+ * memory with another (but for sum and x, above): MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_layer_norm(
+    const void* x, int64_t x_stride, moe_float_fmt x_fmt, const void* branch,
+    const void* weight, const void* bias, moe_float_fmt w_fmt, moe_norm_kind kind, float eps,
+    const int32_t* psum_recv_per_rank, int num_src_ranks, int64_t rows, int hidden, void* sum,
+    void* y, float* mean, float* rstd, void* stream);
+
+/* Host, pure.  Bytes of device workspace moe_layer_norm_backward needs where
+ * it writes dweight or dbias.  Returns 0 on bad input. */
+size_t moe_layer_norm_backward_workspace_bytes(int64_t rows, int hidden);
+
+/*
+ * Gradient of moe_layer_norm.  With d = dy + dy2, xh = (x - mean) * rstd and
+ * g = d * weight, in fp32:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dsum
+ *                                       (MOE_NORM_RMS: without mean(g))
+ *   dweight = sum over rows of d * xh,  dbias = sum over rows of d
+ *   dy      [rows, hidden] bf16; dy2 the same, of a second reader of y (the
+ *           gate beside the experts), or NULL
+ *   x       [rows, x_stride] in x_fmt: the forward call's h (its sum, or x
+ *           where it had no branch)
+ *   mean, rstd  [rows] as the forward call wrote them; mean is not read for
+ *           MOE_NORM_RMS (may be NULL)
+ *   dsum    [rows, hidden] in x_fmt: the gradient that reaches h along the
+ *           residual stream, or NULL
+ *   dx      [rows, hidden] in x_fmt: the gradient of h, which is x's and the
+ *           branch's; may be dsum itself
+ *   dweight, dbias  [hidden] in grad_fmt; either may be NULL.  accumulate != 0:
+ *           the sums are added to what they hold, in fp32, and rounded once.
+ *           Without a valid row they become 0 (or stay, accumulating).
+ * Equal calls give equal bits.  Rows >= R_v enter no result, and their dx is
+ * not written.
+ * workspace: device, >= moe_layer_norm_backward_workspace_bytes(rows, hidden)
+ * bytes, 256-byte aligned, no initialisation needed; not used without dweight
+ * and dbias (may be NULL then).  Calls that may overlap need one each.
+ * Sizes and errors as moe_layer_norm; a short workspace is MOE_ERR_WORKSPACE.
+ */
+moe_status moe_layer_norm_backward(
+    const void* dy, const void* dy2, const void* x, int64_t x_stride, moe_float_fmt x_fmt,
+    const void* weight, moe_float_fmt w_fmt, moe_norm_kind kind, const float* mean,
+    const float* rstd, const void* dsum, const int32_t* psum_recv_per_rank, int num_src_ranks,
+    int64_t rows, int hidden, void* dx, void* dweight, void* dbias, moe_grad_fmt grad_fmt,
+    int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The router: each token's experts and their weights from the gate's logits,
+ * in the form that the layout takes.
+ *   logits  [rows, logits_stride] bf16 or fp32, num_experts columns used
+ *   bias    [num_experts] fp32 or NULL: added to the scores for the choice only
+ *   score   s = softmax(logits) or 1 / (1 + exp(-logits))
+ *   num_groups, topk_groups  1, 1: any expert.  Otherwise the experts are
+ *           num_groups runs of equal length, and only the topk_groups groups
+ *           with the largest sum of their two largest s + bias are chosen from
+ *   topk_ids      [rows, topk] int32: the topk largest s + bias, falling; the
+ *           lowest expert (group) first among equals
+ *   topk_weights  [rows, topk] fp32: s of each, or s / (sum of the chosen s)
+ *           with normalize != 0
+ *   psum_recv_per_rank / num_src_ranks  as for the layout (R_v)
+ * A logit (or bias) of -inf or NaN is an expert that is not available: it is
+ * never chosen, and a NaN or -inf logit has score 0.  +inf counts as the
+ * largest finite fp32 value.  Slots for which no expert is left (all of them
+ * in a row without any) get id -1 and weight 0.  Without a bias and groups
+ * the experts are compared by their logits, otherwise by fp64 scores: scores
+ * that differ are not taken for equal.  Rows >= R_v are neither read nor
+ * written.
+ * Sizes: 1 <= topk <= min(num_experts, MOE_MAX_TOPK), num_experts <=
+ * MOE_MAX_EXPERTS, num_groups <= 64 and a divisor of num_experts,
+ * logits_stride >= num_experts; buffers aligned to their elements.  An output
+ * that shares memory with another buffer: MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_router(
+    const void* logits, int64_t logits_stride, moe_float_fmt fmt, const float* bias,
+    moe_score score, int num_groups, int topk_groups, int normalize,
+    const int32_t* psum_recv_per_rank, int num_src_ranks, int64_t rows, int num_experts,
+    int topk, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/*
+ * Gradient of moe_router's weights (the choice has none):
+ *   topk_ids        [rows, topk] as the forward call wrote them; slots outside
+ *                   [0, num_experts) or of an expert that is not available
+ *                   are passed over (their d_topk_weights is not read into any result)
+ *   d_topk_weights  [rows, topk] fp32
+ *   d_logits        [rows, d_logits_stride] in fmt, num_experts columns
+ *                   written: with w the weights, g their gradients and sums
+ *                   over the row's slots,
+ *     softmax             d x_j = w_j g_j - s_j * sum(w g)    (every expert)
+ *     softmax, normalize  d x_j = w_j (g_j - sum(w g))        (0 if not chosen)
+ *     sigmoid             d x_j = w_j (1 - s_j) g_j
+ *     sigmoid, normalize  d x_j = w_j (1 - s_j) (g_j - sum(w g))
+ *                   An expert that is not available gets 0; one that is named
+ *                   twice gets the sum of its slots.
+ * Rows >= R_v are neither read nor written.  Sizes and errors as moe_router.
+ */
+moe_status moe_router_backward(
+    const void* logits, int64_t logits_stride, moe_float_fmt fmt, moe_score score, int normalize,
+    const int32_t* topk_ids, const float* d_topk_weights, const int32_t* psum_recv_per_rank,
+    int num_src_ranks, int64_t rows, int num_experts, int topk, void* d_logits,
+    int64_t d_logits_stride, void* stream);
+
+/*
+ * Contiguous grouped GEMM with 4-bit weights, "NT": as moe_grouped_gemm_bf16,
+ * for every live expanded row m of expert e (m < psum[e], m < min(status[0],
+ * capacity))
+ *   out[m, j] = bf16( sum over groups g of s[e, j, g] *
+ *                     sum over t in g of a[m, t] * q[e, j, t] )
+ * accumulated in fp32.
+ *   a        [capacity, k] bf16
+ *   w        [num_experts, n, k/2] bytes of two codes each, the lower k in the
+ *            low four bits
+ *   w_scale  [num_experts, n, k/group]: bf16 (MOE_W4_INT4; group 32, 64 or
+ *            128) or UE8M0 bytes (MOE_W4_MXFP4; group 32).  MXFP4 weights are
+ *            exact for scale bytes 2..252 and NaN for byte 255; other bytes make weights
+ *            outside bf16's normal range.
+ *   out      [capacity, n] bf16; rows that are not live are not written
+ * Rows of a that are not live do not enter any result.
+ * Sizes: n % 128 == 0, k % 128 == 0 and n / 64, k / 64 <= 511 (else
+ * MOE_ERR_UNSUPPORTED), align and capacity as for the layout; buffers
+ * 16-byte aligned.  out sharing memory with another buffer:
+ * MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_grouped_gemm_w4(
+    const void* a, const void* w, const void* w_scale, moe_w4_fmt fmt, int group,
+    const int32_t* psum, const int32_t* status, int64_t capacity, int n, int k, int num_experts,
+    int align, void* out, void* stream);
 
 #ifdef __cplusplus
 }

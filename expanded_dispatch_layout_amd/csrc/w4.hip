@@ -23,9 +23,8 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kRows = 16, kCols = 64, kTiles = kCols / 16;
-constexpr int BK = 128;
+constexpr int kThreads = 512, kWaves = 8;
+constexpr int BK = 128;                   // a block of the narrow path
 
 // 4 x 4 words between the wave's 16-lane rows: word i of row r <-> word r of
 // row i.
@@ -90,125 +89,473 @@ struct Scales {  // of one column's 128-deep block
   }
 };
 
+// ------------------------------------------------------------------ items
+
+constexpr int kNarrowRows = 32, kNarrowCols = 64;  // most rows of a narrow item
+constexpr int kMostNarrow = 64;           // rows of an expert whose items are narrow
+constexpr int kTileRows = 128;
+constexpr int kStages = 5;
+constexpr int kABytes = kTileRows * 128, kWBytes = 8192, kSBytes = 2048;
+constexpr int kStageBytes = kABytes + kWBytes + kSBytes;
+constexpr int kLoads = 4;                 // per wave and stage
+
+// The three kinds of items: of 128 rows, of up to 32, of up to 16.
+constexpr int kWide = 0, kTwo = 1, kOne = 2;
+
+struct Shared {
+  __attribute__((aligned(1024))) uint8_t data[kStages * kStageBytes];
+  int pe[MOE_MAX_EXPERTS];                // psum
+  int gp[3][MOE_MAX_EXPERTS + 1];         // prefix of each kind's row groups per expert
+};
+
+struct Args {
+  const uint8_t *a, *w, *sc;
+  int64_t nrows;
+  int n, k, E, align;
+  uint16_t* out;
+};
+
+// First row of expert e, and its live rows.
+__device__ __forceinline__ int rows_of(const Shared& sh, const Args& p, int e, int& st) {
+  if (e >= p.E) return 0;
+  st = e ? max(0, align_up_i(sh.pe[e - 1], p.align)) : 0;
+  const int64_t en = min((int64_t)sh.pe[e], p.nrows);
+  return en > st ? (int)(en - st) : 0;
+}
+
+// The row groups of every kind.  Experts of more than kMostNarrow rows are wide;
+// where narrow items alone fill no more than a round of the workgroups, none is.
+__device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) {
+  int64_t groups = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int st;
+    groups += (rows_of(sh, p, e0 + lane, st) + kNarrowRows - 1) / kNarrowRows;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) groups += __shfl_xor(groups, o, kWave);
+  const bool narrow = groups * (p.n / kNarrowCols) <= gridDim.x;
+  int sum[3] = {0, 0, 0};
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int st;
+    const int e = e0 + lane, rows = rows_of(sh, p, e, st);
+    const int kind = rows > kMostNarrow && !narrow ? kWide : rows > 16 ? kTwo : kOne;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int per = i == kWide ? kTileRows : i == kTwo ? kNarrowRows : 16;
+      const int ng = kind == i ? (rows + per - 1) / per : 0;
+      const int incl = wave_incl_scan_i(ng);
+      if (e < p.E) sh.gp[i][e] = sum[i] + incl - ng;
+      sum[i] += __shfl(incl, 63, 64);
+    }
+  }
+  if (lane < 3) sh.gp[lane][p.E] = lane == 0 ? sum[0] : lane == 1 ? sum[1] : sum[2];
+}
+
+struct Item {
+  int e, col, live, m0;
+};
+// Item i of a kind: expert by expert, column tile by column tile, the row groups
+// innermost: they read the same weights side by side on one XCD.
+__device__ __forceinline__ Item decode(const Shared& sh, const Args& p, int kind, uint32_t i,
+                                       int NT, int cols, int rows) {
+  const int q = (int)(i / (uint32_t)NT);
+  const int* gp = sh.gp[kind];
+  int lo = 0, hi = p.E - 1;  // last e with gp[e] <= q
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gp[mid] <= q) lo = mid;
+    else hi = mid - 1;
+  }
+  Item t;
+  t.e = __builtin_amdgcn_readfirstlane(lo);
+  const int g0 = __builtin_amdgcn_readfirstlane(gp[t.e]);
+  const int ge = __builtin_amdgcn_readfirstlane(gp[t.e + 1]) - g0;
+  const int local = (int)(i - (uint32_t)NT * (uint32_t)g0);
+  int st = 0;
+  const int all = __builtin_amdgcn_readfirstlane(rows_of(sh, p, t.e, st));
+  const int at = local % ge * rows;
+  t.col = local / ge * cols;
+  t.m0 = __builtin_amdgcn_readfirstlane(st) + at;
+  t.live = min(rows, all - at);
+  return t;
+}
+
+// ----------------------------------------------------------------- narrow
+
+// 16 kMt rows, 64 columns.  The eight waves take every eighth 128-deep block of the
+// reduction, kRing blocks in flight, across the items; their sums meet in LDS.
+template <int kGroup, int kMt, int kRing>
+__device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first_item,
+                                       uint32_t last_item, uint32_t nitems, uint32_t& base,
+                                       int lane, int wid) {
+  constexpr bool kFp4 = kGroup == 0;
+  constexpr int kTiles = kNarrowCols / 16;
+  constexpr int kScBytes = kFp4 ? 4 : 2 * Scales<kGroup>::kPer;  // per column and block
+  constexpr int kG = kFp4 ? 1 : 128 / kGroup, kSteps = 4 / kG;   // groups of a block, MFMAs each
+  if (round_item(base, nitems) >= last_item) return;
+  struct Set {
+    u32x4 w[kTiles], x[kMt][4];
+    Scales<kGroup> s[kTiles];
+  } set[kRing];
+  const int c = lane & 15, qd = lane >> 4;
+  const int k = p.k, KB = k / BK, NT = p.n / kNarrowCols;
+  const int nk = (KB - wid + kWaves - 1) / kWaves;  // blocks of this wave per item
+  uint32_t lbase = base;  // loading side
+  int lk = 0;
+  const uint8_t *wp, *sp, *ap[kMt];
+  auto item_of = [&](uint32_t item) __attribute__((always_inline)) {
+    return decode(sh, p, kMt == 2 ? kTwo : kOne, item - first_item, NT, kNarrowCols, 16 * kMt);
+  };
+  auto open = [&]() __attribute__((always_inline)) {
+    const uint32_t item = round_item(lbase, nitems);
+    Item t = {0, 0, 1, 0};  // past the last item: loads of the first weights, unused
+    if (item < last_item) t = item_of(item);
+    const int64_t col = (int64_t)t.e * p.n + t.col + c;
+    wp = p.w + col * (k / 2) + 16 * qd;
+    sp = p.sc + col * KB * kScBytes;
+    // Rows past the live ones repeat the last one: a row of the result comes
+    // from its own row of a alone, and theirs are not stored.
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+      ap[m] = p.a + ((int64_t)(t.m0 + min(16 * m + c, t.live - 1)) * k + 8 * qd) * 2;
+  };
+  auto load = [&](Set& s) __attribute__((always_inline)) {
+    const int kb = wid + kWaves * lk;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      s.w[j] = *reinterpret_cast<const u32x4*>(wp + (int64_t)j * 8 * k + kb * (BK / 2));
+      s.s[j].load(sp + ((int64_t)j * 16 * KB + kb) * kScBytes);
+    }
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s.x[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + (kb * BK + 32 * i) * 2);
+    if (++lk == nk) {
+      lk = 0;
+      lbase += gridDim.x;
+      open();
+    }
+  };
+  v4f acc[kMt][kTiles];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  auto compute = [&](Set& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) exchange(s.w[j]);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      if constexpr (!kFp4) sched_fence();  // keeps the groups' values apart
+      v4f off[kMt];
+      if constexpr (!kFp4) {
+        const u32x4 m24 = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+#pragma unroll
+        for (int m = 0; m < kMt; ++m) {
+          off[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            off[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]),
+                __builtin_bit_cast(bf16x8, m24), off[m], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        if constexpr (kGroup == 32) sched_fence();
+        bf16x8 v[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          v[i] = kFp4 ? fp4_values(s.w[j][i], s.s[j].get(i)) : int4_values(s.w[j][g * kSteps + i]);
+#pragma unroll
+        for (int m = 0; m < kMt; ++m) {
+          v4f part = kFp4 ? acc[m][j] : off[m];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]), v[i], part, 0, 0, 0);
+          if constexpr (kFp4) acc[m][j] = part;
+          else acc[m][j] += part * s.s[j].get(g);
+        }
+      }
+    }
+  };
+  // Sums of the waves.  Lane: rows 4 qd + 0..3 of column 16 j + c.
+  constexpr int kPitch = kNarrowCols + 4;
+  float* part = reinterpret_cast<float*>(sh.data);
+  auto join = [&](uint32_t item) __attribute__((always_inline)) {
+    const Item t = item_of(item);
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          part[((wid * kMt + m) * 16 + 4 * qd + r) * kPitch + 16 * j + c] = acc[m][j][r];
+    wait_lgkm0();
+    barrier();
+    const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;
+    if (row < t.live) {
+      v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i)
+        v += *reinterpret_cast<const v4f*>(part + (i * 16 * kMt + row) * kPitch + col);
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *reinterpret_cast<u32x2*>(p.out + ((int64_t)t.m0 + row) * p.n + t.col + col) =
+          u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+    }
+    wait_lgkm0();
+    barrier();  // the partial sums have been read
+  };
+  clear();
+  if (nk <= 0) {  // fewer blocks than waves: this one has nothing to add
+    for (;;) {
+      const uint32_t item = round_item(base, nitems);
+      if (item >= last_item) return;
+      join(item);
+      base += gridDim.x;
+    }
+  }
+  open();
+#pragma unroll
+  for (int r = 0; r < kRing; ++r) load(set[r]);
+  int ck = 0;
+  for (;;) {
+#pragma unroll
+    for (int r = 0; r < kRing; ++r) {
+      compute(set[r]);
+      load(set[r]);
+      if (++ck == nk) {
+        ck = 0;
+        join(round_item(base, nitems));
+        clear();
+        base += gridDim.x;
+        if (round_item(base, nitems) >= last_item) return;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- wide
+
+__device__ __forceinline__ int x_key(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ void dma4_ptr(const uint8_t* p, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+
+// 128 rows, 64 kFn columns: eight waves, 2 by 4, of 64 x 16 kFn.  Stages of 64
+// along the reduction, five in LDS: rows, codes and one word of scales per
+// column each.  A wave computes on a stage from registers while it reads the
+// next one's fragments.
+template <int kGroup, int kFn>
+__device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, int NT, int lane,
+                                     int wid) {
+  constexpr bool kFp4 = kGroup == 0;
+  constexpr int kFm = 4, kBn = 64 * kFn;
+  const int n = p.n, k = p.k;
+  const Item t = decode(sh, p, kWide, item, NT, kBn, kTileRows);
+  const int e = t.e, n0 = t.col, live = t.live;
+  const int64_t m0 = t.m0;
+  const int wr = wid >> 2, wc = wid & 3, c = lane & 15, qd = lane >> 4;
+  const uint32_t lds0 = lds_addr(sh.data);
+
+  // Loads: rows 16 wid + 8 u + lane / 8 (the last live one in place of those
+  // that are not); 32 columns of codes and 64 of scales, the tile's several times where
+  // it has fewer.  Columns past n repeat the last one and are not stored.
+  const uint8_t* pa[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int row = 16 * wid + 8 * u + (lane >> 3);
+    pa[u] = p.a + (m0 + min(row, live - 1)) * k * 2 + (((lane & 7) ^ x_key(row)) << 4);
+  }
+  const uint8_t *pw, *ps;
+  {
+    const int wcol = 32 * (wid % (kBn / 32)) + (lane >> 1);
+    pw = p.w + ((int64_t)e * n + min(n0 + wcol, n - 1)) * (k / 2) +
+         (((lane & 1) ^ (wcol >> 3 & 1)) << 4);
+    const int scol = 64 * (wid % (kBn / 64)) + lane;
+    const int64_t col = (int64_t)e * n + min(n0 + scol, n - 1);
+    if constexpr (kGroup == 0) ps = p.sc + col * (k / 32);
+    else ps = p.sc + col * (k / kGroup) * 2;
+  }
+  auto stage = [&](int s, uint32_t slot) __attribute__((always_inline)) {
+    const uint32_t at = lds0 + slot;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) dma16_ptr(pa[u] + s * 128, at + (2 * wid + u) * 1024);
+    dma16_ptr(pw + s * 32, at + kABytes + wid * 1024);
+    // The aligned word that holds the stage's scales.
+    const uint8_t* v;
+    if constexpr (kGroup == 32) v = ps + s * 4;
+    else if constexpr (kGroup == 128) v = (const uint8_t*)((uintptr_t)(ps + (s >> 1) * 2) & ~3ull);
+    else v = ps + (s >> 1) * 4;
+    dma4_ptr(v, at + kABytes + kWBytes + wid * 256);
+  };
+
+  const uint32_t fx = lds0 + (wr * 64 + c) * 128 + ((qd ^ x_key(c)) << 4);
+  const uint32_t fw = lds0 + kABytes + (wc * kFn * 16 + c) * 32 + ((c >> 3) << 4) + 4 * qd;
+  const uint32_t fs = lds0 + kABytes + kWBytes + (wc * kFn * 16 + (kFp4 ? c : 4 * qd)) * 4;
+  v4f acc[kFm][kFn] = {};
+  struct Frags {
+    u32x4 x[2][kFm];
+    uint32_t w[2][kFn];
+    uint32_t s[kFp4 ? kFn : 1];
+  } f[2];
+  auto read = [&](Frags& r, uint32_t slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kFn; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        r.w[h][j] = lds_load<uint32_t>(((fw + slot) ^ (uint32_t)(h << 4)) + j * 512);
+      if constexpr (kFp4) r.s[j] = lds_load<uint32_t>(fs + slot + j * 64);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kFm; ++i)
+        r.x[h][i] = lds_load<u32x4>(((fx + slot) ^ (uint32_t)(h << 6)) + i * 2048);
+  };
+  // int4, group 128: whether the word of column 4 qd + r of tile j holds the
+  // stage's scale in its upper half (the same for all tiles: 16 columns apart).
+  const int64_t scol0 = (int64_t)e * n + n0 + 4 * qd;
+  const int per = k / BK;
+  auto scale_of = [&](uint32_t v, int r, int s, int h) __attribute__((always_inline)) {
+    uint32_t up;
+    if constexpr (kGroup == 32) up = h;
+    else if constexpr (kGroup == 64) up = s & 1;
+    else up = (uint32_t)((scol0 + r) * per + (s >> 1)) & 1;
+    return __uint_as_float(up ? v & 0xffff0000u : v << 16);
+  };
+  auto mfma = [](const bf16x8& w, const u32x4& x, const v4f& d) __attribute__((always_inline)) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x), d, 0, 0, 0);
+  };
+  auto compute = [&](Frags& r, int s, uint32_t slot, auto parity) __attribute__((always_inline)) {
+    constexpr int kOdd = decltype(parity)::value;
+    if constexpr (kFp4) {
+#pragma unroll
+      for (int j = 0; j < kFn; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bf16x8 v =
+              fp4_values(r.w[h][j], __uint_as_float((r.s[j] >> (16 * kOdd + 8 * h) & 0xffu) << 23));
+#pragma unroll
+          for (int i = 0; i < kFm; ++i) acc[i][j] = mfma(v, r.x[h][i], acc[i][j]);
+        }
+    } else {
+      const u32x4 m24 = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+      constexpr int kParts = kGroup == 32 ? 2 : 1;  // groups of a stage, at most a stage long
+      v4f off[kParts][kFm];
+#pragma unroll
+      for (int i = 0; i < kFm; ++i) {
+        const bf16x8 c24 = __builtin_bit_cast(bf16x8, m24);
+        const v4f zero = {0.f, 0.f, 0.f, 0.f};
+        off[0][i] = mfma(c24, r.x[0][i], zero);
+        off[kParts - 1][i] = mfma(c24, r.x[1][i], kParts == 1 ? off[0][i] : zero);
+      }
+#pragma unroll
+      for (int j = 0; j < kFn; ++j) {
+        sched_fence();  // one tile's values at a time: no spills
+        v4f part[kFm];
+        const u32x4 sw = lds_load<u32x4>(fs + slot + j * 64);  // of the lane's 4 columns
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bf16x8 v = int4_values(r.w[h][j]);
+#pragma unroll
+          for (int i = 0; i < kFm; ++i)
+            part[i] = mfma(v, r.x[h][i], kParts == 2 || h == 0 ? off[kParts == 2 ? h : 0][i]
+                                                               : part[i]);
+          if (kParts == 2 || h == 1) {
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+              const float sv = scale_of(sw[e4], e4, s, h);
+#pragma unroll
+              for (int i = 0; i < kFm; ++i) acc[i][j][e4] += part[i][e4] * sv;
+            }
+          }
+        }
+      }
+    }
+  };
+
+  const int steps = k / 64;  // even
+  wait_vmcnt<0>();  // the last item's stores do not enter the counts below
+  for (int s = 0; s < kStages - 1 && s < steps; ++s) stage(s, s * kStageBytes);
+  wait_ahead<kLoads, kStages - 2>(min(kStages - 2, steps - 1));
+  barrier();
+  read(f[0], 0);
+  uint32_t now = 0, next = kStageBytes, free = (kStages - 1) * kStageBytes;
+  auto bump = [](uint32_t x) { return x + kStageBytes == kStages * kStageBytes ? 0 : x + kStageBytes; };
+  // Stage s is in registers; the next one's fragments are read once it has
+  // landed for all waves, and the slot of stage s - 1 is loaded anew (that of
+  // stage s still holds int4's scales).
+  auto step = [&](int s, auto parity) __attribute__((always_inline)) {
+    constexpr int kOdd = decltype(parity)::value;
+    wait_ahead<kLoads, kStages - 3>(min(kStages - 3, steps - 2 - s));
+    wait_lgkm0();
+    barrier();
+    if (s + kStages - 1 < steps) stage(s + kStages - 1, free);
+    if (s + 1 < steps) read(f[kOdd ^ 1], next);
+    compute(f[kOdd], s, now, parity);
+    now = next;
+    next = bump(next);
+    free = bump(free);
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, std::integral_constant<int, 0>());
+    step(s + 1, std::integral_constant<int, 1>());
+  }
+  barrier();  // the last stages have been read
+
+  // The lane holds columns 4 qd + 0..3 of tile j for row c of tile i; two lane
+  // swaps make 8 neighbouring columns of two tiles: 16-byte stores.
+  const int tc = n0 + wc * kFn * 16 + (lane >> 5) * 16 + (lane >> 4 & 1) * 8;
+#pragma unroll
+  for (int i = 0; i < kFm; ++i) {
+    const int m = wr * 64 + i * 16 + c;
+    uint16_t* row = p.out + (m0 + m) * n + tc;
+#pragma unroll
+    for (int j = 0; j < kFn; j += 2) {
+      const u32x4 o = pack_tiles(acc[i][j], acc[i][j + 1]);
+      if (m < live && tc + j * 16 < n) *reinterpret_cast<u32x4*>(row + j * 16) = o;
+    }
+  }
+}
+
 template <int kGroup>
 __global__ __launch_bounds__(kThreads) void w4_kernel(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ w, const uint8_t* __restrict__ sc,
     const int32_t* __restrict__ psum, const int32_t* __restrict__ status, int64_t capacity, int n,
     int k, int E, int align, uint16_t* __restrict__ out) {
-  constexpr bool kFp4 = kGroup == 0;
-  constexpr int kScBytes = kFp4 ? 4 : 2 * Scales<kGroup>::kPer;  // per column and block
-  __shared__ v4f lds[kWaves][kRows][kCols / 4 + 1];
-  __shared__ int gp[MOE_MAX_EXPERTS + 1];  // prefix of 16-row groups per expert
+  __shared__ Shared sh;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t nrows = min((int64_t)status[0], capacity);
-  auto expert_rows = [&](int e, int64_t& st, int64_t& en) __attribute__((always_inline)) {
-    st = e ? max(0, align_up_i(psum[e - 1], align)) : 0;
-    en = min((int64_t)psum[e], nrows);
-  };
-  if (wid == 0) {
-    int sum = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      int ng = 0;
-      if (e < E) {
-        int64_t st, en;
-        expert_rows(e, st, en);
-        ng = en > st ? (int)((en - st + kRows - 1) / kRows) : 0;
-      }
-      const int incl = wave_incl_scan_i(ng);
-      if (e < E) gp[e] = sum + incl - ng;
-      sum += __shfl(incl, 63, 64);
-    }
-    if (lane == 0) gp[E] = sum;
-  }
+  const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out};
+  for (int e = threadIdx.x; e < E; e += kThreads) sh.pe[e] = psum[e];
   __syncthreads();
-  const int NT = n / kCols, KB = k / BK;
-  const uint32_t nitems = (uint32_t)__builtin_amdgcn_readfirstlane(gp[E]) * (uint32_t)NT;
-  for (uint32_t base = 0; base < nitems; base += gridDim.x) {
+  if (wid == 0) list_items(sh, p, lane);
+  __syncthreads();
+  const int groups = __builtin_amdgcn_readfirstlane(sh.gp[kWide][E]);
+  // 256 columns where that makes a round of items or more.
+  const int NT256 = (n + 255) / 256, NT128 = n / 128;
+  const bool big = kGroup != 32 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
+  const int NTW = big ? NT256 : NT128, NT = n / kNarrowCols;
+  const uint32_t nwide = (uint32_t)groups * (uint32_t)NTW;
+  const uint32_t end2 =
+      nwide + (uint32_t)__builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]) * (uint32_t)NT;
+  const uint32_t nitems =
+      end2 + (uint32_t)__builtin_amdgcn_readfirstlane(sh.gp[kOne][E]) * (uint32_t)NT;
+  uint32_t base = 0;
+  for (;; base += gridDim.x) {
     const uint32_t item = round_item(base, nitems);
-    if (item >= nitems) break;
-    const int q = (int)(item / (uint32_t)NT);
-    int lo = 0, hi = E - 1;  // last e with gp[e] <= q
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (gp[mid] <= q) lo = mid;
-      else hi = mid - 1;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int g0 = __builtin_amdgcn_readfirstlane(gp[e]);
-    const int ge = __builtin_amdgcn_readfirstlane(gp[e + 1]) - g0;
-    const int local = (int)(item - (uint32_t)NT * (uint32_t)g0);
-    const int n0 = local / ge * kCols;
-    int64_t st, en;
-    expert_rows(e, st, en);
-    const int64_t m0 = st + (int64_t)(local % ge) * kRows;
-    const int live = (int)min((int64_t)kRows, en - m0);
-
-    const int c = lane & 15, qd = lane >> 4;
-    const bool row = c < live;
-    const uint8_t* ap = a + ((m0 + c) * k + 8 * qd) * 2;
-    const uint8_t* wp = w + ((int64_t)e * n + n0 + c) * (k / 2) + 16 * qd;
-    const uint8_t* sp = sc + ((int64_t)e * n + n0 + c) * (int64_t)KB * kScBytes;
-    v4f acc[kTiles] = {};
-    for (int kb = wid; kb < KB; kb += kWaves) {
-      u32x4 av[4], wv[kTiles];
-      Scales<kGroup> s[kTiles];
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
-        wv[j] = *reinterpret_cast<const u32x4*>(wp + (int64_t)j * 16 * (k / 2) + kb * (BK / 2));
-        s[j].load(sp + ((int64_t)j * 16 * KB + kb) * kScBytes);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = u32x4{0, 0, 0, 0};
-        if (row) av[i] = *reinterpret_cast<const u32x4*>(ap + (kb * BK + 32 * i) * 2);
-      }
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) exchange(wv[j]);
-      v4f part[kTiles];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 x = __builtin_bit_cast(bf16x8, av[i]);
-        if constexpr (kFp4) {
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, fp4_values(wv[j][i], s[j].get(i)),
-                                                             acc[j], 0, 0, 0);
-        } else {
-          constexpr int kSteps = kGroup / 32;  // MFMAs per group
-          const u32x4 m24 = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
-          v4f off = {0.f, 0.f, 0.f, 0.f};
-          off = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, m24), off,
-                                                        0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) {
-            const v4f from = i % kSteps == 0 ? off : part[j] + off;
-            part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, int4_values(wv[j][i]), from, 0,
-                                                              0, 0);
-            if (i % kSteps == kSteps - 1) acc[j] += part[j] * s[j].get(i / kSteps);
-          }
-        }
-      }
-    }
-    // lane: rows 4 qd + 0..3 of column 16 j + c
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        reinterpret_cast<float*>(lds[wid][4 * qd + r])[16 * j + c] = acc[j][r];
-    __syncthreads();
-    const int orow = threadIdx.x >> 4, oc = threadIdx.x & 15;
-    v4f v = lds[0][orow][oc];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) v += lds[i][orow][oc];
-    if (orow < live) {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2*>(out + (m0 + orow) * n + n0 + 4 * oc) =
-          u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-    }
-    __syncthreads();  // the partial sums have been read
+    if (item >= nwide) break;
+    if (kGroup != 32 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
+    else wide<kGroup, 2>(sh, p, item, NTW, lane, wid);
   }
+  narrow<kGroup, 2, kGroup == 32 ? 1 : kGroup ? 2 : 3>(sh, p, nwide, end2, nitems, base, lane, wid);
+  narrow<kGroup, 1, kGroup == 32 ? 3 : 4>(sh, p, end2, nitems, nitems, base, lane, wid);
 }
 
 }  // namespace
@@ -240,8 +587,10 @@ extern "C" moe_status moe_grouped_gemm_w4(const void* a, const void* w, const vo
       overlap(out, bytes, w_scale, cols * (k / group) * (fmt == MOE_W4_INT4 ? 2 : 1)) ||
       overlap(out, bytes, psum, num_experts * 4LL) || overlap(out, bytes, status, 8))
     return MOE_ERR_UNSUPPORTED;
-  int64_t grid = ((capacity + kRows - 1) / kRows + num_experts) * (int64_t)(n / kCols);
-  if (grid > 2 * device_cus()) grid = 2 * device_cus();
+  // A workgroup per CU (its LDS) walks the items of the device's layout.
+  int64_t grid = ((capacity + kNarrowRows - 1) / kNarrowRows + num_experts) *
+                 (int64_t)(n / kNarrowCols);
+  if (grid > device_cus()) grid = device_cus();
   grid = (grid + kXcds - 1) / kXcds * kXcds;
   auto kern = fmt == MOE_W4_MXFP4 ? w4_kernel<0>
               : group == 32       ? w4_kernel<32>

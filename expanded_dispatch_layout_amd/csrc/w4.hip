@@ -69,18 +69,16 @@ __device__ __forceinline__ bf16x8 int4_values(uint32_t d) {
 // kGroup 0: MXFP4; otherwise int4 with scales per 32, 64 or 128.
 template <int kGroup>
 struct Scales {  // of one column's 128-deep block
-  static constexpr int kPer = BK / (kGroup ? kGroup : 32);
+  static constexpr int kBytes = kGroup ? 2 * BK / kGroup : 4;
   uint32_t w[2];
-  __device__ __forceinline__ void load(const uint8_t* p) {
+  __device__ __forceinline__ void load(uint32_t lds) {
     if constexpr (kGroup == 0 || kGroup == 64) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
+      w[0] = lds_load<uint32_t>(lds);
     } else if constexpr (kGroup == 128) {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
+      w[0] = lds_load<uint16_t>(lds);
     } else {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-      w[0] = v[0];
-      w[1] = v[1];
+      w[0] = lds_load<uint32_t>(lds);
+      w[1] = lds_load<uint32_t>(lds + 4);
     }
   }
   __device__ __forceinline__ float get(int i) const {  // group i
@@ -99,6 +97,10 @@ constexpr int kABytes = kTileRows * 128, kWBytes = 8192, kSBytes = 2048;
 constexpr int kStageBytes = kABytes + kWBytes + kSBytes;
 constexpr int kLoads = 4;                 // per wave and stage
 
+// Narrow items: partial sums of 16 rows by 64 columns for each wave, then two
+// items' scales.
+constexpr int kPitch = kNarrowCols + 4, kPartBytes = kWaves * 16 * kPitch * 4;
+
 // The three kinds of items: of 128 rows, of up to 32, of up to 16.
 constexpr int kWide = 0, kTwo = 1, kOne = 2;
 
@@ -113,6 +115,7 @@ struct Args {
   int64_t nrows;
   int n, k, E, align;
   uint16_t* out;
+  bool fits;                              // a narrow item's scales have room in LDS
 };
 
 // First row of expert e, and its live rows.
@@ -133,12 +136,12 @@ __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) 
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) groups += __shfl_xor(groups, o, kWave);
-  const bool narrow = groups * (p.n / kNarrowCols) <= gridDim.x;
+  const bool narrow = p.fits && groups * (p.n / kNarrowCols) <= gridDim.x;
   int sum[3] = {0, 0, 0};
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
     const int e = e0 + lane, rows = rows_of(sh, p, e, st);
-    const int kind = rows > kMostNarrow && !narrow ? kWide : rows > 16 ? kTwo : kOne;
+    const int kind = (rows > kMostNarrow || !p.fits) && !narrow ? kWide : rows > 16 ? kTwo : kOne;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const int per = i == kWide ? kTileRows : i == kTwo ? kNarrowRows : 16;
@@ -182,37 +185,53 @@ __device__ __forceinline__ Item decode(const Shared& sh, const Args& p, int kind
 
 // ----------------------------------------------------------------- narrow
 
-// 16 kMt rows, 64 columns.  The eight waves take every eighth 128-deep block of the
-// reduction, kRing blocks in flight, across the items; their sums meet in LDS.
+// An item is 16 kMt rows and 64 cs columns: the waves are cs groups of 64
+// columns by 8 / cs parts of the reduction, which take its 128-deep blocks in
+// turn, kRing of them in flight, across the items.  The parts' sums meet in LDS.
+// The item's scales are one contiguous piece of memory, copied to LDS during
+// the item before it: read where they are needed, 4 bytes of a line at a time,
+// they cost more requests than the codes.
 template <int kGroup, int kMt, int kRing>
 __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first_item,
-                                       uint32_t last_item, uint32_t nitems, uint32_t& base,
-                                       int lane, int wid) {
+                                       uint32_t last_item, uint32_t nitems, int cs,
+                                       uint32_t& base, int lane, int wid) {
   constexpr bool kFp4 = kGroup == 0;
-  constexpr int kTiles = kNarrowCols / 16;
-  constexpr int kScBytes = kFp4 ? 4 : 2 * Scales<kGroup>::kPer;  // per column and block
+  constexpr int kTiles = kNarrowCols / 16, kKind = kMt == 2 ? kTwo : kOne;
   constexpr int kG = kFp4 ? 1 : 128 / kGroup, kSteps = 4 / kG;   // groups of a block, MFMAs each
+  constexpr int kStepLoads = kTiles + 4 * kMt;
   if (round_item(base, nitems) >= last_item) return;
   struct Set {
     u32x4 w[kTiles], x[kMt][4];
-    Scales<kGroup> s[kTiles];
   } set[kRing];
   const int c = lane & 15, qd = lane >> 4;
-  const int k = p.k, KB = k / BK, NT = p.n / kNarrowCols;
-  const int nk = (KB - wid + kWaves - 1) / kWaves;  // blocks of this wave per item
-  uint32_t lbase = base;  // loading side
-  int lk = 0;
-  const uint8_t *wp, *sp, *ap[kMt];
-  auto item_of = [&](uint32_t item) __attribute__((always_inline)) {
-    return decode(sh, p, kMt == 2 ? kTwo : kOne, item - first_item, NT, kNarrowCols, 16 * kMt);
+  const int k = p.k, KB = k / BK, cols = kNarrowCols * cs, NT = p.n / cols;
+  const int ks = kWaves / cs, cg = wid % cs, kp = wid / cs;
+  const int nk = max(0, (KB - kp + ks - 1) / ks);   // blocks of this wave per item
+  const int sc_row = KB * Scales<kGroup>::kBytes, sc_bytes = cols * sc_row;
+  const uint32_t sc0 = lds_addr(sh.data) + kPartBytes * kMt;
+  const uint32_t sc_slot = (uint32_t)(sc_bytes + 1023) & ~1023u;
+  const uint32_t sc_lane = sc0 + (uint32_t)((cg * kNarrowCols + c) * sc_row);
+
+  int count = 0;  // items of this workgroup
+  while (round_item(base + count * gridDim.x, nitems) < last_item) ++count;
+  auto item_of = [&](int i) __attribute__((always_inline)) {
+    return decode(sh, p, kKind, round_item(base + i * gridDim.x, nitems) - first_item, NT, cols,
+                  16 * kMt);
   };
+  auto copy_scales = [&](int i) __attribute__((always_inline)) {
+    if (i >= count) return;
+    const Item t = item_of(i);
+    const uint8_t* from = p.sc + ((int64_t)t.e * p.n + t.col) * sc_row;
+    for (int at = wid * 1024; at < sc_bytes; at += kWaves * 1024)
+      dma16_ptr(from + min(at + lane * 16, sc_bytes - 16), sc0 + (i & 1) * sc_slot + at);
+  };
+
+  int li = 0, lk = 0;  // loading side: item and block
+  const uint8_t *wp, *ap[kMt];
   auto open = [&]() __attribute__((always_inline)) {
-    const uint32_t item = round_item(lbase, nitems);
     Item t = {0, 0, 1, 0};  // past the last item: loads of the first weights, unused
-    if (item < last_item) t = item_of(item);
-    const int64_t col = (int64_t)t.e * p.n + t.col + c;
-    wp = p.w + col * (k / 2) + 16 * qd;
-    sp = p.sc + col * KB * kScBytes;
+    if (li < count) t = item_of(li);
+    wp = p.w + ((int64_t)t.e * p.n + t.col + cg * kNarrowCols + c) * (k / 2) + 16 * qd;
     // Rows past the live ones repeat the last one: a row of the result comes
     // from its own row of a alone, and theirs are not stored.
 #pragma unroll
@@ -220,12 +239,10 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
       ap[m] = p.a + ((int64_t)(t.m0 + min(16 * m + c, t.live - 1)) * k + 8 * qd) * 2;
   };
   auto load = [&](Set& s) __attribute__((always_inline)) {
-    const int kb = wid + kWaves * lk;
+    const int kb = kp + ks * lk;
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
+    for (int j = 0; j < kTiles; ++j)
       s.w[j] = *reinterpret_cast<const u32x4*>(wp + (int64_t)j * 8 * k + kb * (BK / 2));
-      s.s[j].load(sp + ((int64_t)j * 16 * KB + kb) * kScBytes);
-    }
 #pragma unroll
     for (int m = 0; m < kMt; ++m)
 #pragma unroll
@@ -233,7 +250,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
         s.x[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + (kb * BK + 32 * i) * 2);
     if (++lk == nk) {
       lk = 0;
-      lbase += gridDim.x;
+      ++li;
       open();
     }
   };
@@ -244,7 +261,10 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
 #pragma unroll
       for (int j = 0; j < kTiles; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
   };
-  auto compute = [&](Set& s) __attribute__((always_inline)) {
+  auto compute = [&](Set& s, uint32_t scales) __attribute__((always_inline)) {
+    Scales<kGroup> sc[kTiles];
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) sc[j].load(scales + (uint32_t)(16 * j * sc_row));
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) exchange(s.w[j]);
 #pragma unroll
@@ -269,7 +289,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
         bf16x8 v[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-          v[i] = kFp4 ? fp4_values(s.w[j][i], s.s[j].get(i)) : int4_values(s.w[j][g * kSteps + i]);
+          v[i] = kFp4 ? fp4_values(s.w[j][i], sc[j].get(i)) : int4_values(s.w[j][g * kSteps + i]);
 #pragma unroll
         for (int m = 0; m < kMt; ++m) {
           v4f part = kFp4 ? acc[m][j] : off[m];
@@ -278,16 +298,15 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
             part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                 __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]), v[i], part, 0, 0, 0);
           if constexpr (kFp4) acc[m][j] = part;
-          else acc[m][j] += part * s.s[j].get(g);
+          else acc[m][j] += part * sc[j].get(g);
         }
       }
     }
   };
-  // Sums of the waves.  Lane: rows 4 qd + 0..3 of column 16 j + c.
-  constexpr int kPitch = kNarrowCols + 4;
+  // Sums of the parts.  Lane: rows 4 qd + 0..3 of column 16 j + c.
   float* part = reinterpret_cast<float*>(sh.data);
-  auto join = [&](uint32_t item) __attribute__((always_inline)) {
-    const Item t = item_of(item);
+  auto join = [&](int i) __attribute__((always_inline)) {
+    const Item t = item_of(i);
 #pragma unroll
     for (int m = 0; m < kMt; ++m)
 #pragma unroll
@@ -295,48 +314,64 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           part[((wid * kMt + m) * 16 + 4 * qd + r) * kPitch + 16 * j + c] = acc[m][j][r];
+    // This wave's copies of the next item's scales, older than its nk blocks'
+    // loads, have landed.
+    wait_ahead<kStepLoads, 5>(min(5, nk));
     wait_lgkm0();
     barrier();
-    const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;
-    if (row < t.live) {
+    const int per = 16 * cs;  // 4 columns to a thread
+    for (int at = threadIdx.x; at < per * t.live; at += kThreads) {
+      const int row = at / per, col = at % per;
+      const float* from = part + ((col >> 4) * 16 * kMt + row) * kPitch + (col & 15) * 4;
       v4f v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i)
-        v += *reinterpret_cast<const v4f*>(part + (i * 16 * kMt + row) * kPitch + col);
+      for (int q = 0; q < ks; ++q)
+        v += *reinterpret_cast<const v4f*>(from + q * cs * 16 * kMt * kPitch);
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2*>(p.out + ((int64_t)t.m0 + row) * p.n + t.col + col) =
+      *reinterpret_cast<u32x2*>(p.out + ((int64_t)t.m0 + row) * p.n + t.col + col * 4) =
           u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
     }
+    copy_scales(i + 2);  // in place of this item's
     wait_lgkm0();
     barrier();  // the partial sums have been read
   };
+  barrier();  // what was in LDS before has been read
+  copy_scales(0);
+  copy_scales(1);
   clear();
-  if (nk <= 0) {  // fewer blocks than waves: this one has nothing to add
-    for (;;) {
-      const uint32_t item = round_item(base, nitems);
-      if (item >= last_item) return;
-      join(item);
-      base += gridDim.x;
-    }
-  }
-  open();
+  if (nk > 0) {
+    open();
 #pragma unroll
-  for (int r = 0; r < kRing; ++r) load(set[r]);
-  int ck = 0;
-  for (;;) {
+    for (int r = 0; r < kRing; ++r) load(set[r]);
+    wait_vmcnt<kRing * kStepLoads>();
+    barrier();  // the first scales have landed
+    int ci = 0, ck = 0;
+    uint32_t scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes);
+    // One way out, at the end of the unrolled blocks (what is computed past the
+    // last item is not used): with a way out after every block the compiler
+    // joins them all into one that leads back to the loop's start, and waits
+    // there for the youngest load.
+    const int steps = count * nk;
+    for (int t = 0; t < steps; t += kRing) {
 #pragma unroll
-    for (int r = 0; r < kRing; ++r) {
-      compute(set[r]);
-      load(set[r]);
-      if (++ck == nk) {
-        ck = 0;
-        join(round_item(base, nitems));
-        clear();
-        base += gridDim.x;
-        if (round_item(base, nitems) >= last_item) return;
+      for (int r = 0; r < kRing; ++r) {
+        compute(set[r], scales);
+        load(set[r]);
+        scales += (uint32_t)(ks * Scales<kGroup>::kBytes);
+        if (++ck == nk && t + r < steps) {
+          ck = 0;
+          join(ci);
+          clear();
+          ++ci;
+          scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes) + (ci & 1) * sc_slot;
+        }
       }
     }
+  } else {  // fewer blocks than parts: this one has nothing to add
+    wait_vmcnt<0>();
+    barrier();
+    for (int i = 0; i < count; ++i) join(i);
   }
+  base += count * gridDim.x;
 }
 
 // ------------------------------------------------------------------- wide
@@ -532,7 +567,11 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   __shared__ Shared sh;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out};
+  // Bytes of 64 columns' scales, and the room for two items of them.
+  const int sc64 = kNarrowCols * (k / BK) * Scales<kGroup>::kBytes;
+  constexpr int kRoom = (kStages * kStageBytes - 2 * kPartBytes) / 2 / 1024 * 1024;
+  const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out,
+                  sc64 <= kRoom};
   for (int e = threadIdx.x; e < E; e += kThreads) sh.pe[e] = psum[e];
   __syncthreads();
   if (wid == 0) list_items(sh, p, lane);
@@ -541,12 +580,23 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   // 256 columns where that makes a round of items or more.
   const int NT256 = (n + 255) / 256, NT128 = n / 128;
   const bool big = kGroup != 32 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
-  const int NTW = big ? NT256 : NT128, NT = n / kNarrowCols;
+  const int NTW = big ? NT256 : NT128;
   const uint32_t nwide = (uint32_t)groups * (uint32_t)NTW;
-  const uint32_t end2 =
-      nwide + (uint32_t)__builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]) * (uint32_t)NT;
-  const uint32_t nitems =
-      end2 + (uint32_t)__builtin_amdgcn_readfirstlane(sh.gp[kOne][E]) * (uint32_t)NT;
+  // Columns of a narrow item: 64, 128, .. 512, whichever takes least by blocks of
+  // 64 columns in a workgroup's rounds, and about six of them for each item's join.
+  const int two = __builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]);
+  const int one = __builtin_amdgcn_readfirstlane(sh.gp[kOne][E]);
+  int cs = 1;
+  uint32_t least = 0xffffffffu;
+  for (int i = 1; i <= kWaves; i *= 2) {
+    if (n % (kNarrowCols * i) || (int64_t)sc64 * i > kRoom) break;
+    const uint32_t items = (uint32_t)(two + one) * (uint32_t)(n / (kNarrowCols * i));
+    const uint32_t cost = (items + gridDim.x - 1) / gridDim.x * (uint32_t)(i * (k / BK) + 6);
+    if (cost < least) least = cost, cs = i;
+  }
+  const int NT = n / (kNarrowCols * cs);
+  const uint32_t end2 = nwide + (uint32_t)two * (uint32_t)NT;
+  const uint32_t nitems = end2 + (uint32_t)one * (uint32_t)NT;
   uint32_t base = 0;
   for (;; base += gridDim.x) {
     const uint32_t item = round_item(base, nitems);
@@ -554,8 +604,8 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
     if (kGroup != 32 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
     else wide<kGroup, 2>(sh, p, item, NTW, lane, wid);
   }
-  narrow<kGroup, 2, kGroup == 32 ? 1 : kGroup ? 2 : 3>(sh, p, nwide, end2, nitems, base, lane, wid);
-  narrow<kGroup, 1, kGroup == 32 ? 3 : 4>(sh, p, end2, nitems, nitems, base, lane, wid);
+  narrow<kGroup, 2, kGroup == 32 ? 1 : kGroup ? 2 : 3>(sh, p, nwide, end2, nitems, cs, base, lane, wid);
+  narrow<kGroup, 1, kGroup == 32 ? 3 : 4>(sh, p, end2, nitems, nitems, cs, base, lane, wid);
 }
 
 }  // namespace

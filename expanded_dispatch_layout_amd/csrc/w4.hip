@@ -97,16 +97,23 @@ constexpr int kABytes = kTileRows * 128, kWBytes = 8192, kSBytes = 2048;
 constexpr int kStageBytes = kABytes + kWBytes + kSBytes;
 constexpr int kLoads = 4;                 // per wave and stage
 
-// Narrow items: partial sums of 16 rows by 64 columns for each wave, then two
-// items' scales.
-constexpr int kPitch = kNarrowCols + 4, kPartBytes = kWaves * 16 * kPitch * 4;
+// Narrow items: partial sums of 16 rows by 64 or 128 columns for each wave, then
+// two items' scales.
+constexpr int kMaxTiles = 8, kPartBytes = kWaves * 16 * (16 * kMaxTiles + 4) * 4;
 
 // The three kinds of items: of 128 rows, of up to 32, of up to 16.
 constexpr int kWide = 0, kTwo = 1, kOne = 2;
 
+struct __attribute__((aligned(16))) Item {
+  int e, col, live, m0;
+};
+constexpr int kRing2 = 1, kRing1 = 1;       // blocks in flight: items of 32 rows, of 16
+constexpr int kListed = 64;               // narrow items that a workgroup looks up at once
+
 struct Shared {
   __attribute__((aligned(1024))) uint8_t data[kStages * kStageBytes];
   int pe[MOE_MAX_EXPERTS];                // psum
+  Item list[kListed];
   int gp[3][MOE_MAX_EXPERTS + 1];         // prefix of each kind's row groups per expert
 };
 
@@ -129,36 +136,42 @@ __device__ __forceinline__ int rows_of(const Shared& sh, const Args& p, int e, i
 // The row groups of every kind.  Experts of more than kMostNarrow rows are wide;
 // where narrow items alone fill no more than a round of the workgroups, none is.
 __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) {
-  int64_t groups = 0;
+  int groups = 0;  // narrow ones; 512 of one expert are more than any grid holds
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
-    groups += (rows_of(sh, p, e0 + lane, st) + kNarrowRows - 1) / kNarrowRows;
+    const int rows = rows_of(sh, p, e0 + lane, st);
+    groups += __builtin_amdgcn_readlane(
+        wave_incl_scan_i(min(512, (rows + kNarrowRows - 1) / kNarrowRows)), 63);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) groups += __shfl_xor(groups, o, kWave);
-  const bool narrow = p.fits && groups * (p.n / kNarrowCols) <= gridDim.x;
-  int sum[3] = {0, 0, 0};
+  const bool narrow = p.fits && (int64_t)groups * (p.n / kNarrowCols) <= gridDim.x;
+  int wide = 0, both = 0;  // both: of 32 rows, and of 16 (<< 16; at most one an expert)
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
     const int e = e0 + lane, rows = rows_of(sh, p, e, st);
-    const int kind = (rows > kMostNarrow || !p.fits) && !narrow ? kWide : rows > 16 ? kTwo : kOne;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int per = i == kWide ? kTileRows : i == kTwo ? kNarrowRows : 16;
-      const int ng = kind == i ? (rows + per - 1) / per : 0;
-      const int incl = wave_incl_scan_i(ng);
-      if (e < p.E) sh.gp[i][e] = sum[i] + incl - ng;
-      sum[i] += __shfl(incl, 63, 64);
+    const bool is_wide = (rows > kMostNarrow || !p.fits) && !narrow;
+    const int nw = is_wide ? (rows + kTileRows - 1) / kTileRows : 0;
+    const int nb = is_wide   ? 0
+                   : rows > 16 ? (rows + kNarrowRows - 1) / kNarrowRows
+                               : (rows > 0) << 16;
+    const int iw = wave_incl_scan_i(nw), ib = wave_incl_scan_i(nb);
+    if (e < p.E) {
+      sh.gp[kWide][e] = wide + iw - nw;
+      sh.gp[kTwo][e] = (both + ib - nb) & 0xffff;
+      sh.gp[kOne][e] = (both + ib - nb) >> 16;
     }
+    wide += __builtin_amdgcn_readlane(iw, 63);
+    both += __builtin_amdgcn_readlane(ib, 63);
   }
-  if (lane < 3) sh.gp[lane][p.E] = lane == 0 ? sum[0] : lane == 1 ? sum[1] : sum[2];
+  if (lane == 0) {
+    sh.gp[kWide][p.E] = wide;
+    sh.gp[kTwo][p.E] = both & 0xffff;
+    sh.gp[kOne][p.E] = both >> 16;
+  }
 }
 
-struct Item {
-  int e, col, live, m0;
-};
 // Item i of a kind: expert by expert, column tile by column tile, the row groups
-// innermost: they read the same weights side by side on one XCD.
+// innermost: they read the same weights side by side on one XCD.  (i may differ
+// between lanes.)
 __device__ __forceinline__ Item decode(const Shared& sh, const Args& p, int kind, uint32_t i,
                                        int NT, int cols, int rows) {
   const int q = (int)(i / (uint32_t)NT);
@@ -169,18 +182,16 @@ __device__ __forceinline__ Item decode(const Shared& sh, const Args& p, int kind
     if (gp[mid] <= q) lo = mid;
     else hi = mid - 1;
   }
-  Item t;
-  t.e = __builtin_amdgcn_readfirstlane(lo);
-  const int g0 = __builtin_amdgcn_readfirstlane(gp[t.e]);
-  const int ge = __builtin_amdgcn_readfirstlane(gp[t.e + 1]) - g0;
+  const int g0 = gp[lo], ge = gp[lo + 1] - g0;
   const int local = (int)(i - (uint32_t)NT * (uint32_t)g0);
   int st = 0;
-  const int all = __builtin_amdgcn_readfirstlane(rows_of(sh, p, t.e, st));
+  const int all = rows_of(sh, p, lo, st);
   const int at = local % ge * rows;
-  t.col = local / ge * cols;
-  t.m0 = __builtin_amdgcn_readfirstlane(st) + at;
-  t.live = min(rows, all - at);
-  return t;
+  return Item{lo, local / ge * cols, min(rows, all - at), st + at};
+}
+__device__ __forceinline__ Item uniform(const Item& t) {
+  return Item{__builtin_amdgcn_readfirstlane(t.e), __builtin_amdgcn_readfirstlane(t.col),
+              __builtin_amdgcn_readfirstlane(t.live), __builtin_amdgcn_readfirstlane(t.m0)};
 }
 
 // ----------------------------------------------------------------- narrow
@@ -191,33 +202,32 @@ __device__ __forceinline__ Item decode(const Shared& sh, const Args& p, int kind
 // The item's scales are one contiguous piece of memory, copied to LDS during
 // the item before it: read where they are needed, 4 bytes of a line at a time,
 // they cost more requests than the codes.
-template <int kGroup, int kMt, int kRing>
+template <int kGroup, int kMt, int kTiles, int kRing>
 __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first_item,
                                        uint32_t last_item, uint32_t nitems, int cs,
                                        uint32_t& base, int lane, int wid) {
   constexpr bool kFp4 = kGroup == 0;
-  constexpr int kTiles = kNarrowCols / 16, kKind = kMt == 2 ? kTwo : kOne;
+  constexpr int kKind = kMt == 2 ? kTwo : kOne, kCols = 16 * kTiles;  // a wave's columns
+  constexpr int kPitch = kCols + 4;                              // of its partial sums
   constexpr int kG = kFp4 ? 1 : 128 / kGroup, kSteps = 4 / kG;   // groups of a block, MFMAs each
   constexpr int kStepLoads = kTiles + 4 * kMt;
-  if (round_item(base, nitems) >= last_item) return;
   struct Set {
     u32x4 w[kTiles], x[kMt][4];
   } set[kRing];
   const int c = lane & 15, qd = lane >> 4;
-  const int k = p.k, KB = k / BK, cols = kNarrowCols * cs, NT = p.n / cols;
+  const int k = p.k, KB = k / BK, cols = kCols * cs, NT = p.n / cols;
   const int ks = kWaves / cs, cg = wid % cs, kp = wid / cs;
-  const int nk = max(0, (KB - kp + ks - 1) / ks);   // blocks of this wave per item
+  const int nk = KB > kp ? (KB - kp + ks - 1) / ks : 0;  // blocks of this wave per item
+  // Steps of every wave per item: those past its blocks load one address and add
+  // nothing.
+  const int steps = ((KB + ks - 1) / ks + kRing - 1) / kRing * kRing;
   const int sc_row = KB * Scales<kGroup>::kBytes, sc_bytes = cols * sc_row;
-  const uint32_t sc0 = lds_addr(sh.data) + kPartBytes * kMt;
+  const uint32_t sc0 = lds_addr(sh.data) + kWaves * 16 * kPitch * 4;
   const uint32_t sc_slot = (uint32_t)(sc_bytes + 1023) & ~1023u;
-  const uint32_t sc_lane = sc0 + (uint32_t)((cg * kNarrowCols + c) * sc_row);
+  const uint32_t sc_lane = sc0 + (uint32_t)((cg * kCols + c) * sc_row);
 
-  int count = 0;  // items of this workgroup
-  while (round_item(base + count * gridDim.x, nitems) < last_item) ++count;
-  auto item_of = [&](int i) __attribute__((always_inline)) {
-    return decode(sh, p, kKind, round_item(base + i * gridDim.x, nitems) - first_item, NT, cols,
-                  16 * kMt);
-  };
+  int count = 0;  // items in the list
+  auto item_of = [&](int i) __attribute__((always_inline)) { return uniform(sh.list[i]); };
   auto copy_scales = [&](int i) __attribute__((always_inline)) {
     if (i >= count) return;
     const Item t = item_of(i);
@@ -226,29 +236,44 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
       dma16_ptr(from + min(at + lane * 16, sc_bytes - 16), sc0 + (i & 1) * sc_slot + at);
   };
 
-  int li = 0, lk = 0;  // loading side: item and block
+  int li = 0, lk = 0;  // loading side: item and step
   const uint8_t *wp, *ap[kMt];
+  int64_t w_step, x_step, w_tile;
+  auto nothing = [&]() __attribute__((always_inline)) {
+    wp = p.w;
+#pragma unroll
+    for (int m = 0; m < kMt; ++m) ap[m] = p.a;
+    w_step = x_step = w_tile = 0;
+  };
   auto open = [&]() __attribute__((always_inline)) {
-    Item t = {0, 0, 1, 0};  // past the last item: loads of the first weights, unused
-    if (li < count) t = item_of(li);
-    wp = p.w + ((int64_t)t.e * p.n + t.col + cg * kNarrowCols + c) * (k / 2) + 16 * qd;
+    if (li >= count || nk == 0) {
+      nothing();
+      return;
+    }
+    const Item t = item_of(li);
+    wp = p.w + ((int64_t)t.e * p.n + t.col + cg * kCols + c) * (k / 2) + 16 * qd +
+         kp * (BK / 2);
     // Rows past the live ones repeat the last one: a row of the result comes
     // from its own row of a alone, and theirs are not stored.
 #pragma unroll
     for (int m = 0; m < kMt; ++m)
-      ap[m] = p.a + ((int64_t)(t.m0 + min(16 * m + c, t.live - 1)) * k + 8 * qd) * 2;
+      ap[m] = p.a + ((int64_t)(t.m0 + min(16 * m + c, t.live - 1)) * k + 8 * qd + kp * BK) * 2;
+    w_step = ks * (BK / 2);
+    x_step = ks * BK * 2;
+    w_tile = (int64_t)8 * k;
   };
   auto load = [&](Set& s) __attribute__((always_inline)) {
-    const int kb = kp + ks * lk;
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j)
-      s.w[j] = *reinterpret_cast<const u32x4*>(wp + (int64_t)j * 8 * k + kb * (BK / 2));
+    for (int j = 0; j < kTiles; ++j) s.w[j] = *reinterpret_cast<const u32x4*>(wp + j * w_tile);
 #pragma unroll
-    for (int m = 0; m < kMt; ++m)
+    for (int m = 0; m < kMt; ++m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s.x[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + (kb * BK + 32 * i) * 2);
-    if (++lk == nk) {
+      for (int i = 0; i < 4; ++i) s.x[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + 64 * i);
+      ap[m] += x_step;
+    }
+    wp += w_step;
+    if (++lk == nk) nothing();
+    if (lk == steps) {
       lk = 0;
       ++li;
       open();
@@ -303,75 +328,75 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
       }
     }
   };
-  // Sums of the parts.  Lane: rows 4 qd + 0..3 of column 16 j + c.
+  // Sums of the parts, 16 rows at a time.  Lane: rows 4 qd + 0..3 of column 16 j + c.
   float* part = reinterpret_cast<float*>(sh.data);
   auto join = [&](int i) __attribute__((always_inline)) {
     const Item t = item_of(i);
+    // This wave's copies of the next item's scales, older than an item's loads,
+    // have landed.
+    wait_vmcnt<kRing * kStepLoads>();
 #pragma unroll
-    for (int m = 0; m < kMt; ++m)
+    for (int m = 0; m < kMt; ++m) {
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          part[((wid * kMt + m) * 16 + 4 * qd + r) * kPitch + 16 * j + c] = acc[m][j][r];
-    // This wave's copies of the next item's scales, older than its nk blocks'
-    // loads, have landed.
-    wait_ahead<kStepLoads, 5>(min(5, nk));
+          part[(wid * 16 + 4 * qd + r) * kPitch + 16 * j + c] = acc[m][j][r];
+      wait_lgkm0();
+      barrier();
+      if (m == 0) copy_scales(i + 2);  // in place of this item's
+      const int per = cols / 4;        // 4 columns to a thread
+      for (int at = threadIdx.x; at < per * min(16, t.live - 16 * m); at += kThreads) {
+        const int row = at / per, col = at % per;
+        const float* from =
+            part + (col / (kCols / 4) * 16 + row) * kPitch + col % (kCols / 4) * 4;
+        v4f v = {0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < ks; ++q)
+          v += *reinterpret_cast<const v4f*>(from + q * cs * 16 * kPitch);
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<u32x2*>(p.out + ((int64_t)t.m0 + 16 * m + row) * p.n + t.col +
+                                  col * 4) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+      }
+      wait_lgkm0();
+      barrier();  // the partial sums have been read
+    }
+  };
+  for (;; base += count * gridDim.x) {
+    // The next items of this workgroup, looked up by a lane each.
+    barrier();  // the list and the scales before have been read
+    const uint32_t mine = round_item(base + lane * gridDim.x, nitems);
+    const bool here = lane < kListed && mine < last_item;
+    count = __popcll(__ballot(here));
+    if (count == 0) return;
+    if (wid == 0 && here)
+      sh.list[lane] = decode(sh, p, kKind, mine - first_item, NT, cols, 16 * kMt);
     wait_lgkm0();
     barrier();
-    const int per = 16 * cs;  // 4 columns to a thread
-    for (int at = threadIdx.x; at < per * t.live; at += kThreads) {
-      const int row = at / per, col = at % per;
-      const float* from = part + ((col >> 4) * 16 * kMt + row) * kPitch + (col & 15) * 4;
-      v4f v = {0.f, 0.f, 0.f, 0.f};
-      for (int q = 0; q < ks; ++q)
-        v += *reinterpret_cast<const v4f*>(from + q * cs * 16 * kMt * kPitch);
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2*>(p.out + ((int64_t)t.m0 + row) * p.n + t.col + col * 4) =
-          u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-    }
-    copy_scales(i + 2);  // in place of this item's
-    wait_lgkm0();
-    barrier();  // the partial sums have been read
-  };
-  barrier();  // what was in LDS before has been read
-  copy_scales(0);
-  copy_scales(1);
-  clear();
-  if (nk > 0) {
+    li = lk = 0;
     open();
+    copy_scales(0);
 #pragma unroll
     for (int r = 0; r < kRing; ++r) load(set[r]);
     wait_vmcnt<kRing * kStepLoads>();
     barrier();  // the first scales have landed
-    int ci = 0, ck = 0;
-    uint32_t scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes);
-    // One way out, at the end of the unrolled blocks (what is computed past the
-    // last item is not used): with a way out after every block the compiler
-    // joins them all into one that leads back to the loop's start, and waits
-    // there for the youngest load.
-    const int steps = count * nk;
-    for (int t = 0; t < steps; t += kRing) {
+    copy_scales(1);
+    // Items of kRing steps at a time and one way out of each loop: with a way out
+    // after every step the compiler joins them all into one that leads back to
+    // the start, and waits there for the youngest load.
+    for (int ci = 0; ci < count; ++ci) {
+      uint32_t scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes) + (ci & 1) * sc_slot;
+      clear();
+      for (int t = 0; t < steps; t += kRing) {
 #pragma unroll
-      for (int r = 0; r < kRing; ++r) {
-        compute(set[r], scales);
-        load(set[r]);
-        scales += (uint32_t)(ks * Scales<kGroup>::kBytes);
-        if (++ck == nk && t + r < steps) {
-          ck = 0;
-          join(ci);
-          clear();
-          ++ci;
-          scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes) + (ci & 1) * sc_slot;
+        for (int r = 0; r < kRing; ++r) {
+          if (t + r < nk) compute(set[r], scales);
+          load(set[r]);
+          scales += (uint32_t)(ks * Scales<kGroup>::kBytes);
         }
       }
+      join(ci);
     }
-  } else {  // fewer blocks than parts: this one has nothing to add
-    wait_vmcnt<0>();
-    barrier();
-    for (int i = 0; i < count; ++i) join(i);
   }
-  base += count * gridDim.x;
 }
 
 // ------------------------------------------------------------------- wide
@@ -392,7 +417,7 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
   constexpr bool kFp4 = kGroup == 0;
   constexpr int kFm = 4, kBn = 64 * kFn;
   const int n = p.n, k = p.k;
-  const Item t = decode(sh, p, kWide, item, NT, kBn, kTileRows);
+  const Item t = uniform(decode(sh, p, kWide, item, NT, kBn, kTileRows));
   const int e = t.e, n0 = t.col, live = t.live;
   const int64_t m0 = t.m0;
   const int wr = wid >> 2, wc = wid & 3, c = lane & 15, qd = lane >> 4;
@@ -567,11 +592,11 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   __shared__ Shared sh;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Bytes of 64 columns' scales, and the room for two items of them.
+  // Bytes of 64 columns' scales, and the room for an item's (of 128, at least).
   const int sc64 = kNarrowCols * (k / BK) * Scales<kGroup>::kBytes;
-  constexpr int kRoom = (kStages * kStageBytes - 2 * kPartBytes) / 2 / 1024 * 1024;
+  constexpr int kRoom = (kStages * kStageBytes - kPartBytes) / 2 / 1024 * 1024;
   const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out,
-                  sc64 <= kRoom};
+                  2 * sc64 <= kRoom};
   for (int e = threadIdx.x; e < E; e += kThreads) sh.pe[e] = psum[e];
   __syncthreads();
   if (wid == 0) list_items(sh, p, lane);
@@ -582,21 +607,27 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   const bool big = kGroup != 32 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
   const int NTW = big ? NT256 : NT128;
   const uint32_t nwide = (uint32_t)groups * (uint32_t)NTW;
-  // Columns of a narrow item: 64, 128, .. 512, whichever takes least by blocks of
-  // 64 columns in a workgroup's rounds, and about six of them for each item's join.
   const int two = __builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]);
   const int one = __builtin_amdgcn_readfirstlane(sh.gp[kOne][E]);
-  int cs = 1;
-  uint32_t least = 0xffffffffu;
-  for (int i = 1; i <= kWaves; i *= 2) {
-    if (n % (kNarrowCols * i) || (int64_t)sc64 * i > kRoom) break;
-    const uint32_t items = (uint32_t)(two + one) * (uint32_t)(n / (kNarrowCols * i));
-    const uint32_t cost = (items + gridDim.x - 1) / gridDim.x * (uint32_t)(i * (k / BK) + 6);
-    if (cost < least) least = cost, cs = i;
-  }
-  const int NT = n / (kNarrowCols * cs);
-  const uint32_t end2 = nwide + (uint32_t)two * (uint32_t)NT;
-  const uint32_t nitems = end2 + (uint32_t)one * (uint32_t)NT;
+  // Groups of columns in a narrow item: 1, 2, 4 or 8, whichever takes least by
+  // blocks of 64 columns in a workgroup's rounds, and about six of them for each item's
+  // join.
+  auto groups_of = [&](int entries, int cols) __attribute__((always_inline)) {
+    int cs = 1;
+    uint32_t least = 0xffffffffu;
+    for (int i = 1; i <= kWaves; i *= 2) {
+      if (n % (cols * i) || (int64_t)(sc64 / kNarrowCols) * cols * i > kRoom) break;
+      const uint32_t items = (uint32_t)entries * (uint32_t)(n / (cols * i));
+      const uint32_t cost =
+          (items + gridDim.x - 1) / gridDim.x * (uint32_t)(i * (cols / kNarrowCols) * (k / BK) + 6);
+      if (cost < least) least = cost, cs = i;
+    }
+    return cs;
+  };
+  constexpr int kTiles2 = 8, kTiles1 = 4;
+  const int cs2 = groups_of(two, 16 * kTiles2), cs1 = groups_of(one, 16 * kTiles1);
+  const uint32_t end2 = nwide + (uint32_t)two * (uint32_t)(n / (16 * kTiles2 * cs2));
+  const uint32_t nitems = end2 + (uint32_t)one * (uint32_t)(n / (16 * kTiles1 * cs1));
   uint32_t base = 0;
   for (;; base += gridDim.x) {
     const uint32_t item = round_item(base, nitems);
@@ -604,8 +635,8 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
     if (kGroup != 32 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
     else wide<kGroup, 2>(sh, p, item, NTW, lane, wid);
   }
-  narrow<kGroup, 2, kGroup == 32 ? 1 : kGroup ? 2 : 3>(sh, p, nwide, end2, nitems, cs, base, lane, wid);
-  narrow<kGroup, 1, kGroup == 32 ? 3 : 4>(sh, p, end2, nitems, nitems, cs, base, lane, wid);
+  narrow<kGroup, 2, kTiles2, kRing2>(sh, p, nwide, end2, nitems, cs2, base, lane, wid);
+  narrow<kGroup, 1, kTiles1, kRing1>(sh, p, end2, nitems, nitems, cs1, base, lane, wid);
 }
 
 }  // namespace

@@ -55,6 +55,38 @@ __device__ __forceinline__ int wave_incl_scan_i(int v) {
   return v;
 }
 
+// Reductions of 64 lanes by the same moves: the result is in every lane.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_move(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, kCtrl, kRows, 0xf, false);
+}
+template <typename F>
+__device__ __forceinline__ int wave_reduce(int none, int v, F&& f) {
+  v = f(v, dpp_move<0x111, 0xf>(none, v));
+  v = f(v, dpp_move<0x112, 0xf>(none, v));
+  v = f(v, dpp_move<0x114, 0xf>(none, v));
+  v = f(v, dpp_move<0x118, 0xf>(none, v));
+  v = f(v, dpp_move<0x142, 0xa>(none, v));
+  v = f(v, dpp_move<0x143, 0xc>(none, v));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+  return __int_as_float(wave_reduce(0, __float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+__device__ __forceinline__ float wave_max_f(float v) {  // without NaN
+  const int none = (int)0xff800000u;                    // -inf
+  return __int_as_float(wave_reduce(none, __float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
+}
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
+  return (uint32_t)wave_reduce(0, (int)v, [](int a, int b) {
+    return (int)max((uint32_t)a, (uint32_t)b);
+  });
+}
+
 // fp32 -> bf16 bits, round to nearest even (NaN stays a quiet NaN).
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   uint32_t u = __float_as_uint(f);

@@ -22,22 +22,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxHidden = 8192;
 
-// Sum over the 64 lanes, the same in every lane.
-template <int kCtrl, int kRows>
-__device__ __forceinline__ float dpp_move(float v) {
-  return __int_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRows, 0xf, false));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_move<0x111, 0xf>(v);  // row_shr:1
-  v += dpp_move<0x112, 0xf>(v);  // row_shr:2
-  v += dpp_move<0x114, 0xf>(v);  // row_shr:4
-  v += dpp_move<0x118, 0xf>(v);  // row_shr:8
-  v += dpp_move<0x142, 0xa>(v);  // row_bcast:15
-  v += dpp_move<0x143, 0xc>(v);  // row_bcast:31
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
 // 8 consecutive values of a bf16 or fp32 array as floats, and back.
 template <bool kF32>
 struct Chunk;
@@ -105,7 +89,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(
   const float inv = 1.0f / (float)hidden;
   int slot = 0;
   auto team_sum = [&](float v) __attribute__((always_inline)) {
-    v = wave_sum(v);
+    v = wave_sum_f(v);
     if constexpr (kTeam > 1) {
       if (lane == 0) part[slot][wid] = v;
       __syncthreads();
@@ -249,8 +233,8 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(
           }
         }
       }
-      s1[u] = wave_sum(s1[u]);
-      s2[u] = wave_sum(s2[u]);
+      s1[u] = wave_sum_f(s1[u]);
+      s2[u] = wave_sum_f(s2[u]);
       if constexpr (kTeam > 1) {
         if (lane == 0) {
           part[slot][wid][2 * u] = s1[u];

@@ -33,13 +33,7 @@ __device__ __forceinline__ float load_logit(const void* x, bool f32, int64_t at)
   const float v = f32 ? ((const float*)x)[at] : bf16_to_f32(((const uint16_t*)x)[at]);
   return v != v ? -INFINITY : fminf(v, FLT_MAX);
 }
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_sum_x(T v) {
+__device__ __forceinline__ double wave_sum_d(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
   return v;
@@ -59,10 +53,30 @@ __device__ __forceinline__ void wave_best(T& key, int& at) {
   }
 }
 
+// The value that one lane holds (the same number of a lane for all).
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+
 struct Sizes {
   int E, topk, groups, topk_groups;
   bool f32, sigmoid, normalize;
 };
+
+// Logits of experts kPer lane + 0 .. kPer - 1; -inf past the last.
+template <int kPer>
+__device__ __forceinline__ void load_row(const void* __restrict__ logits, const Sizes& z,
+                                         int64_t row_at, int lane, float (&x)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = kPer * lane + i;
+    x[i] = e < z.E ? load_logit(logits, z.f32, row_at + e) : -INFINITY;
+  }
+}
 
 // Scores' common factor of a row: maximum and sum of softmax.
 template <int kPer>
@@ -75,7 +89,7 @@ __device__ __forceinline__ void softmax_stats(const float (&x)[kPer], float& top
   if (top == -INFINITY) return;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) total += expf(x[i] - top);
-  total = wave_sum_x(total);
+  total = wave_sum_f(total);
 }
 
 // Weight of the expert this lane holds the id of (logit v, id < 0: none).
@@ -90,7 +104,7 @@ __device__ __forceinline__ float weight_of(float v, int id, const Sizes& z, floa
   const float m = wave_max_f(low);
   float w = here ? expf(low - m) : 0.f;
   if (z.sigmoid && here) w /= 1.0f + expf(-fabsf(v));
-  const float sum = wave_sum_x(w);
+  const float sum = wave_sum_f(w);
   return here ? w / sum : 0.f;
 }
 
@@ -116,7 +130,315 @@ __device__ __forceinline__ int choose(T (&key)[kPer], const Sizes& z, int lane) 
   return mine;
 }
 
+// The choice of one row by exact keys: the logits themselves, or fp64 scores.
 template <int kPer>
+__device__ __forceinline__ int choose_exactly(const void* __restrict__ logits, int64_t row_at,
+                                              const float* __restrict__ bias, const Sizes& z,
+                                              int lane) {
+  float x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 64 * i;
+    x[i] = e < z.E ? load_logit(logits, z.f32, row_at + e) : -INFINITY;
+  }
+  if (!bias && z.groups == 1) return choose<float, kPer>(x, z, lane);
+  double key[kPer];
+  double top = 0.0, sum = 1.0;
+  if (!z.sigmoid) {
+    float t = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t = fmaxf(t, x[i]);
+    t = wave_max_f(t);
+    if (t == -INFINITY) return -1;
+    top = t;
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += exp((double)x[i] - top);
+    sum = wave_sum_d(sum);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    key[i] = -INFINITY;
+    if (x[i] == -INFINITY) continue;
+    key[i] = z.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : exp((double)x[i] - top) / sum;
+    if (bias) {
+      const float b = bias[lane + 64 * i];
+      key[i] = b != b ? -INFINITY : key[i] + (double)fminf(b, FLT_MAX);
+    }
+  }
+  if (z.groups > 1) {
+    const int per = z.E / z.groups;
+    double group = -INFINITY;  // lane g: the sum of group g's two largest keys
+    for (int g = 0; g < z.groups; ++g) {
+      double first = -INFINITY, second = -INFINITY;
+      int at = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 64 * i;
+        if (e / per != g || !(key[i] > -INFINITY)) continue;
+        if (key[i] > first) {
+          second = first;
+          first = key[i];
+          at = e;
+        } else if (key[i] > second) {
+          second = key[i];
+        }
+      }
+      double best = first;
+      int best_at = at;
+      wave_best(best, best_at);
+      if (best == -INFINITY) continue;
+      double rest = best_at == at ? second : first;
+      int none = 0;
+      wave_best(rest, none);
+      if (lane == g) group = rest > -INFINITY ? best + rest : best;
+    }
+    uint64_t chosen = 0;
+    for (int k = 0; k < z.topk_groups; ++k) {
+      double best = group;
+      int at = group > -INFINITY ? lane : 0x7fffffff;
+      wave_best(best, at);
+      if (best == -INFINITY) break;
+      chosen |= 1ull << at;
+      if (lane == at) group = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (!(chosen >> ((lane + 64 * i) / per & 63) & 1)) key[i] = -INFINITY;
+  }
+  return choose<double, kPer>(key, z, lane);
+}
+
+// How far an fp32 key s + b may be from its exact value.  The score s <= 1: exp's
+// argument is off by 2^-24 of itself, which costs at most 2^-24 * x e^-x < 2^-25;
+// exp, the reciprocal and the product a half step or two each; softmax's sum of
+// up to 16 values in a lane and 6 rounds of lanes 22 half steps; 30 * 2^-24 < 2^-19
+// in all.  The sum with b: 2^-24 of the key.
+__device__ __forceinline__ float key_error(float key) {
+  return 0x1p-18f + 0x1p-22f * fabsf(key);
+}
+// fp32 as unsigned numbers of the same order; no finite number is 0.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((uint32_t)~((int)u >> 31) | 0x80000000u));
+}
+
+// Groups of 2^n lanes (kPer experts to a lane): each lane's two largest keys, then
+// its group's.  Returns the sum of the group's two, -inf without any; rank: how
+// many groups come before it.
+template <typename T, int kPer>
+__device__ __forceinline__ T rank_groups(const T (&key)[kPer], const Sizes& z, int lane,
+                                         int lanes, int& rank) {
+  T m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    m2 = max(m2, min(m1, key[i]));
+    m1 = max(m1, key[i]);
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    const T o1 = __shfl_xor(m1, o, kWave), o2 = __shfl_xor(m2, o, kWave);
+    m2 = max(min(m1, o1), max(m2, o2));
+    m1 = max(m1, o1);
+  }
+  const T sum = m2 > (T)-INFINITY ? m1 + m2 : m1;
+  rank = 0;
+  for (int g = 0; g < z.groups; ++g) {
+    const T other = lane_value(sum, g * lanes);
+    rank += other > sum || (other == sum && g < lane / lanes);
+  }
+  return sum;
+}
+
+// The choice by fp32 keys.  A key is an ordered number whose low bits are
+// replaced by the expert, counted down, so that a maximum of 32-bit numbers finds
+// both, and equal ones by the lowest expert.  Lane l holds experts kPer l + 0 ..
+// kPer - 1.  Sets `unsure` where two neighbours of the order, down to the first
+// one left out, lie nearer than the keys' errors (cut bits included) and are not
+// equal logits with equal biases: the row is then chosen exactly.
+template <int kPer>
+__device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
+                                              const void* __restrict__ logits, int64_t row_at,
+                                              const float* __restrict__ bias, const Sizes& z,
+                                              int lane, bool& unsure) {
+  constexpr uint32_t kIndex = 64 * kPer - 1;  // bits of an expert
+  const bool scores = bias || z.groups > 1;
+  float key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = x[i];
+  if (scores) {
+    float top = 0.f, inv = 1.f;
+    if (!z.sigmoid) {
+      float t = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) t = fmaxf(t, x[i]);
+      top = wave_max_f(t);
+      float total = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) total += __expf(x[i] - top);
+      inv = __builtin_amdgcn_rcpf(wave_sum_f(total));
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (x[i] == -INFINITY) continue;
+      key[i] = z.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : __expf(x[i] - top) * inv;
+      if (bias) {
+        const float b = bias[kPer * lane + i];
+        key[i] = b != b ? -INFINITY : key[i] + fminf(b, FLT_MAX);
+      }
+    }
+  }
+  unsure = false;
+  if (z.groups > 1) {
+    const int lanes = z.E / z.groups / kPer;
+    int rank;
+    const float sum = rank_groups<float, kPer>(key, z, lane, lanes, rank);
+    // The last group chosen and the first one left out.
+    if (z.topk_groups < z.groups) {
+      const bool group = lane < z.groups * lanes;
+      const float a = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups - 1)));
+      const float b = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups)));
+      unsure = b > -INFINITY && a - b <= 2 * (key_error(a) + key_error(b));
+    }
+    if (rank >= z.topk_groups) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) key[i] = -INFINITY;
+    }
+  }
+  // Without a bias the order is the logits', also between the groups chosen.
+  if (!bias && z.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = key[i] > -INFINITY ? x[i] : -INFINITY;
+  }
+  uint32_t u[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    u[i] = key[i] > -INFINITY
+               ? (ordered(key[i]) & ~kIndex) | (kIndex - (uint32_t)(kPer * lane + i))
+               : 0u;
+  uint32_t mine = 0, next = 0;  // lane k: the k-th and the one after it
+  for (int k = 0; k <= z.topk; ++k) {
+    uint32_t best = u[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) best = max(best, u[i]);
+    best = wave_max_u(best);
+    if (lane == k) mine = best;
+    if (lane == k - 1) next = best;
+    if (best == 0) break;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) u[i] = u[i] == best ? 0u : u[i];
+  }
+  const bool here = lane < z.topk && mine != 0;
+  const int id = here ? (int)(kIndex - (mine & kIndex)) : -1;
+  if (here && next != 0) {
+    const int other = (int)(kIndex - (next & kIndex));
+    const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
+    const float error = bias ? key_error(hi) + key_error(lo) : 0.f;
+    bool near = hi - lo <= error || (mine & ~kIndex) == (next & ~kIndex);
+    // Is what was cut off nothing, or the two the same?
+    if (near) {
+      const float a = load_logit(logits, z.f32, row_at + id);
+      const float b = load_logit(logits, z.f32, row_at + other);
+      near = a != b || (bias && bias[id] != bias[other]);
+      if (!bias && near) near = (mine & ~kIndex) == (next & ~kIndex);
+    }
+    unsure |= near;
+  }
+  unsure = __ballot(unsure) != 0;
+  return id;
+}
+
+// The same by fp64 keys, for rows that fp32 leaves open.  Rounding the keys to the
+// ordered numbers keeps their order but for equal ones: all that reach the topk-th
+// are lined up, one to a lane, and ranked by the keys themselves.  Returns false
+// where they are more than the lanes (many equal keys).
+template <int kPer>
+__device__ __forceinline__ bool choose_closely(const float (&x)[kPer],
+                                               const float* __restrict__ bias, const Sizes& z,
+                                               int lane, int& id) {
+  constexpr uint32_t kIndex = 64 * kPer - 1;
+  const bool scores = bias || z.groups > 1;
+  double key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = x[i];
+  if (scores) {
+    double top = 0.0, total = 1.0;
+    if (!z.sigmoid) {
+      float t = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) t = fmaxf(t, x[i]);
+      top = wave_max_f(t);
+      total = 0.0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (x[i] > -INFINITY) total += exp((double)x[i] - top);
+      total = wave_sum_d(total);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (x[i] == -INFINITY) continue;
+      key[i] = z.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : exp((double)x[i] - top) / total;
+      if (bias) {
+        const float b = bias[kPer * lane + i];
+        key[i] = b != b ? -INFINITY : key[i] + (double)fminf(b, FLT_MAX);
+      }
+    }
+  }
+  if (z.groups > 1) {
+    int rank;
+    rank_groups<double, kPer>(key, z, lane, z.E / z.groups / kPer, rank);
+    if (rank >= z.topk_groups) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) key[i] = -INFINITY;
+    }
+  }
+  uint32_t u[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    u[i] = key[i] > -INFINITY ? (ordered((float)key[i]) & ~kIndex) |
+                                    (kIndex - (uint32_t)(kPer * lane + i))
+                              : 0u;
+  double mine = -INFINITY;  // lane c: the c-th candidate
+  int expert = -1;
+  uint32_t least = 0;  // what the topk-th one's number is
+  int count = 0;
+  for (;; ++count) {
+    uint32_t best = u[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) best = max(best, u[i]);
+    best = wave_max_u(best);
+    if (best == 0 || (count >= z.topk && (best & ~kIndex) < least)) break;
+    if (count == kWave) return false;
+    if (count == z.topk - 1) least = best & ~kIndex;
+    double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (u[i] == best) {
+        own = key[i];
+        u[i] = 0;
+      }
+    const int e = (int)(kIndex - (best & kIndex));
+    own = lane_value(own, e / kPer);
+    if (lane == count) {
+      mine = own;
+      expert = e;
+    }
+  }
+  int rank = 0;
+  for (int c = 0; c < count; ++c) {
+    const double other = lane_value(mine, c);
+    rank += other > mine || (other == mine && __builtin_amdgcn_readlane(expert, c) < expert);
+  }
+  id = -1;
+  for (int c = 0; c < count; ++c)
+    if (__builtin_amdgcn_readlane(rank, c) == lane) id = __builtin_amdgcn_readlane(expert, c);
+  if (lane >= z.topk) id = -1;
+  return true;
+}
+
+template <int kPer, bool kQuick>
 __global__ __launch_bounds__(kThreads) void router_kernel(
     const void* __restrict__ logits, int64_t stride, const float* __restrict__ bias, Sizes z,
     const int32_t* __restrict__ psum_rank, int nsrc, int64_t rows, int32_t* __restrict__ ids,
@@ -127,81 +449,16 @@ __global__ __launch_bounds__(kThreads) void router_kernel(
   for (int64_t r = (int64_t)blockIdx.x * kWaves + wid; r < nv;
        r += (int64_t)gridDim.x * kWaves) {
     float x[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
-      x[i] = e < z.E ? load_logit(logits, z.f32, r * stride + e) : -INFINITY;
+    load_row<kPer>(logits, z, r * stride, lane, x);
+    int id = -1;
+    bool unsure = true;
+    if constexpr (kQuick) {
+      id = choose_quickly<kPer>(x, logits, r * stride, bias, z, lane, unsure);
+      if (unsure) unsure = !choose_closely<kPer>(x, bias, z, lane, id);
     }
+    if (unsure) id = choose_exactly<kPer>(logits, r * stride, bias, z, lane);
     float top = 0.f, total = 1.f;
-    int id;
-    if (!bias && z.groups == 1) {
-      if (!z.sigmoid && !z.normalize) softmax_stats<kPer>(x, top, total);
-      id = choose<float, kPer>(x, z, lane);
-    } else {
-      double key[kPer];
-      if (!z.sigmoid) softmax_stats<kPer>(x, top, total);
-      double sum = 1.0;
-      if (!z.sigmoid) {
-        sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (top > -INFINITY) sum += exp((double)x[i] - (double)top);
-        sum = wave_sum_x(sum);
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = -INFINITY;
-        if (x[i] == -INFINITY) continue;
-        key[i] = z.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i]))
-                           : exp((double)x[i] - (double)top) / sum;
-        if (bias) {
-          const float b = bias[e];
-          key[i] = b != b ? -INFINITY : key[i] + (double)fminf(b, FLT_MAX);
-        }
-      }
-      if (z.groups > 1) {
-        const int per = z.E / z.groups;
-        double group = -INFINITY;  // lane g: the sum of group g's two largest keys
-        for (int g = 0; g < z.groups; ++g) {
-          double first = -INFINITY, second = -INFINITY;
-          int at = 0x7fffffff;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 64 * i;
-            if (e / per != g || !(key[i] > -INFINITY)) continue;
-            if (key[i] > first) {
-              second = first;
-              first = key[i];
-              at = e;
-            } else if (key[i] > second) {
-              second = key[i];
-            }
-          }
-          double best = first;
-          int best_at = at;
-          wave_best(best, best_at);
-          if (best == -INFINITY) continue;
-          double rest = best_at == at ? second : first;
-          int none = 0;
-          wave_best(rest, none);
-          if (lane == g) group = rest > -INFINITY ? best + rest : best;
-        }
-        uint64_t chosen = 0;
-        for (int k = 0; k < z.topk_groups; ++k) {
-          double best = group;
-          int at = group > -INFINITY ? lane : 0x7fffffff;
-          wave_best(best, at);
-          if (best == -INFINITY) break;
-          chosen |= 1ull << at;
-          if (lane == at) group = -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (!(chosen >> ((lane + 64 * i) / per & 63) & 1)) key[i] = -INFINITY;
-      }
-      id = choose<double, kPer>(key, z, lane);
-    }
+    if (!z.sigmoid && !z.normalize) softmax_stats<kPer>(x, top, total);
     float v = 0.f;
     if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
     const float w = weight_of(v, id, z, top, total);
@@ -228,11 +485,7 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(
 #pragma unroll
     for (int i = 0; i < kPer; ++i) d[i] = 0.f;
     if (dense) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 64 * i;
-        x[i] = e < z.E ? load_logit(logits, z.f32, r * stride + e) : -INFINITY;
-      }
+      load_row<kPer>(logits, z, r * stride, lane, x);
       softmax_stats<kPer>(x, top, total);
     }
     int id = -1;
@@ -247,20 +500,20 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(
       }
     }
     const float w = weight_of(v, id, z, top, total);
-    const float dot = wave_sum_x(w * g);
+    const float dot = wave_sum_f(w * g);
     float own;  // what the chosen experts get by themselves
     if (z.sigmoid) own = w * (1.0f / (1.0f + expf(v))) * (z.normalize ? g - dot : g);
     else own = w * (z.normalize ? g - dot : g);
     for (int k = 0; k < z.topk; ++k) {
-      const int e = __shfl(id, k, kWave);
-      const float o = __shfl(own, k, kWave);
+      const int e = __builtin_amdgcn_readlane(id, k);
+      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(own), k));
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (e == lane + 64 * i) d[i] += o;
+        if (e == kPer * lane + i) d[i] += o;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
+      const int e = kPer * lane + i;
       if (e >= z.E) continue;
       if (dense && x[i] > -INFINITY) d[i] -= expf(x[i] - top) / total * dot;
       if (z.f32) ((float*)dx)[r * dx_stride + e] = d[i];
@@ -323,11 +576,16 @@ extern "C" moe_status moe_router(const void* logits, int64_t logits_stride, moe_
   if (rows == 0) return MOE_OK;
   const Sizes z = {num_experts,          topk, num_groups, topk_groups, fmt == MOE_FLOAT_F32,
                    score == MOE_SCORE_SIGMOID, normalize != 0};
-  auto kern = num_experts <= 64    ? router_kernel<1>
-              : num_experts <= 128 ? router_kernel<2>
-              : num_experts <= 256 ? router_kernel<4>
-              : num_experts <= 512 ? router_kernel<8>
-                                   : router_kernel<16>;
+  // Groups are quick where each is 2^n lanes.
+  const int per = num_experts <= 64 ? 1 : num_experts <= 128 ? 2 : num_experts <= 256 ? 4
+                  : num_experts <= 512 ? 8 : 16;
+  const int size = num_experts / num_groups, lanes = size / per;
+  const bool quick = num_groups == 1 || (size % per == 0 && (lanes & (lanes - 1)) == 0);
+  auto kern = per == 1   ? (quick ? router_kernel<1, true> : router_kernel<1, false>)
+              : per == 2 ? (quick ? router_kernel<2, true> : router_kernel<2, false>)
+              : per == 4 ? (quick ? router_kernel<4, true> : router_kernel<4, false>)
+              : per == 8 ? (quick ? router_kernel<8, true> : router_kernel<8, false>)
+                         : (quick ? router_kernel<16, true> : router_kernel<16, false>);
   hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(rows)), dim3(kThreads), 0,
                      reinterpret_cast<hipStream_t>(stream), logits, logits_stride, bias, z,
                      psum_recv_per_rank, num_src_ranks, rows, topk_ids, topk_weights);

@@ -438,6 +438,33 @@ __device__ __forceinline__ bool choose_closely(const float (&x)[kPer],
   return true;
 }
 
+// One row by a whole wave.  kQuick: fp32 keys have been or are to be tried.
+template <int kPer, bool kQuick>
+__device__ __forceinline__ void route_row(const void* __restrict__ logits, int64_t stride,
+                                          const float* __restrict__ bias, const Sizes& z,
+                                          int64_t r, int lane, bool tried,
+                                          int32_t* __restrict__ ids,
+                                          float* __restrict__ weights) {
+  float x[kPer];
+  load_row<kPer>(logits, z, r * stride, lane, x);
+  int id = -1;
+  bool unsure = true;
+  if constexpr (kQuick) {
+    if (!tried) id = choose_quickly<kPer>(x, logits, r * stride, bias, z, lane, unsure);
+    if (unsure) unsure = !choose_closely<kPer>(x, bias, z, lane, id);
+  }
+  if (unsure) id = choose_exactly<kPer>(logits, r * stride, bias, z, lane);
+  float top = 0.f, total = 1.f;
+  if (!z.sigmoid && !z.normalize) softmax_stats<kPer>(x, top, total);
+  float v = 0.f;
+  if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
+  const float w = weight_of(v, id, z, top, total);
+  if (lane < z.topk) {
+    ids[r * z.topk + lane] = id;
+    weights[r * z.topk + lane] = w;
+  }
+}
+
 template <int kPer, bool kQuick>
 __global__ __launch_bounds__(kThreads) void router_kernel(
     const void* __restrict__ logits, int64_t stride, const float* __restrict__ bias, Sizes z,
@@ -447,24 +474,191 @@ __global__ __launch_bounds__(kThreads) void router_kernel(
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nv = valid_rows(psum_rank, nsrc, rows);
   for (int64_t r = (int64_t)blockIdx.x * kWaves + wid; r < nv;
-       r += (int64_t)gridDim.x * kWaves) {
+       r += (int64_t)gridDim.x * kWaves)
+    route_row<kPer, kQuick>(logits, stride, bias, z, r, lane, false, ids, weights);
+}
+
+// Reductions of 16 lanes, by rotations: the result is in every lane.
+template <typename F>
+__device__ __forceinline__ int row_reduce(int v, F&& f) {
+  v = f(v, dpp_move<0x128, 0xf>(v, v));  // row_ror:8
+  v = f(v, dpp_move<0x124, 0xf>(v, v));
+  v = f(v, dpp_move<0x122, 0xf>(v, v));
+  v = f(v, dpp_move<0x121, 0xf>(v, v));
+  return v;
+}
+__device__ __forceinline__ uint32_t row_max_u(uint32_t v) {
+  return (uint32_t)row_reduce((int)v,
+                              [](int a, int b) { return (int)max((uint32_t)a, (uint32_t)b); });
+}
+__device__ __forceinline__ float row_max_f(float v) {
+  return __int_as_float(row_reduce(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float row_sum_f(float v) {
+  return __int_as_float(row_reduce(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+
+// The k-th largest number, given the one before it and the largest distance from
+// it (wrapped round): 0 once there is none.
+__device__ __forceinline__ uint32_t below(int k, uint32_t before, uint32_t distance) {
+  return k > 0 && before == 0 ? 0u : before + distance;
+}
+
+// Four rows to a wave, 16 lanes each, for up to 15 choices out of up to 256
+// experts: the reductions of a choice are half as long and serve four rows
+// (16384 rows of 256 experts, 8 chosen: KNOWN us, 33 with a wave to a row).  The
+// choice is choose_quickly's, with kPer experts to a lane; a row that it leaves
+// open is taken by the whole wave afterwards.
+// The next choice is found without taking the last one out: of all numbers minus
+// the last maximum, wrapped round, the largest is the next one below it.
+// (Numbers of 0, which no expert has, are below all: there are some wherever the
+// experts do not suffice.)
+template <int kPer>
+__global__ __launch_bounds__(kThreads) void router_quad_kernel(
+    const void* __restrict__ logits, int64_t stride, const float* __restrict__ bias, Sizes z,
+    bool wide_loads, const int32_t* __restrict__ psum_rank, int nsrc, int64_t rows,
+    int32_t* __restrict__ ids, float* __restrict__ weights) {
+  constexpr uint32_t kIndex = 16 * kPer - 1;
+  const int lane = threadIdx.x & 63, ql = lane & 15;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t nv = valid_rows(psum_rank, nsrc, rows);
+  const bool scores = bias || z.groups > 1;
+  float b[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = kPer * ql + i;
+    b[i] = bias && e < z.E ? bias[e] : 0.f;
+    b[i] = b[i] != b[i] ? -INFINITY : fminf(b[i], FLT_MAX);
+  }
+  for (int64_t r0 = ((int64_t)blockIdx.x * kWaves + wid) * 4; r0 < nv;
+       r0 += (int64_t)gridDim.x * kWaves * 4) {
+    const int64_t r = min(r0 + (lane >> 4), nv - 1);  // rows past the last: the last again
+    const bool real = r0 + (lane >> 4) < nv;
+    const int64_t at = r * stride + kPer * ql;
     float x[kPer];
-    load_row<kPer>(logits, z, r * stride, lane, x);
-    int id = -1;
-    bool unsure = true;
-    if constexpr (kQuick) {
-      id = choose_quickly<kPer>(x, logits, r * stride, bias, z, lane, unsure);
-      if (unsure) unsure = !choose_closely<kPer>(x, bias, z, lane, id);
+    if (wide_loads) {  // fp32, every expert there
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4) {
+        typedef float v4f __attribute__((ext_vector_type(4)));
+        const v4f v = *reinterpret_cast<const v4f*>((const float*)logits + at + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i + j] = fminf(fmaxf(v[j], -INFINITY), FLT_MAX);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        x[i] = kPer * ql + i < z.E ? load_logit(logits, z.f32, at + i) : -INFINITY;
     }
-    if (unsure) id = choose_exactly<kPer>(logits, r * stride, bias, z, lane);
     float top = 0.f, total = 1.f;
-    if (!z.sigmoid && !z.normalize) softmax_stats<kPer>(x, top, total);
+    if (!z.sigmoid && (scores || !z.normalize)) {
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+      top = row_max_f(top);
+      total = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) total += x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+      total = row_sum_f(total);
+    }
+    float key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = x[i];
+    if (scores) {
+      const float inv = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float s =
+            z.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : __expf(x[i] - top) * inv;
+        key[i] = x[i] > -INFINITY ? s + b[i] : -INFINITY;
+      }
+    }
+    bool unsure = false;
+    if (z.groups > 1) {  // of 2^n lanes
+      const int lanes = z.E / z.groups / kPer;
+      float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        m2 = fmaxf(m2, fminf(m1, key[i]));
+        m1 = fmaxf(m1, key[i]);
+      }
+      for (int o = 1; o < lanes; o <<= 1) {
+        const float o1 = __shfl_xor(m1, o, kWave), o2 = __shfl_xor(m2, o, kWave);
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      }
+      // Ordered numbers of the sums, the group in the low four bits; lanes past
+      // the experts have none.
+      const float sum = m2 > -INFINITY ? m1 + m2 : m1;
+      const int g = ql / lanes;
+      uint32_t u = sum > -INFINITY && g < z.groups ? (ordered(sum) & ~15u) | (15u - g) : 0u;
+      uint32_t best = 0, last = 0;
+      for (int k = 0; k <= z.topk_groups; ++k) {
+        last = best;
+        best = below(k, best, row_max_u(u - best));
+      }
+      // last: the topk_groups-th, best: the first one left out (0: none is).
+      const float lo = unordered(last & ~15u), hi = unordered(best | 15u);
+      unsure = best != 0 && z.topk_groups < z.groups &&
+               lo - hi <= 2 * (key_error(lo) + key_error(hi));
+      const bool in = u != 0 && u >= last;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) key[i] = in && key[i] > -INFINITY ? (bias ? key[i] : x[i])
+                                                                       : -INFINITY;
+    }
+    uint32_t u[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      u[i] = key[i] > -INFINITY
+                 ? (ordered(key[i]) & ~kIndex) | (kIndex - (uint32_t)(kPer * ql + i))
+                 : 0u;
+    uint32_t mine = 0, best = 0;  // lane k of the row: the k-th
+    for (int k = 0; k <= z.topk; ++k) {
+      uint32_t m = u[0] - best;
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) m = max(m, u[i] - best);
+      best = below(k, best, row_max_u(m));
+      if (ql == k) mine = best;
+    }
+    const uint32_t next = (uint32_t)dpp_move<0x101, 0xf>(0, (int)mine);  // row_shl:1
+    const bool here = ql < z.topk && mine != 0;
+    const int id = here ? (int)(kIndex - (mine & kIndex)) : -1;
     float v = 0.f;
-    if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
-    const float w = weight_of(v, id, z, top, total);
-    if (lane < z.topk) {
-      ids[r * z.topk + lane] = id;
-      weights[r * z.topk + lane] = w;
+    if (here) v = load_logit(logits, z.f32, r * stride + id);
+    if (here && next != 0) {
+      const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
+      const bool same = (mine & ~kIndex) == (next & ~kIndex);
+      if (same || (bias && hi - lo <= key_error(hi) + key_error(lo))) {
+        const int other = (int)(kIndex - (next & kIndex));
+        unsure |= v != load_logit(logits, z.f32, r * stride + other) ||
+                  (bias && bias[id] != bias[other]);
+      }
+    }
+    float w;
+    if (z.normalize) {
+      const float low = here ? (z.sigmoid ? fminf(v, 0.f) : v) : -INFINITY;
+      const float m = row_max_f(low);
+      w = here ? expf(low - m) : 0.f;
+      if (z.sigmoid) w /= 1.0f + expf(-fabsf(v));
+      const float sum = row_sum_f(w);
+      w = here ? w / sum : 0.f;
+    } else {
+      w = !here ? 0.f : z.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top) / total;
+    }
+    const uint64_t open = __ballot(unsure && real);
+    const bool again = (open >> (lane & 48) & 0xffff) != 0;
+    if (real && !again && ql < z.topk) {
+      ids[r * z.topk + ql] = id;
+      weights[r * z.topk + ql] = w;
+    }
+    if (open) {
+      for (int q = 0; q < 4; ++q)
+        if (open >> (16 * q) & 0xffff)
+          route_row<(kPer + 3) / 4, true>(logits, stride, bias, z, r0 + q, lane, true, ids,
+                                          weights);
     }
   }
 }
@@ -576,11 +770,30 @@ extern "C" moe_status moe_router(const void* logits, int64_t logits_stride, moe_
   if (rows == 0) return MOE_OK;
   const Sizes z = {num_experts,          topk, num_groups, topk_groups, fmt == MOE_FLOAT_F32,
                    score == MOE_SCORE_SIGMOID, normalize != 0};
-  // Groups are quick where each is 2^n lanes.
+  // Four rows to a wave, or one.  Groups are quick where each is 2^n lanes of
+  // either.
+  const int size = num_experts / num_groups;
+  auto fits = [&](int per) {
+    const int lanes = size / per;
+    return num_groups == 1 || (size % per == 0 && (lanes & (lanes - 1)) == 0);
+  };
+  const int quad = num_experts <= 64 ? 4 : num_experts <= 128 ? 8 : 16;
+  if (num_experts <= 256 && topk < 16 && fits(quad) && fits((quad + 3) / 4)) {
+    const bool wide_loads = z.f32 && num_experts == 16 * quad && (uintptr_t)logits % 16 == 0 &&
+                            logits_stride % 4 == 0;
+    const int64_t blocks = (rows + 4 * kWaves - 1) / (4 * kWaves);
+    auto kern = quad == 4   ? router_quad_kernel<4>
+                : quad == 8 ? router_quad_kernel<8>
+                            : router_quad_kernel<16>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0,
+                       reinterpret_cast<hipStream_t>(stream), logits, logits_stride, bias, z,
+                       wide_loads, psum_recv_per_rank, num_src_ranks, rows, topk_ids,
+                       topk_weights);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+  }
   const int per = num_experts <= 64 ? 1 : num_experts <= 128 ? 2 : num_experts <= 256 ? 4
                   : num_experts <= 512 ? 8 : 16;
-  const int size = num_experts / num_groups, lanes = size / per;
-  const bool quick = num_groups == 1 || (size % per == 0 && (lanes & (lanes - 1)) == 0);
+  const bool quick = fits(per);
   auto kern = per == 1   ? (quick ? router_kernel<1, true> : router_kernel<1, false>)
               : per == 2 ? (quick ? router_kernel<2, true> : router_kernel<2, false>)
               : per == 4 ? (quick ? router_kernel<4, true> : router_kernel<4, false>)

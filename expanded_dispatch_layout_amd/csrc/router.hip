@@ -209,13 +209,14 @@ __device__ __forceinline__ int choose_exactly(const void* __restrict__ logits, i
   return choose<double, kPer>(key, z, lane);
 }
 
-// How far an fp32 key s + b may be from its exact value.  The score s <= 1: exp's
-// argument is off by 2^-24 of itself, which costs at most 2^-24 * x e^-x < 2^-25;
-// exp, the reciprocal and the product a half step or two each; softmax's sum of
-// up to 16 values in a lane and 6 rounds of lanes 22 half steps; 30 * 2^-24 < 2^-19
-// in all.  The sum with b: 2^-24 of the key.
-__device__ __forceinline__ float key_error(float key) {
-  return 0x1p-18f + 0x1p-22f * fabsf(key);
+// How far an fp32 key s + b may be from its exact value, in units of 2^-24 for
+// s <= 1.  exp's argument is off by two half steps, which cost at most 2 * x e^-x /
+// (1 + e^-x)^2 < 0.5 for the sigmoid and 2 * x e^-x < 0.8 for softmax; exp itself 2,
+// of which the sigmoid takes a quarter; 1 + e 1; the reciprocal and product 3;
+// softmax's sum of up to 16 values in a lane and 6 rounds of lanes 22.  So below 5 and
+// 29; 8 and 64 are taken.  The sum with b: 1 of the key; 4 is taken.
+__device__ __forceinline__ float key_error(float key, bool sigmoid) {
+  return (sigmoid ? 0x1p-21f : 0x1p-18f) + 0x1p-22f * fabsf(key);
 }
 // fp32 as unsigned numbers of the same order; no finite number is 0.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -300,7 +301,7 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
       const bool group = lane < z.groups * lanes;
       const float a = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups - 1)));
       const float b = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups)));
-      unsure = b > -INFINITY && a - b <= 2 * (key_error(a) + key_error(b));
+      unsure = b > -INFINITY && a - b <= 2 * (key_error(a, z.sigmoid) + key_error(b, z.sigmoid));
     }
     if (rank >= z.topk_groups) {
 #pragma unroll
@@ -335,7 +336,7 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
   if (here && next != 0) {
     const int other = (int)(kIndex - (next & kIndex));
     const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
-    const float error = bias ? key_error(hi) + key_error(lo) : 0.f;
+    const float error = bias ? key_error(hi, z.sigmoid) + key_error(lo, z.sigmoid) : 0.f;
     bool near = hi - lo <= error || (mine & ~kIndex) == (next & ~kIndex);
     // Is what was cut off nothing, or the two the same?
     if (near) {
@@ -508,11 +509,19 @@ __device__ __forceinline__ uint32_t below(int k, uint32_t before, uint32_t dista
   return k > 0 && before == 0 ? 0u : before + distance;
 }
 
-// Four rows to a wave, 16 lanes each, for up to 15 choices out of up to 256
+// Key of one expert in fp64; softmax, which is only compared with its own row
+// here, without its sum.
+__device__ __forceinline__ double exact_key(float v, float b, const Sizes& z, float top) {
+  return z.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) + (double)b : exp((double)v - (double)top);
+}
+
+// Four rows to a wave, 16 lanes each, for up to 14 choices out of up to 256
 // experts: the reductions of a choice are half as long and serve four rows
 // (16384 rows of 256 experts, 8 chosen: KNOWN us, 33 with a wave to a row).  The
-// choice is choose_quickly's, with kPer experts to a lane; a row that it leaves
-// open is taken by the whole wave afterwards.
+// choice is choose_quickly's, with kPer experts to a lane.  What it leaves open is
+// settled by fp64 keys of the few that matter; where these do not do, a row is
+// taken by the whole wave afterwards (with rows left to that whenever two keys are
+// near, one in 170, it took KNOWN us: whoever has one ends last).
 // The next choice is found without taking the last one out: of all numbers minus
 // the last maximum, wrapped round, the largest is the next one below it.
 // (Numbers of 0, which no expert has, are below all: there are some wherever the
@@ -527,6 +536,8 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nv = valid_rows(psum_rank, nsrc, rows);
   const bool scores = bias || z.groups > 1;
+  // Can a lane tell an exact key by itself?  (Softmax's sum would be fp64, too.)
+  const bool exact = z.sigmoid || !bias;
   float b[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -603,8 +614,42 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       // last: the topk_groups-th, best: the first one left out (0: none is).
       const float lo = unordered(last & ~15u), hi = unordered(best | 15u);
       unsure = best != 0 && z.topk_groups < z.groups &&
-               lo - hi <= 2 * (key_error(lo) + key_error(hi));
-      const bool in = u != 0 && u >= last;
+               lo - hi <= 2 * (key_error(lo, z.sigmoid) + key_error(hi, z.sigmoid));
+      bool in = u != 0 && u >= last;
+      if (exact && __ballot(unsure)) {
+        // fp64 sums of the two largest, from those that may be among them.
+        float cut = m2 > -INFINITY ? m2 : m1;
+        cut -= 2 * key_error(cut, z.sigmoid);
+        uint32_t todo = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          todo |= (uint32_t)(key[i] > -INFINITY && key[i] >= cut) << i;
+        double d1 = -INFINITY, d2 = -INFINITY;
+        while (__ballot(todo != 0)) {
+          const int at_i = __builtin_ctz(todo | 0x10000u);
+          float xv = 0.f, bv = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (i == at_i) xv = x[i], bv = b[i];
+          const double d = todo ? exact_key(xv, bv, z, top) : -INFINITY;
+          d2 = max(d2, min(d1, d));
+          d1 = max(d1, d);
+          todo &= todo - 1;
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+          const double o1 = __shfl_xor(d1, o, kWave), o2 = __shfl_xor(d2, o, kWave);
+          d2 = max(min(d1, o1), max(d2, o2));
+          d1 = max(d1, o1);
+        }
+        const double both = d2 > -INFINITY ? d1 + d2 : d1;
+        int rank = 0;
+        for (int j = 0; j < z.groups; ++j) {
+          const double other = __shfl(both, (lane & 48) + j * lanes, kWave);
+          rank += other > both || (other == both && j < g);
+        }
+        in = u != 0 && rank < z.topk_groups;
+        unsure = false;
+      }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) key[i] = in && key[i] > -INFINITY ? (bias ? key[i] : x[i])
                                                                        : -INFINITY;
@@ -616,7 +661,7 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
                  ? (ordered(key[i]) & ~kIndex) | (kIndex - (uint32_t)(kPer * ql + i))
                  : 0u;
     uint32_t mine = 0, best = 0;  // lane k of the row: the k-th
-    for (int k = 0; k <= z.topk; ++k) {
+    for (int k = 0; k < z.topk + 2; ++k) {
       uint32_t m = u[0] - best;
 #pragma unroll
       for (int i = 1; i < kPer; ++i) m = max(m, u[i] - best);
@@ -624,19 +669,45 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       if (ql == k) mine = best;
     }
     const uint32_t next = (uint32_t)dpp_move<0x101, 0xf>(0, (int)mine);  // row_shl:1
-    const bool here = ql < z.topk && mine != 0;
-    const int id = here ? (int)(kIndex - (mine & kIndex)) : -1;
+    int id = mine != 0 ? (int)(kIndex - (mine & kIndex)) : -1;
     float v = 0.f;
-    if (here) v = load_logit(logits, z.f32, r * stride + id);
-    if (here && next != 0) {
+    if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
+    bool near = false;  // the order of this one and the next is open
+    if (ql < z.topk && next != 0) {
       const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
-      const bool same = (mine & ~kIndex) == (next & ~kIndex);
-      if (same || (bias && hi - lo <= key_error(hi) + key_error(lo))) {
+      const float error = key_error(hi, z.sigmoid) + key_error(lo, z.sigmoid);
+      if ((mine & ~kIndex) == (next & ~kIndex) || (bias && hi - lo <= error)) {
         const int other = (int)(kIndex - (next & kIndex));
-        unsure |= v != load_logit(logits, z.f32, r * stride + other) ||
-                  (bias && bias[id] != bias[other]);
+        near = v != load_logit(logits, z.f32, r * stride + other) ||
+               (bias && bias[id] != bias[other]);
       }
     }
+    if (!exact) {
+      unsure |= near;
+    } else if (__ballot(near)) {
+      // The topk + 2 that are lined up, by their exact keys.  What was not lined up
+      // lies below the last of them: it has to lie below the topk-th key, too.
+      float bv = 0.f;
+      if (bias && id >= 0) bv = fminf(bias[id], FLT_MAX);
+      const double d = id < 0 ? -INFINITY : bias ? exact_key(v, bv, z, top) : (double)v;
+      int rank = 0;
+      for (int j = 0; j < z.topk + 2; ++j) {
+        const double other = __shfl(d, (lane & 48) + j, kWave);
+        const int oid = __shfl(id, (lane & 48) + j, kWave);
+        // (Lanes without an expert, -1, keep their order.)
+        rank += other > d || (other == d && ((uint32_t)oid < (uint32_t)id ||
+                                             (oid == id && j < ql)));
+      }
+      const float end = unordered(best | kIndex);
+      unsure |= rank == z.topk - 1 && best != 0 &&
+                d <= (double)end + (bias ? key_error(end, z.sigmoid) : 0.f);
+      const int from = ql < z.topk + 2 ? rank : ql;  // a place of its own for every lane
+      id = __builtin_amdgcn_ds_permute(((lane & 48) + from) * 4, id);
+      v = __int_as_float(
+          __builtin_amdgcn_ds_permute(((lane & 48) + from) * 4, __float_as_int(v)));
+    }
+    const bool here = ql < z.topk && id >= 0;
+    if (!here) id = -1;
     float w;
     if (z.normalize) {
       const float low = here ? (z.sigmoid ? fminf(v, 0.f) : v) : -INFINITY;
@@ -778,7 +849,7 @@ extern "C" moe_status moe_router(const void* logits, int64_t logits_stride, moe_
     return num_groups == 1 || (size % per == 0 && (lanes & (lanes - 1)) == 0);
   };
   const int quad = num_experts <= 64 ? 4 : num_experts <= 128 ? 8 : 16;
-  if (num_experts <= 256 && topk < 16 && fits(quad) && fits((quad + 3) / 4)) {
+  if (num_experts <= 256 && topk < 15 && fits(quad) && fits((quad + 3) / 4)) {
     const bool wide_loads = z.f32 && num_experts == 16 * quad && (uintptr_t)logits % 16 == 0 &&
                             logits_stride % 4 == 0;
     const int64_t blocks = (rows + 4 * kWaves - 1) / (4 * kWaves);

@@ -67,6 +67,19 @@ struct Sizes {
   bool f32, sigmoid, normalize;
 };
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// kPer fp32 logits or biases, 16 bytes at a time; NaN becomes -inf.
+template <int kPer>
+__device__ __forceinline__ void load_wide(const float* p, float (&x)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {
+    const v4f v = *reinterpret_cast<const v4f*>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[i + j] = fminf(fmaxf(v[j], -INFINITY), FLT_MAX);
+  }
+}
+
 // Logits of experts kPer lane + 0 .. kPer - 1; -inf past the last.
 template <int kPer>
 __device__ __forceinline__ void load_row(const void* __restrict__ logits, const Sizes& z,
@@ -539,11 +552,15 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
   // Can a lane tell an exact key by itself?  (Softmax's sum would be fp64, too.)
   const bool exact = z.sigmoid || !bias;
   float b[kPer];
+  if (bias && wide_loads) {
+    load_wide<kPer>(bias + kPer * ql, b);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = kPer * ql + i;
-    b[i] = bias && e < z.E ? bias[e] : 0.f;
-    b[i] = b[i] != b[i] ? -INFINITY : fminf(b[i], FLT_MAX);
+    for (int i = 0; i < kPer; ++i) {
+      const int e = kPer * ql + i;
+      b[i] = bias && e < z.E ? bias[e] : 0.f;
+      b[i] = fminf(fmaxf(b[i], -INFINITY), FLT_MAX);  // NaN: -inf
+    }
   }
   for (int64_t r0 = ((int64_t)blockIdx.x * kWaves + wid) * 4; r0 < nv;
        r0 += (int64_t)gridDim.x * kWaves * 4) {
@@ -552,13 +569,7 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
     const int64_t at = r * stride + kPer * ql;
     float x[kPer];
     if (wide_loads) {  // fp32, every expert there
-#pragma unroll
-      for (int i = 0; i < kPer; i += 4) {
-        typedef float v4f __attribute__((ext_vector_type(4)));
-        const v4f v = *reinterpret_cast<const v4f*>((const float*)logits + at + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[i + j] = fminf(fmaxf(v[j], -INFINITY), FLT_MAX);
-      }
+      load_wide<kPer>((const float*)logits + at, x);
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
@@ -734,53 +745,84 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
   }
 }
 
+// A wave to a row.  wide: fp32, 64 kPer experts, 16-byte rows.
 template <int kPer>
 __global__ __launch_bounds__(kThreads) void router_backward_kernel(
     const void* __restrict__ logits, int64_t stride, const int32_t* __restrict__ ids,
-    const float* __restrict__ dw, Sizes z, const int32_t* __restrict__ psum_rank, int nsrc,
-    int64_t rows, void* __restrict__ dx, int64_t dx_stride) {
+    const float* __restrict__ dw, Sizes z, bool wide, const int32_t* __restrict__ psum_rank,
+    int nsrc, int64_t rows, void* __restrict__ dx, int64_t dx_stride) {
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t nv = valid_rows(psum_rank, nsrc, rows);
   const bool dense = !z.sigmoid && !z.normalize;  // every available expert has a gradient
   for (int64_t r = (int64_t)blockIdx.x * kWaves + wid; r < nv;
        r += (int64_t)gridDim.x * kWaves) {
-    float x[kPer], d[kPer];
-    float top = 0.f, total = 1.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) d[i] = 0.f;
-    if (dense) {
-      load_row<kPer>(logits, z, r * stride, lane, x);
-      softmax_stats<kPer>(x, top, total);
-    }
     int id = -1;
     float g = 0.f, v = 0.f;
     if (lane < z.topk) {
       id = ids[r * z.topk + lane];
-      if (id < 0 || id >= z.E) id = -1;
-      if (id >= 0) {
-        v = load_logit(logits, z.f32, r * stride + id);
-        if (v == -INFINITY) id = -1;
-        else g = dw[r * z.topk + lane];
-      }
+      g = dw[r * z.topk + lane];
     }
+    float d[kPer];  // softmax's values, then the gradients
+    float top = 0.f, total = 1.f, inv = 1.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) d[i] = 0.f;
+    if (dense) {
+      bool done = false;
+      if constexpr (kPer % 4 == 0) {
+        if (wide) {
+          load_wide<kPer>((const float*)logits + r * stride + kPer * lane, d);
+          done = true;
+        }
+      }
+      if (!done) load_row<kPer>(logits, z, r * stride, lane, d);
+      top = d[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) top = fmaxf(top, d[i]);
+      top = wave_max_f(top);
+      total = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        d[i] = d[i] > -INFINITY ? expf(d[i] - top) : 0.f;
+        total += d[i];
+      }
+      total = wave_sum_f(total);
+      inv = total > 0.f ? 1.0f / total : 0.f;
+    }
+    if (id < 0 || id >= z.E) id = -1;
+    if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
+    if (v == -INFINITY) id = -1;
+    if (id < 0) g = 0.f;  // whatever it was
     const float w = weight_of(v, id, z, top, total);
     const float dot = wave_sum_f(w * g);
     float own;  // what the chosen experts get by themselves
     if (z.sigmoid) own = w * (1.0f / (1.0f + expf(v))) * (z.normalize ? g - dot : g);
     else own = w * (z.normalize ? g - dot : g);
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) d[i] *= -inv * dot;
+    }
     for (int k = 0; k < z.topk; ++k) {
       const int e = __builtin_amdgcn_readlane(id, k);
-      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(own), k));
+      if (e < 0) continue;
+      const float o = lane_value(own, k);
+      const float add = lane == e / kPer ? o : 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (e == kPer * lane + i) d[i] += o;
+        if (e % kPer == i) d[i] += add;  // the same branch for all lanes
+    }
+    if constexpr (kPer % 4 == 0) {
+      if (wide) {
+        v4f* to = reinterpret_cast<v4f*>((float*)dx + r * dx_stride + kPer * lane);
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) to[i / 4] = v4f{d[i], d[i + 1], d[i + 2], d[i + 3]};
+        continue;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = kPer * lane + i;
       if (e >= z.E) continue;
-      if (dense && x[i] > -INFINITY) d[i] -= expf(x[i] - top) / total * dot;
       if (z.f32) ((float*)dx)[r * dx_stride + e] = d[i];
       else ((uint16_t*)dx)[r * dx_stride + e] = f32_to_bf16_rne(d[i]);
     }
@@ -851,7 +893,7 @@ extern "C" moe_status moe_router(const void* logits, int64_t logits_stride, moe_
   const int quad = num_experts <= 64 ? 4 : num_experts <= 128 ? 8 : 16;
   if (num_experts <= 256 && topk < 15 && fits(quad) && fits((quad + 3) / 4)) {
     const bool wide_loads = z.f32 && num_experts == 16 * quad && (uintptr_t)logits % 16 == 0 &&
-                            logits_stride % 4 == 0;
+                            (uintptr_t)bias % 16 == 0 && logits_stride % 4 == 0;
     const int64_t blocks = (rows + 4 * kWaves - 1) / (4 * kWaves);
     auto kern = quad == 4   ? router_quad_kernel<4>
                 : quad == 8 ? router_quad_kernel<8>
@@ -903,9 +945,12 @@ extern "C" moe_status moe_router_backward(
               : num_experts <= 256 ? router_backward_kernel<4>
               : num_experts <= 512 ? router_backward_kernel<8>
                                    : router_backward_kernel<16>;
+  const bool wide = z.f32 && (num_experts == 256 || num_experts == 512 || num_experts == 1024) &&
+                    (uintptr_t)logits % 16 == 0 && (uintptr_t)d_logits % 16 == 0 &&
+                    logits_stride % 4 == 0 && d_logits_stride % 4 == 0;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid_of(rows)), dim3(kThreads), 0,
                      reinterpret_cast<hipStream_t>(stream), logits, logits_stride, topk_ids,
-                     d_topk_weights, z, psum_recv_per_rank, num_src_ranks, rows, d_logits,
+                     d_topk_weights, z, wide, psum_recv_per_rank, num_src_ranks, rows, d_logits,
                      d_logits_stride);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

@@ -12,10 +12,9 @@
 // column; a 4 x 4 exchange between the four 16-lane rows of the wave then leaves each
 // of its four words in the MFMA that covers the word's 32 deep group.  MXFP4:
 // v_cvt_scalef32_pk_bf16_fp4 makes two values with their scale, exactly (a
-// normal bf16 number for bytes 2..252).  int4: with u = q + 8, the bits 0x4180 | u << 3
-// are the bf16 value 16 + u; the product starts from -24 * (the rows' own sum)
-// instead of 0, one MFMA with a constant operand for all the columns, and is
-// scaled in fp32 once its group is complete.
+// normal bf16 number for bytes 2..252).  int4: the codes enter as 8 + q; the product
+// starts from -8 * (the rows' own sum) instead of 0, one MFMA with a constant
+// operand for all the columns, and is scaled in fp32 once its group is complete.
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -54,17 +53,22 @@ __device__ __forceinline__ bf16x8 fp4_values(uint32_t d, float scale) {
   r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3));
   return __builtin_bit_cast(bf16x8, r);
 }
-// 8 int4 codes q as 24 + q.
+// 8 int4 codes q as 8 + q.  An E4M3 byte below 16 is that many times 2^-9
+// (subnormal up to 7, and on in the first binade), so a half byte with its sign bit
+// turned is 8 + q: two values an instruction, as for MXFP4.
 __device__ __forceinline__ bf16x8 int4_values(uint32_t d) {
-  const uint32_t lo = ((d << 3) & 0x78787878u) ^ 0xc0c0c0c0u;  // codes 0, 2, 4, 6
-  const uint32_t hi = ((d >> 1) & 0x78787878u) ^ 0xc0c0c0c0u;  // codes 1, 3, 5, 7
+  const uint32_t even = (d & 0x0f0f0f0fu) ^ 0x08080808u;
+  const uint32_t odd = ((d >> 4) & 0x0f0f0f0fu) ^ 0x08080808u;
+  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);  // codes 0..3
+  const uint32_t hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);  // codes 4..7
   u32x4 r;
-  r[0] = __builtin_amdgcn_perm(hi, lo, 0x0c040c00u) | 0x41004100u;
-  r[1] = __builtin_amdgcn_perm(hi, lo, 0x0c050c01u) | 0x41004100u;
-  r[2] = __builtin_amdgcn_perm(hi, lo, 0x0c060c02u) | 0x41004100u;
-  r[3] = __builtin_amdgcn_perm(hi, lo, 0x0c070c03u) | 0x41004100u;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
   return __builtin_bit_cast(bf16x8, r);
 }
+constexpr uint32_t kMinus8 = 0xc100c100u;  // two bf16 values of -8
 
 // kGroup 0: MXFP4; otherwise int4 with scales per 32, 64 or 128.
 template <int kGroup>
@@ -92,10 +96,7 @@ struct Scales {  // of one column's 128-deep block
 constexpr int kNarrowRows = 32, kNarrowCols = 64;  // most rows of a narrow item
 constexpr int kMostNarrow = 64;           // rows of an expert whose items are narrow
 constexpr int kTileRows = 128;
-constexpr int kStages = 5;
-constexpr int kABytes = kTileRows * 128, kWBytes = 8192, kSBytes = 2048;
-constexpr int kStageBytes = kABytes + kWBytes + kSBytes;
-constexpr int kLoads = 4;                 // per wave and stage
+constexpr int kDataBytes = 140 * 1024;
 
 // Narrow items: partial sums of 16 rows by 64 or 128 columns for each wave, then
 // two items' scales.
@@ -111,7 +112,7 @@ constexpr int kRing2 = 1, kRing1 = 1;       // blocks in flight: items of 32 row
 constexpr int kListed = 64;               // narrow items that a workgroup looks up at once
 
 struct Shared {
-  __attribute__((aligned(1024))) uint8_t data[kStages * kStageBytes];
+  __attribute__((aligned(1024))) uint8_t data[kDataBytes];
   int pe[MOE_MAX_EXPERTS];                // psum
   Item list[kListed];
   int gp[3][MOE_MAX_EXPERTS + 1];         // prefix of each kind's row groups per expert
@@ -297,7 +298,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
       if constexpr (!kFp4) sched_fence();  // keeps the groups' values apart
       v4f off[kMt];
       if constexpr (!kFp4) {
-        const u32x4 m24 = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+        const u32x4 m8 = {kMinus8, kMinus8, kMinus8, kMinus8};
 #pragma unroll
         for (int m = 0; m < kMt; ++m) {
           off[m] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -305,7 +306,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
           for (int i = 0; i < kSteps; ++i)
             off[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                 __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]),
-                __builtin_bit_cast(bf16x8, m24), off[m], 0, 0, 0);
+                __builtin_bit_cast(bf16x8, m8), off[m], 0, 0, 0);
         }
       }
 #pragma unroll
@@ -407,86 +408,101 @@ __device__ __forceinline__ void dma4_ptr(const uint8_t* p, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 
-// 128 rows, 64 kFn columns: eight waves, 2 by 4, of 64 x 16 kFn.  Stages of 64
-// along the reduction, five in LDS: rows, codes and one word of scales per
-// column each.  A wave computes on a stage from registers while it reads the
-// next one's fragments.
+// 128 rows, 64 kFn columns: eight waves, 2 by 4, of 64 x 16 kFn.  Waves 4-7
+// stream the rows, 64 deep along the reduction at a time, waves 0-3 the codes and
+// scales, 128 deep: a stage is one request for each row or column, and requests (4
+// bytes of scales, 32 of codes) are what bounds shorter ones (8192 rows, 8 x 4096 x
+// 7168, MXFP4: KNOWN us with 64 for all).  A wave computes on 64 from registers while it
+// reads the next ones' fragments.
 template <int kGroup, int kFn>
 __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, int NT, int lane,
                                      int wid) {
   constexpr bool kFp4 = kGroup == 0;
   constexpr int kFm = 4, kBn = 64 * kFn;
+  constexpr int kA = kFn == 4 ? 4 : 5, kW = kFn == 4 ? 4 : 6;      // stages in LDS
+  constexpr int kScWords = kGroup == 32 ? 2 : 1;                   // per column and stage
+  constexpr int kABytes = kTileRows * 128, kCodeBytes = kBn * 64;  // of a stage
+  constexpr int kWBytes = kCodeBytes + kScWords * 1024;
+  constexpr int kALoads = 4, kWLoads = kFn + kScWords;             // per wave and stage
+  static_assert(kA * kABytes + kW * kWBytes <= kDataBytes);
   const int n = p.n, k = p.k;
   const Item t = uniform(decode(sh, p, kWide, item, NT, kBn, kTileRows));
   const int e = t.e, n0 = t.col, live = t.live;
   const int64_t m0 = t.m0;
   const int wr = wid >> 2, wc = wid & 3, c = lane & 15, qd = lane >> 4;
-  const uint32_t lds0 = lds_addr(sh.data);
+  const uint32_t lds0 = lds_addr(sh.data), ldsw = lds0 + kA * kABytes;
+  const bool rows_role = wid >= 4;
+  const int rw = wid & 3;  // among the waves of its role
 
-  // Loads: rows 16 wid + 8 u + lane / 8 (the last live one in place of those
-  // that are not); 32 columns of codes and 64 of scales, the tile's several times where
-  // it has fewer.  Columns past n repeat the last one and are not stored.
-  const uint8_t* pa[2];
+  // Rows: 8 (4 rw + i) + lane / 8 in chunks of 16 bytes, the last live one in place of
+  // those that are not.  Columns: 16 (kFn rw + i) + lane / 4; scales: 64 rw + lane
+  // (the tile's again where it has fewer).  Columns past n repeat the last one and are
+  // not stored.
+  const uint8_t *src[4], *ps;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int row = 16 * wid + 8 * u + (lane >> 3);
-    pa[u] = p.a + (m0 + min(row, live - 1)) * k * 2 + (((lane & 7) ^ x_key(row)) << 4);
+  for (int i = 0; i < 4; ++i) {
+    if (rows_role) {
+      const int row = 8 * (4 * rw + i) + (lane >> 3);
+      src[i] = p.a + (m0 + min(row, live - 1)) * k * 2 + (((lane & 7) ^ x_key(row)) << 4);
+    } else {
+      const int col = 16 * (kFn * rw + i % kFn) + (lane >> 2);
+      src[i] = p.w + ((int64_t)e * n + min(n0 + col, n - 1)) * (k / 2) +
+               (((lane & 3) ^ (col >> 2 & 3)) << 4);
+    }
   }
-  const uint8_t *pw, *ps;
   {
-    const int wcol = 32 * (wid % (kBn / 32)) + (lane >> 1);
-    pw = p.w + ((int64_t)e * n + min(n0 + wcol, n - 1)) * (k / 2) +
-         (((lane & 1) ^ (wcol >> 3 & 1)) << 4);
-    const int scol = 64 * (wid % (kBn / 64)) + lane;
-    const int64_t col = (int64_t)e * n + min(n0 + scol, n - 1);
-    if constexpr (kGroup == 0) ps = p.sc + col * (k / 32);
+    const int64_t col = (int64_t)e * n + min(n0 + (64 * rw + lane) % kBn, n - 1);
+    if constexpr (kFp4) ps = p.sc + col * (k / 32);
     else ps = p.sc + col * (k / kGroup) * 2;
   }
-  auto stage = [&](int s, uint32_t slot) __attribute__((always_inline)) {
-    const uint32_t at = lds0 + slot;
+  auto load_rows = [&](int s, uint32_t slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) dma16_ptr(pa[u] + s * 128, at + (2 * wid + u) * 1024);
-    dma16_ptr(pw + s * 32, at + kABytes + wid * 1024);
-    // The aligned word that holds the stage's scales.
-    const uint8_t* v;
-    if constexpr (kGroup == 32) v = ps + s * 4;
-    else if constexpr (kGroup == 128) v = (const uint8_t*)((uintptr_t)(ps + (s >> 1) * 2) & ~3ull);
-    else v = ps + (s >> 1) * 4;
-    dma4_ptr(v, at + kABytes + kWBytes + wid * 256);
+    for (int i = 0; i < 4; ++i) dma16_ptr(src[i] + s * 128, lds0 + slot + (4 * rw + i) * 1024);
+  };
+  auto load_codes = [&](int s, uint32_t slot) __attribute__((always_inline)) {
+    const uint32_t at = ldsw + slot;
+#pragma unroll
+    for (int i = 0; i < kFn; ++i) dma16_ptr(src[i] + s * 64, at + (kFn * rw + i) * 1024);
+    // The aligned words that hold the stage's scales.
+    const uint8_t* v = ps + s * (kGroup == 32 ? 8 : 4);
+    if constexpr (kGroup == 128) v = (const uint8_t*)((uintptr_t)(ps + s * 2) & ~3ull);
+#pragma unroll
+    for (int i = 0; i < kScWords; ++i)
+      dma4_ptr(v + 4 * i, at + kCodeBytes + i * 1024 + rw * 256);
   };
 
   const uint32_t fx = lds0 + (wr * 64 + c) * 128 + ((qd ^ x_key(c)) << 4);
-  const uint32_t fw = lds0 + kABytes + (wc * kFn * 16 + c) * 32 + ((c >> 3) << 4) + 4 * qd;
-  const uint32_t fs = lds0 + kABytes + kWBytes + (wc * kFn * 16 + (kFp4 ? c : 4 * qd)) * 4;
+  const uint32_t fw = ldsw + (wc * kFn * 16 + c) * 64 + ((c >> 2) << 4) + 4 * qd;
+  const uint32_t fs = ldsw + kCodeBytes + (wc * kFn * 16 + (kFp4 ? c : 4 * qd)) * 4;
   v4f acc[kFm][kFn] = {};
   struct Frags {
     u32x4 x[2][kFm];
     uint32_t w[2][kFn];
     uint32_t s[kFp4 ? kFn : 1];
   } f[2];
-  auto read = [&](Frags& r, uint32_t slot) __attribute__((always_inline)) {
+  // Half kOdd of a stage of codes, and its rows.
+  auto read = [&](Frags& r, uint32_t x_slot, uint32_t w_slot, auto parity)
+                  __attribute__((always_inline)) {
+    constexpr int kOdd = decltype(parity)::value;
 #pragma unroll
     for (int j = 0; j < kFn; ++j) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        r.w[h][j] = lds_load<uint32_t>(((fw + slot) ^ (uint32_t)(h << 4)) + j * 512);
-      if constexpr (kFp4) r.s[j] = lds_load<uint32_t>(fs + slot + j * 64);
+        r.w[h][j] = lds_load<uint32_t>(((fw + w_slot) ^ (uint32_t)((2 * kOdd + h) << 4)) + j * 1024);
+      if constexpr (kFp4) r.s[j] = lds_load<uint32_t>(fs + w_slot + j * 64);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < kFm; ++i)
-        r.x[h][i] = lds_load<u32x4>(((fx + slot) ^ (uint32_t)(h << 6)) + i * 2048);
+        r.x[h][i] = lds_load<u32x4>(((fx + x_slot) ^ (uint32_t)(h << 6)) + i * 2048);
   };
-  // int4, group 128: whether the word of column 4 qd + r of tile j holds the
-  // stage's scale in its upper half (the same for all tiles: 16 columns apart).
-  const int64_t scol0 = (int64_t)e * n + n0 + 4 * qd;
+  // The scale of column 4 qd + r for half h of 64-deep stage s, in the word that
+  // holds it.  Group 128: column e n + n0 + 4 qd + r starts at that times k / 128
+  // scales, of which all but r k / 128 are even.
   const int per = k / BK;
   auto scale_of = [&](uint32_t v, int r, int s, int h) __attribute__((always_inline)) {
-    uint32_t up;
-    if constexpr (kGroup == 32) up = h;
-    else if constexpr (kGroup == 64) up = s & 1;
-    else up = (uint32_t)((scol0 + r) * per + (s >> 1)) & 1;
+    const int up = kGroup == 32 ? h : kGroup == 64 ? s & 1 : ((r & per) ^ (s >> 1)) & 1;
     return __uint_as_float(up ? v & 0xffff0000u : v << 16);
   };
   auto mfma = [](const bf16x8& w, const u32x4& x, const v4f& d) __attribute__((always_inline)) {
@@ -505,21 +521,23 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
           for (int i = 0; i < kFm; ++i) acc[i][j] = mfma(v, r.x[h][i], acc[i][j]);
         }
     } else {
-      const u32x4 m24 = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};  // -24
+      const u32x4 m8 = {kMinus8, kMinus8, kMinus8, kMinus8};
       constexpr int kParts = kGroup == 32 ? 2 : 1;  // groups of a stage, at most a stage long
       v4f off[kParts][kFm];
 #pragma unroll
       for (int i = 0; i < kFm; ++i) {
-        const bf16x8 c24 = __builtin_bit_cast(bf16x8, m24);
+        const bf16x8 c8 = __builtin_bit_cast(bf16x8, m8);
         const v4f zero = {0.f, 0.f, 0.f, 0.f};
-        off[0][i] = mfma(c24, r.x[0][i], zero);
-        off[kParts - 1][i] = mfma(c24, r.x[1][i], kParts == 1 ? off[0][i] : zero);
+        off[0][i] = mfma(c8, r.x[0][i], zero);
+        off[kParts - 1][i] = mfma(c8, r.x[1][i], kParts == 1 ? off[0][i] : zero);
       }
 #pragma unroll
       for (int j = 0; j < kFn; ++j) {
         sched_fence();  // one tile's values at a time: no spills
         v4f part[kFm];
-        const u32x4 sw = lds_load<u32x4>(fs + slot + j * 64);  // of the lane's 4 columns
+        // Of the lane's 4 columns.
+        const u32x4 sw =
+            lds_load<u32x4>(fs + slot + (kScWords == 2 ? kOdd * 1024 : 0) + j * 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const bf16x8 v = int4_values(r.w[h][j]);
@@ -540,28 +558,45 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     }
   };
 
-  const int steps = k / 64;  // even
+  const int steps = k / 64, stages = k / 128;
   wait_vmcnt<0>();  // the last item's stores do not enter the counts below
-  for (int s = 0; s < kStages - 1 && s < steps; ++s) stage(s, s * kStageBytes);
-  wait_ahead<kLoads, kStages - 2>(min(kStages - 2, steps - 1));
+  if (rows_role) {
+    for (int s = 0; s < kA && s < steps; ++s) load_rows(s, s * kABytes);
+    wait_ahead<kALoads, kA - 1>(min(kA - 1, steps - 1));
+  } else {
+    for (int s = 0; s < kW - 1 && s < stages; ++s) load_codes(s, s * kWBytes);
+    wait_ahead<kWLoads, kW - 2>(min(kW - 2, stages - 1));
+  }
   barrier();
-  read(f[0], 0);
-  uint32_t now = 0, next = kStageBytes, free = (kStages - 1) * kStageBytes;
-  auto bump = [](uint32_t x) { return x + kStageBytes == kStages * kStageBytes ? 0 : x + kStageBytes; };
-  // Stage s is in registers; the next one's fragments are read once it has
-  // landed for all waves, and the slot of stage s - 1 is loaded anew (that of
-  // stage s still holds int4's scales).
+  read(f[0], 0, 0, std::integral_constant<int, 0>());
+  // Slots: of the rows computed (loaded anew at once: they are in registers), and of
+  // the codes computed (int4's scales are still read there) and before them.
+  uint32_t x_now = 0, w_now = 0, w_old = (kW - 1) * kWBytes;
+  auto bump = [](uint32_t at, uint32_t by, uint32_t end) __attribute__((always_inline)) {
+    return at + by == end ? 0 : at + by;
+  };
   auto step = [&](int s, auto parity) __attribute__((always_inline)) {
     constexpr int kOdd = decltype(parity)::value;
-    wait_ahead<kLoads, kStages - 3>(min(kStages - 3, steps - 2 - s));
+    const int t2 = s >> 1;
+    const uint32_t x_next = bump(x_now, kABytes, kA * kABytes);
+    const uint32_t w_next = kOdd ? bump(w_now, kWBytes, kW * kWBytes) : w_now;
+    // The next half has landed for all waves, and all have read this one.
+    if (rows_role) wait_ahead<kALoads, kA - 2>(min(kA - 2, steps - 2 - s));
+    else if (kOdd) wait_ahead<kWLoads, kW - 2>(min(kW - 2, stages - 2 - t2));
     wait_lgkm0();
     barrier();
-    if (s + kStages - 1 < steps) stage(s + kStages - 1, free);
-    if (s + 1 < steps) read(f[kOdd ^ 1], next);
-    compute(f[kOdd], s, now, parity);
-    now = next;
-    next = bump(next);
-    free = bump(free);
+    if (rows_role) {
+      if (s + kA < steps) load_rows(s + kA, x_now);
+    } else if (!kOdd) {
+      if (t2 + kW - 1 < stages) load_codes(t2 + kW - 1, w_old);
+    }
+    if (s + 1 < steps) read(f[kOdd ^ 1], x_next, w_next, std::integral_constant<int, kOdd ^ 1>());
+    compute(f[kOdd], s, w_now, parity);
+    if (kOdd) {
+      w_old = w_now;
+      w_now = w_next;
+    }
+    x_now = x_next;
   };
   for (int s = 0; s < steps; s += 2) {
     step(s, std::integral_constant<int, 0>());
@@ -594,7 +629,7 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Bytes of 64 columns' scales, and the room for an item's (of 128, at least).
   const int sc64 = kNarrowCols * (k / BK) * Scales<kGroup>::kBytes;
-  constexpr int kRoom = (kStages * kStageBytes - kPartBytes) / 2 / 1024 * 1024;
+  constexpr int kRoom = (kDataBytes - kPartBytes) / 2 / 1024 * 1024;
   const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out,
                   2 * sc64 <= kRoom};
   for (int e = threadIdx.x; e < E; e += kThreads) sh.pe[e] = psum[e];
@@ -604,7 +639,7 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   const int groups = __builtin_amdgcn_readfirstlane(sh.gp[kWide][E]);
   // 256 columns where that makes a round of items or more.
   const int NT256 = (n + 255) / 256, NT128 = n / 128;
-  const bool big = kGroup != 32 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
+  const bool big = kGroup == 0 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
   const int NTW = big ? NT256 : NT128;
   const uint32_t nwide = (uint32_t)groups * (uint32_t)NTW;
   const int two = __builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]);
@@ -632,7 +667,7 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   for (;; base += gridDim.x) {
     const uint32_t item = round_item(base, nitems);
     if (item >= nwide) break;
-    if (kGroup != 32 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
+    if (kGroup == 0 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
     else wide<kGroup, 2>(sh, p, item, NTW, lane, wid);
   }
   narrow<kGroup, 2, kTiles2, kRing2>(sh, p, nwide, end2, nitems, cs2, base, lane, wid);

@@ -2,8 +2,8 @@
 
 Tolerance: half a step of the bf16 result (2^-8 of it), and the fp32 sum: each
 MFMA's result may be cut off (2^-23 of the sum so far), k / 32 times, with 32
-terms inside.  Sizes of the terms: |a| s |q|, for int4 |a| s (2 * 24 + |q|),
-since the codes enter as 24 + q and 24 a is taken off.
+terms inside.  Sizes of the terms: |a| s |q|, for int4 |a| s (2 * 8 + |q|),
+since the codes enter as 8 + q and 8 a is taken off.
 """
 
 import numpy as np
@@ -78,7 +78,7 @@ def run(counts, n, k, fmt, group, align=16, spare=0, whole=False, seed=0):
         return
     if fmt == "int4":
         s = np.repeat(np.abs(scale_values(sc)).astype(np.float64), group, axis=-1)
-        mag = mag + 48 * B.grouped(np.abs(av), s, lab)[0]
+        mag = mag + 16 * B.grouped(np.abs(av), s, lab)[0]
     tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -23 * (k / 32 + 32) * mag
     bad = ~(np.abs(got - want) <= tol)[live]
     assert not bad.any(), (bad.sum(), np.abs(got - want)[live][bad].max())

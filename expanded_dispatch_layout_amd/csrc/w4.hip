@@ -480,22 +480,26 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     uint32_t w[2][kFn];
     uint32_t s[kFp4 ? kFn : 1];
   } f[2];
-  // Half kOdd of a stage of codes, and its rows.
-  auto read = [&](Frags& r, uint32_t x_slot, uint32_t w_slot, auto parity)
+  // Read u of half kOdd of a stage of codes and scales, and of its rows.
+  constexpr int kReads = 2 * kFn + (kFp4 ? kFn : 0) + 2 * kFm;
+  auto read = [&](Frags& r, uint32_t x_slot, uint32_t w_slot, auto parity, int u)
                   __attribute__((always_inline)) {
     constexpr int kOdd = decltype(parity)::value;
-#pragma unroll
-    for (int j = 0; j < kFn; ++j) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        r.w[h][j] = lds_load<uint32_t>(((fw + w_slot) ^ (uint32_t)((2 * kOdd + h) << 4)) + j * 1024);
-      if constexpr (kFp4) r.s[j] = lds_load<uint32_t>(fs + w_slot + j * 64);
+    if (u < 2 * kFn) {
+      const int j = u >> 1, h = u & 1;
+      r.w[h][j] = lds_load<uint32_t>(((fw + w_slot) ^ (uint32_t)((2 * kOdd + h) << 4)) + j * 1024);
+      return;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < kFm; ++i)
-        r.x[h][i] = lds_load<u32x4>(((fx + x_slot) ^ (uint32_t)(h << 6)) + i * 2048);
+    u -= 2 * kFn;
+    if constexpr (kFp4) {
+      if (u < kFn) {
+        r.s[u] = lds_load<uint32_t>(fs + w_slot + u * 64);
+        return;
+      }
+      u -= kFn;
+    }
+    const int h = u / kFm, i = u % kFm;
+    r.x[h][i] = lds_load<u32x4>(((fx + x_slot) ^ (uint32_t)(h << 6)) + i * 2048);
   };
   // The scale of column 4 qd + r for half h of 64-deep stage s, in the word that
   // holds it.  Group 128: column e n + n0 + 4 qd + r starts at that times k / 128
@@ -508,43 +512,65 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
   auto mfma = [](const bf16x8& w, const u32x4& x, const v4f& d) __attribute__((always_inline)) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x), d, 0, 0, 0);
   };
-  auto compute = [&](Frags& r, int s, uint32_t slot, auto parity) __attribute__((always_inline)) {
+  // The products of half kOdd of a stage, from registers; next(u) is called between
+  // them, u = 0 .. kReads - 1.  The order is fixed (sched_fence): left to itself the compiler
+  // puts the reads first and waits for them.
+  auto compute = [&](Frags& r, int s, uint32_t slot, auto parity, auto&& next)
+                     __attribute__((always_inline)) {
     constexpr int kOdd = decltype(parity)::value;
+    int u = 0;
+    auto between = [&]() __attribute__((always_inline)) {
+      sched_fence();
+      if (u < kReads) next(u);
+      ++u;
+      sched_fence();
+    };
     if constexpr (kFp4) {
+      auto values = [&](int g) __attribute__((always_inline)) {  // column tile g / 2, half g % 2
+        const int j = g >> 1, h = g & 1;
+        return fp4_values(r.w[h][j],
+                          __uint_as_float((r.s[j] >> (16 * kOdd + 8 * h) & 0xffu) << 23));
+      };
+      bf16x8 v = values(0), after;
 #pragma unroll
-      for (int j = 0; j < kFn; ++j)
+      for (int g = 0; g < 2 * kFn; ++g) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bf16x8 v =
-              fp4_values(r.w[h][j], __uint_as_float((r.s[j] >> (16 * kOdd + 8 * h) & 0xffu) << 23));
-#pragma unroll
-          for (int i = 0; i < kFm; ++i) acc[i][j] = mfma(v, r.x[h][i], acc[i][j]);
+        for (int i = 0; i < kFm; ++i) {
+          acc[i][g >> 1] = mfma(v, r.x[g & 1][i], acc[i][g >> 1]);
+          if (i == 1 && g + 1 < 2 * kFn) after = values(g + 1);
+          between();
         }
+        v = after;
+      }
     } else {
-      const u32x4 m8 = {kMinus8, kMinus8, kMinus8, kMinus8};
-      constexpr int kParts = kGroup == 32 ? 2 : 1;  // groups of a stage, at most a stage long
+      const bf16x8 c8 = __builtin_bit_cast(bf16x8, u32x4{kMinus8, kMinus8, kMinus8, kMinus8});
+      constexpr int kParts = kGroup == 32 ? 2 : 1;  // groups of a half, at most a half long
       v4f off[kParts][kFm];
 #pragma unroll
-      for (int i = 0; i < kFm; ++i) {
-        const bf16x8 c8 = __builtin_bit_cast(bf16x8, m8);
-        const v4f zero = {0.f, 0.f, 0.f, 0.f};
-        off[0][i] = mfma(c8, r.x[0][i], zero);
-        off[kParts - 1][i] = mfma(c8, r.x[1][i], kParts == 1 ? off[0][i] : zero);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kFm; ++i) {
+          const v4f zero = {0.f, 0.f, 0.f, 0.f};
+          off[h % kParts][i] = mfma(c8, r.x[h][i], h < kParts ? zero : off[0][i]);
+          between();
+        }
+      bf16x8 v = int4_values(r.w[0][0]), after;
 #pragma unroll
       for (int j = 0; j < kFn; ++j) {
-        sched_fence();  // one tile's values at a time: no spills
         v4f part[kFm];
         // Of the lane's 4 columns.
         const u32x4 sw =
             lds_load<u32x4>(fs + slot + (kScWords == 2 ? kOdd * 1024 : 0) + j * 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bf16x8 v = int4_values(r.w[h][j]);
 #pragma unroll
-          for (int i = 0; i < kFm; ++i)
-            part[i] = mfma(v, r.x[h][i], kParts == 2 || h == 0 ? off[kParts == 2 ? h : 0][i]
-                                                               : part[i]);
+          for (int i = 0; i < kFm; ++i) {
+            part[i] = mfma(v, r.x[h][i], h < kParts ? off[h][i] : part[i]);
+            if (i == 1 && 2 * j + h + 1 < 2 * kFn)
+              after = int4_values(r.w[(h + 1) & 1][j + (h + 1) / 2]);
+            between();
+          }
+          v = after;
           if (kParts == 2 || h == 1) {
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
@@ -556,6 +582,7 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
         }
       }
     }
+    while (u < kReads) between();
   };
 
   const int steps = k / 64, stages = k / 128;
@@ -568,7 +595,8 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     wait_ahead<kWLoads, kW - 2>(min(kW - 2, stages - 1));
   }
   barrier();
-  read(f[0], 0, 0, std::integral_constant<int, 0>());
+#pragma unroll
+  for (int u = 0; u < kReads; ++u) read(f[0], 0, 0, std::integral_constant<int, 0>(), u);
   // Slots: of the rows computed (loaded anew at once: they are in registers), and of
   // the codes computed (int4's scales are still read there) and before them.
   uint32_t x_now = 0, w_now = 0, w_old = (kW - 1) * kWBytes;
@@ -590,8 +618,10 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     } else if (!kOdd) {
       if (t2 + kW - 1 < stages) load_codes(t2 + kW - 1, w_old);
     }
-    if (s + 1 < steps) read(f[kOdd ^ 1], x_next, w_next, std::integral_constant<int, kOdd ^ 1>());
-    compute(f[kOdd], s, w_now, parity);
+    // (After the last step the fragments read are not used.)
+    compute(f[kOdd], s, w_now, parity, [&](int u) __attribute__((always_inline)) {
+      read(f[kOdd ^ 1], x_next, w_next, std::integral_constant<int, kOdd ^ 1>(), u);
+    });
     if (kOdd) {
       w_old = w_now;
       w_now = w_next;

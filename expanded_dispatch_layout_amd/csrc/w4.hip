@@ -402,7 +402,13 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
 
 // ------------------------------------------------------------------- wide
 
-__device__ __forceinline__ int x_key(int row) { return (row >> 1) & 7; }
+// Rows of 128 bytes: chunks of 16 bytes are XOR-swizzled by bits 2, 1 and 3 of the
+// row, so that the 16 lanes that a 16-byte LDS read serves at once fall on different
+// banks: 16 consecutive rows, or rows 0-3 and 12-15 with 4-11 of the lanes that read
+// two chunks further on.
+__device__ __forceinline__ int x_key(int row) {
+  return (row >> 2 & 1) | (row & 2) | (row >> 1 & 4);
+}
 __device__ __forceinline__ void dma4_ptr(const uint8_t* p, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
@@ -471,8 +477,15 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
       dma4_ptr(v + 4 * i, at + kCodeBytes + i * 1024 + rw * 256);
   };
 
-  const uint32_t fx = lds0 + (wr * 64 + c) * 128 + ((qd ^ x_key(c)) << 4);
-  const uint32_t fw = ldsw + (wc * kFn * 16 + c) * 64 + ((c >> 2) << 4) + 4 * qd;
+  // A lane reads 16 codes of its column at once, 16 qd + 0..15 of a half's 64, one
+  // word for each of the half's two MFMAs, and the rows' chunks 2 qd and 2 qd + 1 to
+  // match: any order along the reduction will do that both operands have.  Groups of 32
+  // scaled in fp32 want an MFMA each: the upper lanes' first words and the lower lanes'
+  // second ones change places, and the chunks are 0, 2, 1, 3 and 4 on.
+  const int chunk = kGroup == 32 ? (qd >> 1) | (qd << 1 & 2) : 2 * qd;
+  const uint32_t fx = lds0 + (wr * 64 + c) * 128 + ((chunk ^ x_key(c)) << 4);
+  const uint32_t fw =
+      ldsw + (wc * kFn * 16 + c) * 64 + (((qd >> 1) ^ (c >> 2)) << 4) + 8 * (qd & 1);
   const uint32_t fs = ldsw + kCodeBytes + (wc * kFn * 16 + (kFp4 ? c : 4 * qd)) * 4;
   v4f acc[kFm][kFn] = {};
   struct Frags {
@@ -481,16 +494,18 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     uint32_t s[kFp4 ? kFn : 1];
   } f[2];
   // Read u of half kOdd of a stage of codes and scales, and of its rows.
-  constexpr int kReads = 2 * kFn + (kFp4 ? kFn : 0) + 2 * kFm;
+  constexpr int kReads = kFn + (kFp4 ? kFn : 0) + 2 * kFm;
   auto read = [&](Frags& r, uint32_t x_slot, uint32_t w_slot, auto parity, int u)
                   __attribute__((always_inline)) {
     constexpr int kOdd = decltype(parity)::value;
-    if (u < 2 * kFn) {
-      const int j = u >> 1, h = u & 1;
-      r.w[h][j] = lds_load<uint32_t>(((fw + w_slot) ^ (uint32_t)((2 * kOdd + h) << 4)) + j * 1024);
+    if (u < kFn) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 v = lds_load<u32x2>(((fw + w_slot) ^ (uint32_t)(kOdd << 5)) + u * 1024);
+      r.w[0][u] = v[0];
+      r.w[1][u] = v[1];
       return;
     }
-    u -= 2 * kFn;
+    u -= kFn;
     if constexpr (kFp4) {
       if (u < kFn) {
         r.s[u] = lds_load<uint32_t>(fs + w_slot + u * 64);
@@ -499,7 +514,8 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
       u -= kFn;
     }
     const int h = u / kFm, i = u % kFm;
-    r.x[h][i] = lds_load<u32x4>(((fx + x_slot) ^ (uint32_t)(h << 6)) + i * 2048);
+    r.x[h][i] =
+        lds_load<u32x4>(((fx + x_slot) ^ (uint32_t)(h << (kGroup == 32 ? 6 : 4))) + i * 2048);
   };
   // The scale of column 4 qd + r for half h of 64-deep stage s, in the word that
   // holds it.  Group 128: column e n + n0 + 4 qd + r starts at that times k / 128
@@ -528,8 +544,9 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     if constexpr (kFp4) {
       auto values = [&](int g) __attribute__((always_inline)) {  // column tile g / 2, half g % 2
         const int j = g >> 1, h = g & 1;
-        return fp4_values(r.w[h][j],
-                          __uint_as_float((r.s[j] >> (16 * kOdd + 8 * h) & 0xffu) << 23));
+        // The lane's 16 codes are of one group: byte qd / 2 of the half's two.
+        const uint32_t scale = r.s[j] >> (16 * kOdd + 8 * (qd >> 1)) & 0xffu;
+        return fp4_values(r.w[h][j], __uint_as_float(scale << 23));
       };
       bf16x8 v = values(0), after;
 #pragma unroll
@@ -545,6 +562,14 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     } else {
       const bf16x8 c8 = __builtin_bit_cast(bf16x8, u32x4{kMinus8, kMinus8, kMinus8, kMinus8});
       constexpr int kParts = kGroup == 32 ? 2 : 1;  // groups of a half, at most a half long
+      if constexpr (kGroup == 32) {
+#pragma unroll
+        for (int j = 0; j < kFn; ++j) {
+          const auto w = __builtin_amdgcn_permlane32_swap(r.w[0][j], r.w[1][j], false, false);
+          r.w[0][j] = w[0];
+          r.w[1][j] = w[1];
+        }
+      }
       v4f off[kParts][kFm];
 #pragma unroll
       for (int h = 0; h < 2; ++h)

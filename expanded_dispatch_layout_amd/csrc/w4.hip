@@ -96,7 +96,7 @@ struct Scales {  // of one column's 128-deep block
 constexpr int kNarrowRows = 32, kNarrowCols = 64;  // most rows of a narrow item
 constexpr int kMostNarrow = 64;           // rows of an expert whose items are narrow
 constexpr int kTileRows = 128;
-constexpr int kDataBytes = 140 * 1024;
+constexpr int kDataBytes = 141 * 1024;
 
 // Narrow items: partial sums of 16 rows by 64 or 128 columns for each wave, then
 // two items' scales.
@@ -425,11 +425,15 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
                                      int wid) {
   constexpr bool kFp4 = kGroup == 0;
   constexpr int kFm = 4, kBn = 64 * kFn;
-  constexpr int kA = kFn == 4 ? 4 : 5, kW = kFn == 4 ? 4 : 6;      // stages in LDS
+  // Rows are staged 128 deep, too, where the tile has room for it: one barrier for
+  // twice the products (KNOWN).
+  constexpr bool kPair = kFn == 2;
   constexpr int kScWords = kGroup == 32 ? 2 : 1;                   // per column and stage
-  constexpr int kABytes = kTileRows * 128, kCodeBytes = kBn * 64;  // of a stage
+  constexpr int kA = kPair ? 3 : 4, kW = kPair && kScWords == 1 ? 5 : 4;  // stages in LDS
+  constexpr int kHalf = kTileRows * 128;                           // rows, 64 deep
+  constexpr int kABytes = kPair ? 2 * kHalf : kHalf, kCodeBytes = kBn * 64;  // of a stage
   constexpr int kWBytes = kCodeBytes + kScWords * 1024;
-  constexpr int kALoads = 4, kWLoads = kFn + kScWords;             // per wave and stage
+  constexpr int kALoads = kPair ? 8 : 4, kWLoads = kFn + kScWords;  // per wave and stage
   static_assert(kA * kABytes + kW * kWBytes <= kDataBytes);
   const int n = p.n, k = p.k;
   const Item t = uniform(decode(sh, p, kWide, item, NT, kBn, kTileRows));
@@ -463,7 +467,11 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
   }
   auto load_rows = [&](int s, uint32_t slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dma16_ptr(src[i] + s * 128, lds0 + slot + (4 * rw + i) * 1024);
+    for (int h = 0; h < (kPair ? 2 : 1); ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dma16_ptr(src[i] + s * (kABytes / kTileRows) + h * 128,
+                  lds0 + slot + h * kHalf + (4 * rw + i) * 1024);
   };
   auto load_codes = [&](int s, uint32_t slot) __attribute__((always_inline)) {
     const uint32_t at = ldsw + slot;
@@ -610,11 +618,11 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     while (u < kReads) between();
   };
 
-  const int steps = k / 64, stages = k / 128;
+  const int stages = k / 128, steps = 2 * stages, a_stages = kPair ? stages : steps;
   wait_vmcnt<0>();  // the last item's stores do not enter the counts below
   if (rows_role) {
-    for (int s = 0; s < kA && s < steps; ++s) load_rows(s, s * kABytes);
-    wait_ahead<kALoads, kA - 1>(min(kA - 1, steps - 1));
+    for (int s = 0; s < kA && s < a_stages; ++s) load_rows(s, s * kABytes);
+    wait_ahead<kALoads, kA - 1>(min(kA - 1, a_stages - 1));
   } else {
     for (int s = 0; s < kW - 1 && s < stages; ++s) load_codes(s, s * kWBytes);
     wait_ahead<kWLoads, kW - 2>(min(kW - 2, stages - 1));
@@ -622,30 +630,38 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
   barrier();
 #pragma unroll
   for (int u = 0; u < kReads; ++u) read(f[0], 0, 0, std::integral_constant<int, 0>(), u);
-  // Slots: of the rows computed (loaded anew at once: they are in registers), and of
-  // the codes computed (int4's scales are still read there) and before them.
+  // Slots: of the rows computed (loaded anew once they are in registers), and of the
+  // codes computed (int4's scales are still read there) and before them.
   uint32_t x_now = 0, w_now = 0, w_old = (kW - 1) * kWBytes;
   auto bump = [](uint32_t at, uint32_t by, uint32_t end) __attribute__((always_inline)) {
     return at + by == end ? 0 : at + by;
   };
+  // Half s of the reduction.  Before the next half's fragments are read, it has landed
+  // for all waves, and all have read the slots that are then loaded anew: the rows' of
+  // this half's stage, and the codes' of the stage before (they are loaded every second
+  // half, kW - 1 stages ahead).  A pair's second half is there with its first.
   auto step = [&](int s, auto parity) __attribute__((always_inline)) {
     constexpr int kOdd = decltype(parity)::value;
-    const int t2 = s >> 1;
-    const uint32_t x_next = bump(x_now, kABytes, kA * kABytes);
+    constexpr bool kSync = !kPair || kOdd, kCodes = kPair ? kOdd : !kOdd;
+    const int t2 = s >> 1, as = kPair ? t2 : s;
+    const uint32_t x_next = kSync ? bump(x_now, kABytes, kA * kABytes) : x_now;
     const uint32_t w_next = kOdd ? bump(w_now, kWBytes, kW * kWBytes) : w_now;
-    // The next half has landed for all waves, and all have read this one.
-    if (rows_role) wait_ahead<kALoads, kA - 2>(min(kA - 2, steps - 2 - s));
-    else if (kOdd) wait_ahead<kWLoads, kW - 2>(min(kW - 2, stages - 2 - t2));
-    wait_lgkm0();
-    barrier();
-    if (rows_role) {
-      if (s + kA < steps) load_rows(s + kA, x_now);
-    } else if (!kOdd) {
-      if (t2 + kW - 1 < stages) load_codes(t2 + kW - 1, w_old);
+    if constexpr (kSync) {
+      constexpr int kAhead = kPair ? kW - 3 : kW - 2;
+      if (rows_role) wait_ahead<kALoads, kA - 2>(min(kA - 2, a_stages - 2 - as));
+      else if (kOdd) wait_ahead<kWLoads, kAhead>(min(kAhead, stages - 2 - t2));
+      wait_lgkm0();
+      barrier();
+      if (rows_role) {
+        if (as + kA < a_stages) load_rows(as + kA, x_now);
+      } else if (kCodes) {
+        if (t2 + kW - 1 < stages) load_codes(t2 + kW - 1, w_old);
+      }
     }
     // (After the last step the fragments read are not used.)
     compute(f[kOdd], s, w_now, parity, [&](int u) __attribute__((always_inline)) {
-      read(f[kOdd ^ 1], x_next, w_next, std::integral_constant<int, kOdd ^ 1>(), u);
+      read(f[kOdd ^ 1], x_next + (kPair && !kOdd ? kHalf : 0), w_next,
+           std::integral_constant<int, kOdd ^ 1>(), u);
     });
     if (kOdd) {
       w_old = w_now;

@@ -587,30 +587,54 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
           off[h % kParts][i] = mfma(c8, r.x[h][i], h < kParts ? zero : off[0][i]);
           between();
         }
+      // Scales of the lane's 4 columns in tile j.
+      auto scales = [&](int j) __attribute__((always_inline)) {
+        return lds_load<u32x4>(fs + slot + (kScWords == 2 ? kOdd * 1024 : 0) + j * 64);
+      };
+      auto add_row = [&](int j, int i, int h, const u32x4& sw, const v4f& part)
+                         __attribute__((always_inline)) {
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) acc[i][j][c4] += part[c4] * scale_of(sw[c4], c4, s, h);
+      };
       bf16x8 v = int4_values(r.w[0][0]), after;
+      if constexpr (kParts == 1) {
+        // A tile's group is complete with its second MFMAs; it is scaled between the
+        // next tile's, when they are done.
+        v4f part[kFn][kFm];
+        u32x4 sw[kFn];
 #pragma unroll
-      for (int j = 0; j < kFn; ++j) {
-        v4f part[kFm];
-        // Of the lane's 4 columns.
-        const u32x4 sw =
-            lds_load<u32x4>(fs + slot + (kScWords == 2 ? kOdd * 1024 : 0) + j * 64);
+        for (int j = 0; j < kFn; ++j) sw[j] = scales(j);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int g = 0; g < 2 * kFn; ++g) {
+          const int h = g / kFn, j = g % kFn;
 #pragma unroll
           for (int i = 0; i < kFm; ++i) {
-            part[i] = mfma(v, r.x[h][i], h < kParts ? off[h][i] : part[i]);
-            if (i == 1 && 2 * j + h + 1 < 2 * kFn)
-              after = int4_values(r.w[(h + 1) & 1][j + (h + 1) / 2]);
+            part[j][i] = mfma(v, r.x[h][i], h ? part[j][i] : off[0][i]);
+            if (i == 1 && g + 1 < 2 * kFn) after = int4_values(r.w[(g + 1) / kFn][(g + 1) % kFn]);
+            if (h && j > 0) add_row(j - 1, i, h, sw[j - 1], part[j - 1][i]);
             between();
           }
           v = after;
-          if (kParts == 2 || h == 1) {
+        }
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              const float sv = scale_of(sw[e4], e4, s, h);
+        for (int i = 0; i < kFm; ++i) add_row(kFn - 1, i, 1, sw[kFn - 1], part[kFn - 1][i]);
+      } else {
 #pragma unroll
-              for (int i = 0; i < kFm; ++i) acc[i][j][e4] += part[i][e4] * sv;
+        for (int j = 0; j < kFn; ++j) {
+          const u32x4 sw = scales(j);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v4f part[kFm];
+#pragma unroll
+            for (int i = 0; i < kFm; ++i) {
+              part[i] = mfma(v, r.x[h][i], off[h][i]);
+              if (i == 1 && 2 * j + h + 1 < 2 * kFn)
+                after = int4_values(r.w[(h + 1) & 1][j + (h + 1) / 2]);
+              between();
             }
+            v = after;
+#pragma unroll
+            for (int i = 0; i < kFm; ++i) add_row(j, i, h, sw, part[i]);
           }
         }
       }

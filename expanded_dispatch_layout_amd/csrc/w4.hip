@@ -94,7 +94,6 @@ struct Scales {  // of one column's 128-deep block
 // ------------------------------------------------------------------ items
 
 constexpr int kNarrowRows = 32, kNarrowCols = 64;  // most rows of a narrow item
-constexpr int kMostNarrow = 64;           // rows of an expert whose items are narrow
 constexpr int kTileRows = 128;
 constexpr int kDataBytes = 141 * 1024;
 
@@ -134,22 +133,33 @@ __device__ __forceinline__ int rows_of(const Shared& sh, const Args& p, int e, i
   return en > st ? (int)(en - st) : 0;
 }
 
-// The row groups of every kind.  Experts of more than kMostNarrow rows are wide;
-// where narrow items alone fill no more than a round of the workgroups, none is.
+// The row groups of every kind.  Experts of up to 32 rows are narrow.  The others
+// are all narrow or all wide, by the rounds that the workgroups make of their
+// 128-column tiles of 32 or 128 rows, which take about 0.55 and 1.3 us for 128 of the
+// reduction (weights of 8 x 4096 x 7168 in MXFP4, narrow / wide: 40 rows each 68 / 82 us,
+// 56 rows 93 / 75, 75 rows 93 / 77; 8 x 7168 x 2048 in int4: 40 rows 41 / 63, 56 rows
+// 42 / 57, 87 rows 60 / 57; 64 x 1024 x 1024 in MXFP4: 40 rows 27 / 26, 56 rows 37 /
+// 25).  A bound on rows alone leaves some experts on either side, and the two halves
+// then run one after the other (56 rows and a bound of 64: 98, 47 and 44).
 __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) {
-  int groups = 0;  // narrow ones; 512 of one expert are more than any grid holds
+  int n32 = 0, n128 = 0;  // row groups of those (of up to 2^25 rows: enough to tell)
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
-    const int rows = rows_of(sh, p, e0 + lane, st);
-    groups += __builtin_amdgcn_readlane(
-        wave_incl_scan_i(min(512, (rows + kNarrowRows - 1) / kNarrowRows)), 63);
+    const int rows = min(rows_of(sh, p, e0 + lane, st), 1 << 25);
+    const bool more = rows > kNarrowRows;
+    n32 += __builtin_amdgcn_readlane(
+        wave_incl_scan_i(more ? (rows + kNarrowRows - 1) / kNarrowRows : 0), 63);
+    n128 += __builtin_amdgcn_readlane(
+        wave_incl_scan_i(more ? (rows + kTileRows - 1) / kTileRows : 0), 63);
   }
-  const bool narrow = p.fits && (int64_t)groups * (p.n / kNarrowCols) <= gridDim.x;
+  const int64_t tiles = p.n / 128, grid = gridDim.x;
+  const bool narrow =
+      p.fits && 5 * ((n32 * tiles + grid - 1) / grid) < 12 * ((n128 * tiles + grid - 1) / grid);
   int wide = 0, both = 0;  // both: of 32 rows, and of 16 (<< 16; at most one an expert)
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
     const int e = e0 + lane, rows = rows_of(sh, p, e, st);
-    const bool is_wide = (rows > kMostNarrow || !p.fits) && !narrow;
+    const bool is_wide = (rows > kNarrowRows || !p.fits) && !narrow;
     const int nw = is_wide ? (rows + kTileRows - 1) / kTileRows : 0;
     const int nb = is_wide   ? 0
                    : rows > 16 ? (rows + kNarrowRows - 1) / kNarrowRows

@@ -348,23 +348,28 @@ def moe_silu_mul_bf16(gate_up, m_indices, psum, status, num_experts, align, out,
     _check("moe_silu_mul_bf16", code)
 
 
-def _need(fn, *specs):
+def _gpu():
+    """The current GPU; -2, which no tensor is on, before any is used."""
+    import torch
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _need(fn, *specs, gpu=None):
     """Each (name, tensor, dtype, shape) is a contiguous tensor of that type and
     shape on the current GPU (the library sees plain pointers and cannot
-    tell).  Tensors that are None are passed over."""
-    import torch
-    device = None
+    tell).  Tensors that are None are passed over.  gpu: _gpu(), where the caller has
+    asked for it already."""
     for name, t, dtype, shape in specs:
         if t is None:
             continue
-        if t.dtype != dtype or t.shape != shape:
+        if t.dtype is not dtype or t.shape != shape:
             raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)}, "
                              f"got {t.dtype} of shape {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
-        if device is None:
-            device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-        if t.get_device() != device:
+        if gpu is None:
+            gpu = _gpu()
+        if t.get_device() != gpu:
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
 
 
@@ -501,24 +506,22 @@ def moe_adamw(tensors, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=
     _check(fn, code)
 
 
-def _need_rows(fn, name, t, dtypes, shape):
-    """A matrix of one of those types and that shape on the current GPU, whose
-    columns are contiguous (its rows may be apart).  Returns whether it is fp32,
-    and the elements from row to row."""
-    import torch
+def _need_rows(fn, name, t, dtypes, shape, gpu):
+    """A matrix of one of those types and that shape on that GPU, whose columns are
+    contiguous (its rows may be apart).  Returns the elements from row to row."""
     if t.dtype not in dtypes or t.shape != shape:
         raise ValueError(f"{fn}: {name} must be {' or '.join(map(str, dtypes))} of shape "
                          f"{tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}")
-    row, col = t.stride()
-    if t.shape[1] > 1 and col != 1 and t.shape[0] > 0:
+    (rows, cols), (row, col) = shape, t.stride()
+    if cols > 1 and col != 1 and rows > 0:
         raise ValueError(f"{fn}: {name} must have contiguous rows")
-    if t.get_device() != (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2):
+    if t.get_device() != gpu:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
-    if t.shape[0] <= 1:
-        row = max(row, t.shape[1])   # the distance to a row that is not there
-    elif row < t.shape[1]:
+    if rows <= 1:
+        return max(row, cols)    # the distance to a row that is not there
+    if row < cols:
         raise ValueError(f"{fn}: {name} has rows that overlap")
-    return t.dtype == torch.float32, row
+    return row
 
 
 def moe_layer_norm(x, weight, y, bias=None, branch=None, sum=None, mean=None, rstd=None,
@@ -528,17 +531,17 @@ def moe_layer_norm(x, weight, y, bias=None, branch=None, sum=None, mean=None, rs
     rstd [rows] fp32 (each may be None).  weight, bias [H] bf16 or fp32.  kind
     'layer' or 'rms'."""
     import torch
-    fn, bf, f32 = "moe_layer_norm", torch.bfloat16, torch.float32
+    fn, bf, f32, gpu = "moe_layer_norm", torch.bfloat16, torch.float32, _gpu()
     rows, H = x.shape
-    x_f32, stride = _need_rows(fn, "x", x, (bf, f32), (rows, H))
+    stride = _need_rows(fn, "x", x, (bf, f32), (rows, H), gpu)
     nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
     wdt = f32 if weight.dtype == f32 else bf
     _need(fn, ("weight", weight, wdt, (H,)), ("bias", bias, wdt, (H,)), ("y", y, bf, (rows, H)),
           ("branch", branch, bf, (rows, H)), ("sum", sum, x.dtype, (rows, H)),
           ("mean", mean, f32, (rows,)), ("rstd", rstd, f32, (rows,)),
-          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)), gpu=gpu)
     code = lib().moe_layer_norm(
-        _ptr(x), stride, x_f32, _ptr(branch), _ptr(weight), _ptr(bias), wdt == f32, NORM[kind],
+        _ptr(x), stride, x.dtype is f32, _ptr(branch), _ptr(weight), _ptr(bias), wdt == f32, NORM[kind],
         eps, _ptr(psum_recv_per_rank), nsrc, rows, H, _ptr(sum), _ptr(y), _ptr(mean), _ptr(rstd),
         _stream(stream))
     _check(fn, code)
@@ -557,9 +560,9 @@ def moe_layer_norm_backward(dy, x, weight, rstd, dx, mean=None, dy2=None, dsum=N
     workspace: a uint8 tensor of at least moe_layer_norm_backward_workspace_bytes
     (None without dweight and dbias)."""
     import torch
-    fn, bf, f32 = "moe_layer_norm_backward", torch.bfloat16, torch.float32
+    fn, bf, f32, gpu = "moe_layer_norm_backward", torch.bfloat16, torch.float32, _gpu()
     rows, H = x.shape
-    x_f32, stride = _need_rows(fn, "x", x, (bf, f32), (rows, H))
+    stride = _need_rows(fn, "x", x, (bf, f32), (rows, H), gpu)
     nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
     size = 0 if workspace is None else workspace.numel()
     wdt = f32 if weight.dtype == f32 else bf
@@ -571,9 +574,9 @@ def moe_layer_norm_backward(dy, x, weight, rstd, dx, mean=None, dy2=None, dsum=N
           ("dx", dx, x.dtype, (rows, H)), ("dweight", dweight, gdt, (H,)),
           ("dbias", dbias, gdt, (H,)),
           ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)),
-          ("workspace", workspace, torch.uint8, (size,)))
+          ("workspace", workspace, torch.uint8, (size,)), gpu=gpu)
     code = lib().moe_layer_norm_backward(
-        _ptr(dy), _ptr(dy2), _ptr(x), stride, x_f32, _ptr(weight), wdt == f32, NORM[kind],
+        _ptr(dy), _ptr(dy2), _ptr(x), stride, x.dtype is f32, _ptr(weight), wdt == f32, NORM[kind],
         _ptr(mean), _ptr(rstd), _ptr(dsum), _ptr(psum_recv_per_rank), nsrc, rows, H, _ptr(dx),
         _ptr(dweight), _ptr(dbias), MOE_GRAD_BF16 if gdt == bf else MOE_GRAD_F32,
         bool(accumulate), _ptr(workspace), size, _stream(stream))
@@ -586,16 +589,16 @@ def moe_router(logits, topk_ids, topk_weights, bias=None, score="softmax", num_g
     topk_weights [rows, topk] fp32; bias [E] fp32 or None.  score 'softmax' or
     'sigmoid'."""
     import torch
-    fn, f32 = "moe_router", torch.float32
+    fn, f32, gpu = "moe_router", torch.float32, _gpu()
     rows, E = logits.shape
-    is_f32, stride = _need_rows(fn, "logits", logits, (torch.bfloat16, f32), (rows, E))
+    stride = _need_rows(fn, "logits", logits, (torch.bfloat16, f32), (rows, E), gpu)
     topk = topk_ids.shape[1]
     nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
     _need(fn, ("topk_ids", topk_ids, torch.int32, (rows, topk)),
           ("topk_weights", topk_weights, f32, (rows, topk)), ("bias", bias, f32, (E,)),
-          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)), gpu=gpu)
     code = lib().moe_router(
-        _ptr(logits), stride, is_f32, _ptr(bias), SCORE[score], num_groups, topk_groups,
+        _ptr(logits), stride, logits.dtype is f32, _ptr(bias), SCORE[score], num_groups, topk_groups,
         bool(normalize), _ptr(psum_recv_per_rank), nsrc, rows, E, topk, _ptr(topk_ids),
         _ptr(topk_weights), _stream(stream))
     _check(fn, code)
@@ -606,17 +609,17 @@ def moe_router_backward(logits, topk_ids, d_topk_weights, d_logits, score="softm
     """logits [rows, E] and topk_ids [rows, topk] of moe_router, d_topk_weights
     [rows, topk] fp32 -> d_logits [rows, E] of the logits' type (rows may be apart)."""
     import torch
-    fn = "moe_router_backward"
+    fn, f32, gpu = "moe_router_backward", torch.float32, _gpu()
     rows, E = logits.shape
-    is_f32, stride = _need_rows(fn, "logits", logits, (torch.bfloat16, torch.float32), (rows, E))
-    _, d_stride = _need_rows(fn, "d_logits", d_logits, (logits.dtype,), (rows, E))
+    stride = _need_rows(fn, "logits", logits, (torch.bfloat16, f32), (rows, E), gpu)
+    d_stride = _need_rows(fn, "d_logits", d_logits, (logits.dtype,), (rows, E), gpu)
     topk = topk_ids.shape[1]
     nsrc = 0 if psum_recv_per_rank is None else psum_recv_per_rank.numel()
     _need(fn, ("topk_ids", topk_ids, torch.int32, (rows, topk)),
-          ("d_topk_weights", d_topk_weights, torch.float32, (rows, topk)),
-          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)))
+          ("d_topk_weights", d_topk_weights, f32, (rows, topk)),
+          ("psum_recv_per_rank", psum_recv_per_rank, torch.int32, (nsrc,)), gpu=gpu)
     code = lib().moe_router_backward(
-        _ptr(logits), stride, is_f32, SCORE[score], bool(normalize), _ptr(topk_ids),
+        _ptr(logits), stride, logits.dtype is f32, SCORE[score], bool(normalize), _ptr(topk_ids),
         _ptr(d_topk_weights), _ptr(psum_recv_per_rank), nsrc, rows, E, topk, _ptr(d_logits),
         d_stride, _stream(stream))
     _check(fn, code)

@@ -4,17 +4,20 @@
 //
 // int4: q in [-8, 7], bf16 scales; MXFP4: q an E2M1 value, s = 2^(byte - 127).
 //
-// One workgroup of four waves per item (expert, up to 16 of its rows, 64
-// columns); the waves take every fourth 128-deep block of the reduction, straight
-// from memory into registers, and their sums meet in LDS in the waves' order.
+// One workgroup of eight waves per CU walks the items of the device's layout:
+// "narrow" ones of up to 32 rows of an expert, whose time is the weights' stream, and
+// "wide" ones of 128 rows, which feed the matrix cores through LDS.
 //
-// Codes to bf16.  A lane loads 16 bytes, 32 codes along the reduction, of one
-// column; a 4 x 4 exchange between the four 16-lane rows of the wave then leaves each
-// of its four words in the MFMA that covers the word's 32 deep group.  MXFP4:
-// v_cvt_scalef32_pk_bf16_fp4 makes two values with their scale, exactly (a
-// normal bf16 number for bytes 2..252).  int4: the codes enter as 8 + q; the product
-// starts from -8 * (the rows' own sum) instead of 0, one MFMA with a constant
-// operand for all the columns, and is scaled in fp32 once its group is complete.
+// Codes to bf16, in registers, by each wave that needs them.  MXFP4:
+// v_cvt_scalef32_pk_bf16_fp4 makes two values with their scale, exactly (a normal bf16
+// number for bytes 2..252).  int4: the codes enter as 8 + q; the product starts from
+// -8 * (the rows' own sum) instead of 0, one MFMA with a constant operand for all the
+// columns, and is scaled in fp32 once its group is complete.
+//
+// One token's eight experts, 4096 x 7168, MXFP4: 31 us, 4.0 TB/s (a plain sum over as
+// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 474 us, 1.02 PFLOP/s;
+// int4 780 us (a quarter to a half more MFMAs and half the tile's columns, since the
+// scaled sums need the registers).
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -107,7 +110,6 @@ constexpr int kWide = 0, kTwo = 1, kOne = 2;
 struct __attribute__((aligned(16))) Item {
   int e, col, live, m0;
 };
-constexpr int kRing2 = 1, kRing1 = 1;       // blocks in flight: items of 32 rows, of 16
 constexpr int kListed = 64;               // narrow items that a workgroup looks up at once
 
 struct Shared {
@@ -207,13 +209,19 @@ __device__ __forceinline__ Item uniform(const Item& t) {
 
 // ----------------------------------------------------------------- narrow
 
-// An item is 16 kMt rows and 64 cs columns: the waves are cs groups of 64
-// columns by 8 / cs parts of the reduction, which take its 128-deep blocks in
-// turn, kRing of them in flight, across the items.  The parts' sums meet in LDS.
-// The item's scales are one contiguous piece of memory, copied to LDS during
-// the item before it: read where they are needed, 4 bytes of a line at a time,
-// they cost more requests than the codes.
-template <int kGroup, int kMt, int kTiles, int kRing>
+// The weights' stream decides.  An item is 16 kMt rows and 16 kTiles cs columns: the
+// waves are cs groups of 16 kTiles columns by 8 / cs parts of the reduction, which take
+// its 128-deep blocks in turn, straight from memory into registers; the next block is
+// asked for, also of the next item, once the present one is used, and the two waves of
+// a SIMD take turns (two blocks in flight are no faster, 31.3 us against 31.2 for one
+// token's eight products of 4096 x 7168, and four cost 1 us: their code is longer than
+// the few steps a wave makes).  The parts' sums meet in LDS, in the parts' order.
+// 17 to 32 rows take 128 columns to a wave, so that the rows are read half as often
+// (200 rows, 8 x 7168 x 2048, int4: 34 us with 64 columns, 30 so).
+// The item's scales are one contiguous piece of memory, copied to LDS during the item
+// before it: read where they are needed, 4 bytes of a line at a time, they cost more
+// requests than the codes (51 us against 36, at that time).
+template <int kGroup, int kMt, int kTiles>
 __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first_item,
                                        uint32_t last_item, uint32_t nitems, int cs,
                                        uint32_t& base, int lane, int wid) {
@@ -222,16 +230,14 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
   constexpr int kPitch = kCols + 4;                              // of its partial sums
   constexpr int kG = kFp4 ? 1 : 128 / kGroup, kSteps = 4 / kG;   // groups of a block, MFMAs each
   constexpr int kStepLoads = kTiles + 4 * kMt;
-  struct Set {
-    u32x4 w[kTiles], x[kMt][4];
-  } set[kRing];
+  u32x4 wv[kTiles], xv[kMt][4];  // the block loaded
   const int c = lane & 15, qd = lane >> 4;
   const int k = p.k, KB = k / BK, cols = kCols * cs, NT = p.n / cols;
   const int ks = kWaves / cs, cg = wid % cs, kp = wid / cs;
   const int nk = KB > kp ? (KB - kp + ks - 1) / ks : 0;  // blocks of this wave per item
-  // Steps of every wave per item: those past its blocks load one address and add
+  // Steps of every wave per item: one past its blocks loads one address and adds
   // nothing.
-  const int steps = ((KB + ks - 1) / ks + kRing - 1) / kRing * kRing;
+  const int steps = (KB + ks - 1) / ks;
   const int sc_row = KB * Scales<kGroup>::kBytes, sc_bytes = cols * sc_row;
   const uint32_t sc0 = lds_addr(sh.data) + kWaves * 16 * kPitch * 4;
   const uint32_t sc_slot = (uint32_t)(sc_bytes + 1023) & ~1023u;
@@ -273,13 +279,13 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
     x_step = ks * BK * 2;
     w_tile = (int64_t)8 * k;
   };
-  auto load = [&](Set& s) __attribute__((always_inline)) {
+  auto load = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) s.w[j] = *reinterpret_cast<const u32x4*>(wp + j * w_tile);
+    for (int j = 0; j < kTiles; ++j) wv[j] = *reinterpret_cast<const u32x4*>(wp + j * w_tile);
 #pragma unroll
     for (int m = 0; m < kMt; ++m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.x[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + 64 * i);
+      for (int i = 0; i < 4; ++i) xv[m][i] = *reinterpret_cast<const u32x4*>(ap[m] + 64 * i);
       ap[m] += x_step;
     }
     wp += w_step;
@@ -297,12 +303,12 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
 #pragma unroll
       for (int j = 0; j < kTiles; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
   };
-  auto compute = [&](Set& s, uint32_t scales) __attribute__((always_inline)) {
+  auto compute = [&](uint32_t scales) __attribute__((always_inline)) {
     Scales<kGroup> sc[kTiles];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) sc[j].load(scales + (uint32_t)(16 * j * sc_row));
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) exchange(s.w[j]);
+    for (int j = 0; j < kTiles; ++j) exchange(wv[j]);
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       if constexpr (!kFp4) sched_fence();  // keeps the groups' values apart
@@ -315,7 +321,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
 #pragma unroll
           for (int i = 0; i < kSteps; ++i)
             off[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]),
+                __builtin_bit_cast(bf16x8, xv[m][g * kSteps + i]),
                 __builtin_bit_cast(bf16x8, m8), off[m], 0, 0, 0);
         }
       }
@@ -325,14 +331,14 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
         bf16x8 v[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-          v[i] = kFp4 ? fp4_values(s.w[j][i], sc[j].get(i)) : int4_values(s.w[j][g * kSteps + i]);
+          v[i] = kFp4 ? fp4_values(wv[j][i], sc[j].get(i)) : int4_values(wv[j][g * kSteps + i]);
 #pragma unroll
         for (int m = 0; m < kMt; ++m) {
           v4f part = kFp4 ? acc[m][j] : off[m];
 #pragma unroll
           for (int i = 0; i < kSteps; ++i)
             part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, s.x[m][g * kSteps + i]), v[i], part, 0, 0, 0);
+                __builtin_bit_cast(bf16x8, xv[m][g * kSteps + i]), v[i], part, 0, 0, 0);
           if constexpr (kFp4) acc[m][j] = part;
           else acc[m][j] += part * sc[j].get(g);
         }
@@ -345,7 +351,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
     const Item t = item_of(i);
     // This wave's copies of the next item's scales, older than an item's loads,
     // have landed.
-    wait_vmcnt<kRing * kStepLoads>();
+    wait_vmcnt<kStepLoads>();
 #pragma unroll
     for (int m = 0; m < kMt; ++m) {
 #pragma unroll
@@ -386,24 +392,20 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
     li = lk = 0;
     open();
     copy_scales(0);
-#pragma unroll
-    for (int r = 0; r < kRing; ++r) load(set[r]);
-    wait_vmcnt<kRing * kStepLoads>();
+    load();
+    wait_vmcnt<kStepLoads>();
     barrier();  // the first scales have landed
     copy_scales(1);
-    // Items of kRing steps at a time and one way out of each loop: with a way out
-    // after every step the compiler joins them all into one that leads back to
-    // the start, and waits there for the youngest load.
+    // The loop has one way out: with one after every step, also unrolled, the compiler
+    // joins them into one that leads back to the start, and waits there for the
+    // youngest load.
     for (int ci = 0; ci < count; ++ci) {
       uint32_t scales = sc_lane + (uint32_t)(kp * Scales<kGroup>::kBytes) + (ci & 1) * sc_slot;
       clear();
-      for (int t = 0; t < steps; t += kRing) {
-#pragma unroll
-        for (int r = 0; r < kRing; ++r) {
-          if (t + r < nk) compute(set[r], scales);
-          load(set[r]);
-          scales += (uint32_t)(ks * Scales<kGroup>::kBytes);
-        }
+      for (int t = 0; t < steps; ++t) {
+        if (t < nk) compute(scales);
+        load();
+        scales += (uint32_t)(ks * Scales<kGroup>::kBytes);
       }
       join(ci);
     }
@@ -428,15 +430,16 @@ __device__ __forceinline__ void dma4_ptr(const uint8_t* p, uint32_t lds) {
 // stream the rows, 64 deep along the reduction at a time, waves 0-3 the codes and
 // scales, 128 deep: a stage is one request for each row or column, and requests (4
 // bytes of scales, 32 of codes) are what bounds shorter ones (8192 rows, 8 x 4096 x
-// 7168, MXFP4: KNOWN us with 64 for all).  A wave computes on 64 from registers while it
-// reads the next ones' fragments.
+// 7168, MXFP4: 606 us with 64 for all, 515 so).  A wave computes on 64 from registers
+// while it reads the next ones' fragments, a read between any two MFMAs (515 -> 490;
+// with 8-byte reads of the codes 474).
 template <int kGroup, int kFn>
 __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, int NT, int lane,
                                      int wid) {
   constexpr bool kFp4 = kGroup == 0;
   constexpr int kFm = 4, kBn = 64 * kFn;
-  // Rows are staged 128 deep, too, where the tile has room for it: one barrier for
-  // twice the products (KNOWN).
+  // Rows are staged 128 deep, too, where the tile leaves room for it: one barrier for
+  // twice the products (800 rows, 8 x 4096 x 7168: 91 -> 80 us).
   constexpr bool kPair = kFn == 2;
   constexpr int kScWords = kGroup == 32 ? 2 : 1;                   // per column and stage
   constexpr int kA = kPair ? 3 : 4, kW = kPair && kScWords == 1 ? 5 : 4;  // stages in LDS
@@ -707,7 +710,9 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, uint32_t item, i
     step(s, std::integral_constant<int, 0>());
     step(s + 1, std::integral_constant<int, 1>());
   }
-  barrier();  // the last stages have been read
+  // The last stages have been read (int4's scales are asked for after the steps' waits).
+  wait_lgkm0();
+  barrier();
 
   // The lane holds columns 4 qd + 0..3 of tile j for row c of tile i; two lane
   // swaps make 8 neighbouring columns of two tiles: 16-byte stores.
@@ -775,8 +780,8 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
     if (kGroup == 0 && big) wide<kGroup, 4>(sh, p, item, NTW, lane, wid);
     else wide<kGroup, 2>(sh, p, item, NTW, lane, wid);
   }
-  narrow<kGroup, 2, kTiles2, kRing2>(sh, p, nwide, end2, nitems, cs2, base, lane, wid);
-  narrow<kGroup, 1, kTiles1, kRing1>(sh, p, end2, nitems, nitems, cs1, base, lane, wid);
+  narrow<kGroup, 2, kTiles2>(sh, p, nwide, end2, nitems, cs2, base, lane, wid);
+  narrow<kGroup, 1, kTiles1>(sh, p, end2, nitems, nitems, cs1, base, lane, wid);
 }
 
 }  // namespace

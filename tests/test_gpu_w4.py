@@ -114,6 +114,39 @@ def test_many_experts_and_long_rows(fmt, group):
     run([2, 200], 511 * 64 // 128 * 128, 128, fmt, group, 16, whole=True)
 
 
+@pytest.mark.parametrize("fmt,group,k", [("mxfp4", 32, 9472), ("mxfp4", 32, 9600),
+                                         ("int4", 32, 4736), ("int4", 32, 4864),
+                                         ("int4", 64, 9472), ("int4", 64, 9600),
+                                         ("int4", 128, 18944), ("int4", 128, 19072)])
+def test_where_the_scales_just_fit(fmt, group, k):
+    """The longest reduction whose scales the items of few rows hold, and the next."""
+    run([3, 0, 20, 33, 140], 256, k, fmt, group, 16, whole=True, seed=k)
+
+
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("int4", 128)])
+@pytest.mark.parametrize("rows", [1, 20])
+def test_more_items_than_are_listed_at_once(fmt, group, rows):
+    """1024 experts of 16384 columns: over 64 items for every workgroup."""
+    E, n, k, align = 1024, 16384, 128, 32
+    psum, status, cap = layout([rows] * E, align)
+    w, sc = weights(E, n, k, fmt, group, 3, whole=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    a = torch.randint(-3, 4, (cap, k), device="cuda", generator=g).to(BF)
+    out = torch.full((cap, n), 7.0, dtype=BF, device="cuda")
+    M.moe_grouped_gemm_w4(a, w, sc, fmt, psum, status, align, out)
+    table = ([*range(8), *range(-8, 0)] if fmt == "int4" else
+             [*B.E2M1.tolist(), *(-B.E2M1).tolist()])
+    table = torch.tensor(table, device="cuda")
+    for e in range(0, E, 61):
+        q = torch.stack([w[e] & 15, w[e] >> 4], dim=-1).view(n, k)
+        s = sc[e].float() if fmt == "int4" else torch.exp2(sc[e].float() - 127)
+        v = table[q.long()].double() * s.double().repeat_interleave(group, dim=1)
+        at = slice(e * align, e * align + rows)
+        assert torch.equal(out[at], (a[at].double() @ v.t()).float().to(BF)), e
+        assert bool((out[e * align + rows:(e + 1) * align] == 7).all())
+
+
 @pytest.mark.parametrize("fmt,group", FORMATS)
 def test_one_code_at_a_time(fmt, group):
     """Row t of a is the unit vector of k = t: the output is the weights themselves,

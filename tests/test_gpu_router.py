@@ -237,3 +237,96 @@ def test_many_rows():
     M.moe_router_backward(x, ids, dw, dx)
     M.moe_router_backward(many, ids2, dw.repeat(5000, 1), dx2)
     assert torch.equal(dx2, dx.repeat(5000, 1))
+
+
+def check_near(x, topk, bias, score, groups, topk_groups, normalize):
+    """As run(); of keys that fp64 itself cannot tell, either order.  How many rows had
+    such keys is returned.
+
+    The oracle forms a score as exp(l), with l of a size below 8 here from a logarithm
+    and a difference: l is off by at most 2^-53 (8 + 8 + 2), and exp adds a unit of
+    2^-52: 2^-48 of the score at most.  The kernel's, an exp of a difference, a sum and
+    a quotient, is nearer.  Adding the bias rounds by 2^-53 of a smaller number.  So two
+    keys that are compared are off by 4 * 2^-48 of the row's largest score together, and
+    sums of two by twice that.  (Logits 1 and 2 steps of 2^-20 apart and biases that make
+    up for them do differ by less: 64 experts' scores lie about 2^-6, by a part of
+    2^-20 to either side, and so the steps' products with them about 2^-26, the biases'
+    own step: their keys differ by 1e-20 in more than one row.)"""
+    rows, E = x.shape
+    ids = torch.full((rows, topk), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((rows, topk), -9.0, device="cuda")
+    M.moe_router(x, ids, w, bias, score, groups, topk_groups, normalize)
+    want, _ = B.router(np64(x), topk, None if bias is None else np64(bias), score, groups,
+                       topk_groups, normalize)
+    got = ids.cpu().numpy().astype(np.int64)
+    bad = np.nonzero((got != want).any(axis=1))[0]
+    assert bias is not None or groups > 1 or len(bad) == 0
+    s = np.exp(B.log_scores(B.clean(np64(x)), score))
+    per = E // groups
+    for r in bad:
+        tol = 8 * 2.0 ** -48 * s[r].max()
+        key = np.where(np.isneginf(np64(x)[r]), -np.inf,
+                       s[r] + (0 if bias is None else np64(bias)))
+        sums = np.sort(key.reshape(groups, per), axis=1)[:, -2:].sum(1)
+        of = got[r] // per                           # the groups it chose, and the best others
+        rest = [g for g in np.argsort(-sums, kind="stable") if g not in of]
+        chosen = [*dict.fromkeys(of), *rest][:topk_groups]
+        assert set(of) <= set(chosen), (r, got[r], want[r])
+        out = [g for g in range(groups) if g not in chosen]
+        if out:
+            assert sums[chosen].min() >= sums[out].max() - tol, (r, got[r], want[r])
+        best = np.sort(key[np.isin(np.arange(E) // per, chosen)])[::-1][:topk]
+        assert len(set(got[r])) == topk and (got[r] >= 0).all(), (r, got[r])
+        assert np.abs(key[got[r]] - best).max() <= tol, (r, got[r], want[r])
+    ww = B.router_weights(np64(x), got, score, normalize)
+    assert (np.abs(np64(w) - ww) <= REL * ww + TINY).all()
+    return len(bad)
+
+
+@pytest.mark.parametrize("E", [64, 100, 128, 200, 256, 512, 1024])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_keys_too_near_for_fp32(E, score):
+    """Logits 2^-20 apart, with biases that take back their scores: every neighbour
+    lies within fp32's errors."""
+    rng = np.random.default_rng(E)
+    for topk in (1, 8, 14, 15, 16):
+        for groups, topk_groups in ((1, 1), (4, 2), (4, 3)):
+            for taken_back in (True, False):
+                if topk > E // groups * topk_groups:
+                    continue
+                print(f"[near keys {E} {score} top {topk} {groups} {topk_groups} "
+                      f"{taken_back}]", flush=True)
+                base = 0.5 + rng.integers(0, 3 if topk % 2 else 1 << 19, E) * 2.0 ** -20
+                x = base + rng.integers(0, 4, (203, E)) * 2.0 ** -20
+                x[7::9, ::3] = -INF
+                bias = None
+                if taken_back:
+                    s = np.exp(B.log_scores(x[:1], score))[0]
+                    b = -s.astype(np.float32) + np.float32(2.0 ** -26) * rng.integers(0, 4, E)
+                    bias = torch.from_numpy(b.astype(np.float32)).cuda()
+                held = torch.full((203, E + 4), -INF, device="cuda")
+                for at in (0, 1):                    # 16-byte rows, and others
+                    view = held[:, at:at + E]
+                    view.copy_(torch.from_numpy(x))
+                    print(f"  of 203 rows {check_near(view, topk, bias, score, groups, topk_groups, bool(at))}"
+                          " in another order", flush=True)
+
+
+@pytest.mark.parametrize("E,groups", [(256, 8), (64, 4), (128, 16), (60, 5), (512, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_whose_sums_leave_fp32(E, groups, score):
+    """A bias of the lowest value is a key like others; two of a group's sum to less
+    than fp32 holds, and the largest to more."""
+    low = torch.finfo(F32).min
+    x = logits_of(E, 37, E)
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        b = np.full(E, low)
+        if seed:
+            b[rng.random(E) < 0.1] = 0.0
+        if seed == 2:
+            b = rng.choice([low, low / 2, -low / 2, -low, 0.75 * -low], E)
+        bias = torch.from_numpy(b).float().cuda()
+        for topk in (3, 12):
+            run(x, topk, bias, score, groups, 3)
+            run(x, topk, bias, score)

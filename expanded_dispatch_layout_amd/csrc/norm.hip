@@ -408,7 +408,8 @@ bool shared(std::initializer_list<Buffer> written, std::initializer_list<Buffer>
 moe_status check_sizes(int64_t rows, int hidden, int64_t x_stride, moe_float_fmt x_fmt,
                        moe_float_fmt w_fmt, moe_norm_kind kind,
                        const int32_t* psum_recv_per_rank, int num_src_ranks) {
-  if (rows < 0 || rows > (1LL << 30) || hidden <= 0 || hidden % 8 != 0 || x_stride < hidden)
+  if (rows < 0 || rows > (1LL << 30) || hidden <= 0 || hidden % 8 != 0 || x_stride < hidden ||
+      x_stride > (1LL << 30))
     return MOE_ERR_SHAPE;
   if (num_src_ranks < 0 || (psum_recv_per_rank && num_src_ranks == 0)) return MOE_ERR_SHAPE;
   if (bad_float(x_fmt) || bad_float(w_fmt) || (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) ||

@@ -24,6 +24,15 @@
  * they are scattered) and leaving through moe_gather with the top-k weights
  * and the routed scaling factor.
  *
+ * Around the experts of a layer (before either standard path):
+ *   moe_layer_norm        the norm of the residual stream, the branch before it added
+ *   moe_grouped_gemm_bf16 the gate's logits, as one group
+ *   moe_router            each token's experts and weights, as the layout takes them
+ * and back, with the gradients that the training calls leave: moe_router_backward,
+ * the grouped gradients of the gate, moe_layer_norm_backward.
+ * moe_grouped_gemm_w4 takes the place of moe_grouped_gemm_bf16 for experts' weights of
+ * 4 bits (int4 or MXFP4).
+ *
  * The decode path's masked slab [P1 "Why decode stays on V1 low_latency";
  * P3 pre_permute_deepep_v2_to_deep_gemm / post_permute_deep_gemm_to_
  * deepep_v2, masked branches; _run_masked_gemm] runs after moe_expand_layout:
@@ -668,10 +677,12 @@ moe_status moe_adamw(
  *   mean, rstd  [rows] fp32, what the backward pass takes; may be NULL (mean:
  *           0 for MOE_NORM_RMS)
  *   psum_recv_per_rank / num_src_ranks  as for the layout (R_v)
- * Rows >= R_v are neither read nor written.  A row whose h holds an infinity
- * or a NaN gets NaN throughout.
+ * Rows >= R_v are neither read nor written.  A row whose h holds a NaN gets NaN
+ * throughout, and one with an infinity, too, but for MOE_NORM_RMS: its rstd is 0, and
+ * y the NaN of 0 times infinity there and bias (or 0) beside it.  So is, in fp32, a
+ * row whose sum of squares passes the largest value, without the NaN.
  * Sizes: hidden % 8 == 0 and hidden <= 8192 (else MOE_ERR_UNSUPPORTED);
- * x_stride >= hidden, rows of x 16-byte aligned; 0 <= eps < infinity; buffers
+ * hidden <= x_stride <= 2^30, rows of x 16-byte aligned; 0 <= eps < infinity; buffers
  * 16-byte aligned, mean and rstd 4-byte.  A buffer that is written and shares
  * memory with another (but for sum and x, above): MOE_ERR_UNSUPPORTED.
  */
@@ -736,9 +747,10 @@ moe_status moe_layer_norm_backward(
  * never chosen, and a NaN or -inf logit has score 0.  +inf counts as the
  * largest finite fp32 value.  Slots for which no expert is left (all of them
  * in a row without any) get id -1 and weight 0.  Without a bias and groups
- * the experts are compared by their logits, otherwise by fp64 scores: scores
- * that differ are not taken for equal.  Rows >= R_v are neither read nor
- * written.
+ * the experts are compared by their logits, otherwise by fp64 scores (and sums of
+ * scores), which are told apart down to fp64's own rounding.  A bias of the lowest
+ * fp32 value is a key like others; only -inf and NaN exclude an expert.  Rows >= R_v
+ * are neither read nor written.
  * Sizes: 1 <= topk <= min(num_experts, MOE_MAX_TOPK), num_experts <=
  * MOE_MAX_EXPERTS, num_groups <= 64 and a divisor of num_experts,
  * logits_stride >= num_experts; buffers aligned to their elements.  An output
@@ -788,7 +800,10 @@ moe_status moe_router_backward(
  *            exact for scale bytes 2..252 and NaN for byte 255; other bytes make weights
  *            outside bf16's normal range.
  *   out      [capacity, n] bf16; rows that are not live are not written
- * Rows of a that are not live do not enter any result.
+ * Rows of a that are not live do not enter any result.  Equal calls give equal bits; a
+ * row's last bit may depend on how many rows there are beside it (sums over k are formed
+ * in parts for few rows and in one for many).  MOE_W4_INT4 forms sums of a (8 + q) and
+ * of 8 a: infinities in a row give NaN, and values beyond 2^120 may.
  * Sizes: n % 128 == 0, k % 128 == 0 and n / 64, k / 64 <= 511 (else
  * MOE_ERR_UNSUPPORTED), align and capacity as for the layout; buffers
  * 16-byte aligned.  out sharing memory with another buffer:

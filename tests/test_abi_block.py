@@ -48,6 +48,12 @@ def test_norm_rejects_bad_arguments():
     assert _norm(rows=0) == M.MOE_OK
 
 
+def test_strides_past_the_limit():
+    assert _norm(xs=(1 << 30) + 8) == M.MOE_ERR_SHAPE
+    assert _norm(xs=1 << 62) == M.MOE_ERR_SHAPE
+    assert _norm_back(xs=1 << 62) == M.MOE_ERR_SHAPE
+
+
 def test_norm_refuses_shared_memory():
     for out in ("sum", "y", "mean", "rstd"):
         for other in ("x", "branch", "w", "b"):

@@ -148,6 +148,18 @@ def test_hard_rows():
     assert bool(torch.isinf(o["rstd"]).all())        # 1 / 0, as the formula has it
 
 
+def test_infinities_under_rms():
+    x, w, b = rand(1, 4, 2056, dtype=F32), rand(2, 2056, dtype=F32), rand(3, 2056, dtype=F32)
+    x[0, 7], x[1, 7], x[2, 7] = float("inf"), float("nan"), 1e20
+    o = forward(x, w, b, None, "rms", 1e-6, None)
+    rest = torch.arange(2056, device="cuda") != 7
+    assert bool(torch.isnan(o["y"][0, 7])) and bool(torch.isnan(o["y"][1]).all())
+    assert o["rstd"][0] == 0 and o["rstd"][2] == 0
+    assert torch.equal(o["y"][0, rest], b[rest].to(BF)) and torch.equal(o["y"][2], b.to(BF))
+    compare_forward(forward(x[3:], w, b, None, "rms", 1e-6, None), x[3:], w, b, None, "rms",
+                    1e-6, None)
+
+
 def backward(case, x, dy, weight, mean, rstd, kind, nv, dy2=None, dsum=None, gdt=F32, bias=True,
              weight_grad=True, accumulate=False, in_place=False):
     rows, H = x.shape

@@ -21,7 +21,7 @@
 // choose_closely and choose_exactly, the last without any limit on groups or ties.
 //
 // Memory is not what bounds it: 16384 rows of 256 experts with bias and groups, 8
-// chosen, are 18 MB, 4 us at a copy's rate, and take 17 us; the 256 keys and the
+// chosen, are 18 MB, 4 us at a copy's rate, and take 18 us; the 256 keys and the
 // choices are about 380 vector instructions a row.  Its gradient, 34 MB: 12 us.
 #include <float.h>
 #include <math.h>

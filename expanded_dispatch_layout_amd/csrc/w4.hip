@@ -15,7 +15,8 @@
 // columns, and is scaled in fp32 once its group is complete.
 //
 // One token's eight experts, 4096 x 7168, MXFP4: 31 us, 4.0 TB/s (a plain sum over as
-// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 474 us, 1.02 PFLOP/s;
+// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 474 to 514 us by the
+// machine, 0.94 to 1.02 PFLOP/s;
 // int4 780 us (a quarter to a half more MFMAs and half the tile's columns, since the
 // scaled sums need the registers).
 #include "gemm_backward.hpp"

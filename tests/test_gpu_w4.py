@@ -123,6 +123,14 @@ def test_where_the_scales_just_fit(fmt, group, k):
     run([3, 0, 20, 33, 140], 256, k, fmt, group, 16, whole=True, seed=k)
 
 
+@pytest.mark.parametrize("counts", [[500] * 8, [1000, 900, 1030, 129, 300, 33, 20, 640],
+                                    [2300, 0, 1, 16, 1200, 700]])
+@pytest.mark.parametrize("n", [2176, 2304])
+def test_a_last_round_of_few_tiles(counts, n):
+    """A little more than a round or two of wide items: the rest go in parts."""
+    run(counts, n, 256, "mxfp4", 32, 128, whole=True, seed=n)
+
+
 @pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("int4", 128)])
 @pytest.mark.parametrize("rows", [1, 20])
 def test_more_items_than_are_listed_at_once(fmt, group, rows):

@@ -6,7 +6,7 @@
 //
 // One workgroup of eight waves per CU walks the items of the device's layout:
 // "narrow" ones of up to 32 rows of an expert, whose time is the weights' stream, and
-// "wide" ones of 128 rows, which feed the matrix cores through LDS.
+// "wide" ones of 128 rows or "tall" ones of 256, which feed the matrix cores through LDS.
 //
 // Codes to bf16, in registers, by each wave that needs them.  MXFP4:
 // v_cvt_scalef32_pk_bf16_fp4 makes two values with their scale, exactly (a normal bf16
@@ -15,9 +15,8 @@
 // columns, and is scaled in fp32 once its group is complete.
 //
 // One token's eight experts, 4096 x 7168, MXFP4: 31 us, 4.0 TB/s (a plain sum over as
-// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 474 to 514 us by the
-// machine, 0.94 to 1.02 PFLOP/s;
-// int4 780 us (a quarter to a half more MFMAs and half the tile's columns, since the
+// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 418 us, 1.15 PFLOP/s;
+// int4 772 us (a quarter to a half more MFMAs and a quarter of the tile, since the
 // scaled sums need the registers).
 #include "gemm_backward.hpp"
 
@@ -28,6 +27,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 512, kWaves = 8;
 constexpr int BK = 128;                   // a block of the narrow path
+
+// The lane's number, formed here and now: not held, nor what is made of it, for longer.
+__device__ __forceinline__ int lane_now() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+  return l;
+}
 
 // 4 x 4 words between the wave's 16-lane rows: word i of row r <-> word r of
 // row i.
@@ -98,7 +104,7 @@ struct Scales {  // of one column's 128-deep block
 // ------------------------------------------------------------------ items
 
 constexpr int kNarrowRows = 32, kNarrowCols = 64;  // most rows of a narrow item
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128, kTallRows = 256;  // of a wide item
 constexpr int kDataBytes = 141 * 1024;
 
 // Narrow items: partial sums of 16 rows by 64 or 128 columns for each wave, then
@@ -118,6 +124,7 @@ struct Shared {
   int pe[MOE_MAX_EXPERTS];                // psum
   Item list[kListed];
   int gp[3][MOE_MAX_EXPERTS + 1];         // prefix of each kind's row groups per expert
+  int tile;                               // rows of a wide item
 };
 
 struct Args {
@@ -144,8 +151,9 @@ __device__ __forceinline__ int rows_of(const Shared& sh, const Args& p, int e, i
 // 42 / 57, 87 rows 60 / 57; 64 x 1024 x 1024 in MXFP4: 40 rows 27 / 26, 56 rows 37 /
 // 25).  A bound on rows alone leaves some experts on either side, and the two halves
 // then run one after the other (56 rows and a bound of 64: 98, 47 and 44).
+template <int kGroup>
 __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) {
-  int n32 = 0, n128 = 0;  // row groups of those (of up to 2^25 rows: enough to tell)
+  int n32 = 0, n128 = 0, n256 = 0;  // row groups of those (of up to 2^25 rows: enough to tell)
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
     const int rows = min(rows_of(sh, p, e0 + lane, st), 1 << 25);
@@ -154,16 +162,32 @@ __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) 
         wave_incl_scan_i(more ? (rows + kNarrowRows - 1) / kNarrowRows : 0), 63);
     n128 += __builtin_amdgcn_readlane(
         wave_incl_scan_i(more ? (rows + kTileRows - 1) / kTileRows : 0), 63);
+    n256 += __builtin_amdgcn_readlane(
+        wave_incl_scan_i(more ? (rows + kTallRows - 1) / kTallRows : 0), 63);
   }
   const int64_t tiles = p.n / 128, grid = gridDim.x;
   const bool narrow =
       p.fits && 5 * ((n32 * tiles + grid - 1) / grid) < 12 * ((n128 * tiles + grid - 1) / grid);
+  const int64_t tiles256 = (p.n + 255) / 256;
+  // 256 rows by the rounds, too: 9, 16 and 29 are what tiles of 128 x 128, 128 x 256 and
+  // 256 x 256 last, also as the parts of a last round (w4_kernel).
+  auto rounds = [&](int64_t items, int each, int parts) __attribute__((always_inline)) {
+    const int64_t rest = items % grid;
+    const int last = rest == 0                             ? 0
+                     : parts == 4 && rest * 4 <= grid ? 9
+                     : rest * 2 <= grid               ? (parts == 4 ? 16 : 9)
+                                                      : each;
+    return items / grid * each + last;
+  };
+  const bool tall = kGroup == 0 && !narrow && n256 * tiles256 >= grid &&
+                    rounds(n256 * tiles256, 29, 4) < rounds(n128 * tiles256, 16, 2);
+  const int tile = tall ? kTallRows : kTileRows;
   int wide = 0, both = 0;  // both: of 32 rows, and of 16 (<< 16; at most one an expert)
   for (int e0 = 0; e0 < p.E; e0 += 64) {
     int st;
     const int e = e0 + lane, rows = rows_of(sh, p, e, st);
     const bool is_wide = (rows > kNarrowRows || !p.fits) && !narrow;
-    const int nw = is_wide ? (rows + kTileRows - 1) / kTileRows : 0;
+    const int nw = is_wide ? (rows + tile - 1) / tile : 0;
     const int nb = is_wide   ? 0
                    : rows > 16 ? (rows + kNarrowRows - 1) / kNarrowRows
                                : (rows > 0) << 16;
@@ -177,6 +201,7 @@ __device__ __forceinline__ void list_items(Shared& sh, const Args& p, int lane) 
     both += __builtin_amdgcn_readlane(ib, 63);
   }
   if (lane == 0) {
+    sh.tile = tile;
     sh.gp[kWide][p.E] = wide;
     sh.gp[kTwo][p.E] = both & 0xffff;
     sh.gp[kOne][p.E] = both >> 16;
@@ -364,7 +389,7 @@ __device__ __forceinline__ void narrow(Shared& sh, const Args& p, uint32_t first
       barrier();
       if (m == 0) copy_scales(i + 2);  // in place of this item's
       const int per = cols / 4;        // 4 columns to a thread
-      for (int at = threadIdx.x; at < per * min(16, t.live - 16 * m); at += kThreads) {
+      for (int at = 64 * wid + lane; at < per * min(16, t.live - 16 * m); at += kThreads) {
         const int row = at / per, col = at % per;
         const float* from =
             part + (col / (kCols / 4) * 16 + row) * kPitch + col % (kCols / 4) * 4;
@@ -729,6 +754,179 @@ __device__ __forceinline__ void wide(Shared& sh, const Args& p, const Item& t, i
   }
 }
 
+// ------------------------------------------------------------------- tall
+
+// MXFP4, 256 rows, 256 columns: eight waves, 2 by 4, of 128 x 64.  A code is decoded for
+// twice as many rows and LDS is read a tenth less than with 128 rows (8192 rows, 8 x 4096
+// x 7168: 462 -> 418 us; 6500 rows, 16 x 4096 x 4096: 242 -> 211).  128 sums to a
+// thread leave room for one set of row fragments, 32 deep: each is read anew as soon as
+// its last product has been issued.  Roles and stages as in wide; 3 stages of rows, 2 of
+// codes.
+__device__ __forceinline__ void tall(Shared& sh, const Args& p, const Item& t, int lane,
+                                     int wid) {
+  constexpr int kFm = 8, kFn = 4, kBn = 64 * kFn;
+  constexpr int kA = 3, kW = 2;                                    // stages in LDS
+  constexpr int kABytes = kTallRows * 128, kCodeBytes = kBn * 64, kWBytes = kCodeBytes + 1024;
+  static_assert(kA * kABytes + kW * kWBytes <= kDataBytes);
+  const int n = p.n, k = p.k;
+  const int e = t.e, n0 = t.col, live = t.live;
+  const int64_t m0 = t.m0;
+  const int wr = wid >> 2, wc = wid & 3, c = lane & 15, qd = lane >> 4;
+  const uint32_t lds0 = lds_addr(sh.data), ldsw = lds0 + kA * kABytes;
+  const bool rows_role = wid >= 4;
+  const int rw = wid & 3;
+
+  // As in wide: rows 8 (8 rw + i) + lane / 8, columns 16 (4 rw + i) + lane / 4.  Their
+  // offsets (256 lines of less than 2^16 bytes) are formed anew each time: held, they
+  // would not leave room for the sums.
+  const int64_t col0 = (int64_t)e * n + n0;
+  const uint8_t* const base = rows_role ? p.a + m0 * k * 2 : p.w + col0 * (k / 2);
+  const uint8_t* const base_sc = p.sc + col0 * (k / 32);
+  const uint32_t last = rows_role ? live - 1 : n - 1 - n0, pitch = rows_role ? k * 2 : k / 2;
+  auto load_rows = [&](int s, uint32_t slot) __attribute__((always_inline)) {
+    const uint8_t* from = settled(base + s * 128);
+    const uint32_t l = lane_now();
+    const uint32_t swz = ((l & 7) ^ x_key(l >> 3)) << 4;
+#pragma unroll
+    for (int i = 0; i < kFm; ++i) {
+      const uint32_t row = min((uint32_t)(8 * (kFm * rw + i)) + (l >> 3), last);
+      dma16(from, __umul24(row, pitch) + (swz ^ (uint32_t)((i & 1) << 6)),
+            lds0 + slot + (kFm * rw + i) * 1024);
+      sched_fence();
+    }
+  };
+  auto load_codes = [&](int s, uint32_t slot) __attribute__((always_inline)) {
+    const uint32_t at = ldsw + slot;
+    const uint8_t* from = settled(base + s * 64);
+    const uint32_t l = lane_now();
+    const uint32_t swz = ((l & 3) ^ (l >> 4)) << 4;
+#pragma unroll
+    for (int i = 0; i < kFn; ++i) {
+      const uint32_t col = min((uint32_t)(16 * (kFn * rw + i)) + (l >> 2), last);
+      dma16(from, __umul24(col, pitch) + swz, at + (kFn * rw + i) * 1024);
+      sched_fence();
+    }
+    dma4(base_sc + s * 4, __umul24(min(64 * rw + l, last), (uint32_t)(k / 32)),
+         at + kCodeBytes + rw * 256);
+  };
+
+  const uint32_t fx = lds0 + (wr * 128 + c) * 128 + (((2 * qd) ^ x_key(c)) << 4);
+  const uint32_t fw =
+      ldsw + (wc * kFn * 16 + c) * 64 + (((qd >> 1) ^ (c >> 2)) << 4) + 8 * (qd & 1);
+  const uint32_t fs = ldsw + kCodeBytes + (wc * kFn * 16 + c) * 4;
+  v4f acc[kFm][kFn] = {};
+  u32x4 x[kFm];
+  uint32_t w[2][kFn], sc[kFn];
+  bf16x8 v;
+  auto read_x = [&](uint32_t slot, int h, int i) __attribute__((always_inline)) {
+    x[i] = lds_load<u32x4>(((fx + slot) ^ (uint32_t)(h << 4)) + i * 2048);
+  };
+  auto read_w = [&](uint32_t slot, int odd, int j) __attribute__((always_inline)) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 d = lds_load<u32x2>(((fw + slot) ^ (uint32_t)(odd << 5)) + j * 1024);
+    w[0][j] = d[0];
+    w[1][j] = d[1];
+  };
+  auto values = [&](int j, int h, int odd) __attribute__((always_inline)) {
+    const uint32_t scale = sc[j] >> (16 * odd + 8 * (qd >> 1)) & 0xffu;
+    return fp4_values(w[h][j], __uint_as_float(scale << 23));
+  };
+  // Column tile j with 32 of the reduction; the next one's values are made at row d, and
+  // between(i) is called after row i's product.
+  auto products = [&](int j, int d, auto&& next, auto&& between) __attribute__((always_inline)) {
+    bf16x8 after = v;
+#pragma unroll
+    for (int i = 0; i < kFm; ++i) {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, x[i]),
+                                                          acc[i][j], 0, 0, 0);
+      if (i == d) after = next();
+      sched_fence();
+      between(i);
+      sched_fence();
+    }
+    v = after;
+  };
+
+  const int stages = k / 128, steps = 2 * stages;
+  wait_vmcnt<0>();  // the last item's stores do not enter the counts below
+  if (rows_role) {
+    for (int s = 0; s < kA && s < steps; ++s) load_rows(s, s * kABytes);
+    wait_ahead<kFm, kA - 1>(min(kA - 1, steps - 1));
+  } else {
+    for (int s = 0; s < kW && s < stages; ++s) load_codes(s, s * kWBytes);
+    wait_ahead<kFn + 1, kW - 1>(min(kW - 1, stages - 1));
+  }
+  barrier();
+#pragma unroll
+  for (int j = 0; j < kFn; ++j) {
+    read_w(0, 0, j);
+    sc[j] = lds_load<uint32_t>(fs + j * 64);
+  }
+#pragma unroll
+  for (int i = 0; i < kFm; ++i) read_x(0, 0, i);
+  v = values(0, 0, 0);
+  uint32_t x_now = 0, w_now = 0;
+  auto nothing = [](int) __attribute__((always_inline)) {};
+  // Half s of a stage of codes.  Once its rows are in registers for all waves and the
+  // next half has landed, their slot is loaded anew, and that of the codes' stage, whose
+  // last ones were read a half before.
+  auto step = [&](int s, auto parity) __attribute__((always_inline)) {
+    constexpr int kOdd = decltype(parity)::value;
+    const uint32_t x_next = x_now + kABytes == kA * kABytes ? 0 : x_now + kABytes;
+    const uint32_t w_next = kOdd ? (w_now ? 0 : kWBytes) : w_now;
+    products(0, 2, [&]() { return values(1, 0, kOdd); }, nothing);
+    products(1, 2, [&]() { return values(2, 0, kOdd); }, nothing);
+    products(2, 2, [&]() { return values(3, 0, kOdd); }, nothing);
+    products(3, 2, [&]() { return values(0, 1, kOdd); }, [&](int i) { read_x(x_now, 1, i); });
+    products(0, 2, [&]() { return values(1, 1, kOdd); }, nothing);
+    products(1, 2, [&]() { return values(2, 1, kOdd); }, nothing);
+    products(2, 2, [&]() { return values(3, 1, kOdd); }, nothing);
+    int role = wid;
+    asm volatile("" : "+s"(role));  // compared here: a held comparison takes a vector register
+    const bool rows_now = role >= 4;
+    if (rows_now) wait_ahead<kFm, 1>(min(1, steps - 2 - s));
+    else if (kOdd) wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier();
+    if (rows_now) {
+      if (s + kA < steps) load_rows(s + kA, x_now);
+    } else if (kOdd) {
+      if ((s >> 1) + kW < stages) load_codes((s >> 1) + kW, w_now);
+    }
+    uint32_t fs_next = fs + w_next;
+    asm volatile("" : "+v"(fs_next));  // one address
+    // (After the last half what is read is not used.)
+    products(3, 7, [&]() { return values(0, 0, kOdd ^ 1); }, [&](int i) {
+      if (i < kFn) {
+        read_w(w_next, kOdd ^ 1, i);
+        if (kOdd) sc[i] = lds_load<uint32_t>(fs_next + i * 64);
+      }
+      read_x(x_next, 0, i);
+    });
+    x_now = x_next;
+    w_now = w_next;
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, std::integral_constant<int, 0>());
+    step(s + 1, std::integral_constant<int, 1>());
+  }
+  wait_lgkm0();
+  barrier();  // the last stages have been read
+
+  const int l = lane_now(), row0 = wr * 128 + (l & 15);
+  const int tc = n0 + wc * kFn * 16 + (l >> 5) * 16 + (l >> 4 & 1) * 8;
+#pragma unroll
+  for (int i = 0; i < kFm; ++i) {
+    const int m = row0 + i * 16;
+    uint16_t* row = p.out + (m0 + m) * n + tc;
+#pragma unroll
+    for (int j = 0; j < kFn; j += 2) {
+      const u32x4 o = pack_tiles(acc[i][j], acc[i][j + 1]);
+      if (m < live && tc + j * 16 < n) *reinterpret_cast<u32x4*>(row + j * 16) = o;
+    }
+  }
+}
+
 template <int kGroup>
 __global__ __launch_bounds__(kThreads) void w4_kernel(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ w, const uint8_t* __restrict__ sc,
@@ -740,24 +938,29 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   // Bytes of 64 columns' scales, and the room for an item's (of 128, at least).
   const int sc64 = kNarrowCols * (k / BK) * Scales<kGroup>::kBytes;
   constexpr int kRoom = (kDataBytes - kPartBytes) / 2 / 1024 * 1024;
-  const Args p = {a, w, sc, min((int64_t)status[0], capacity), n, k, E, align, out,
+  const Args p = {a, w, sc, min((int64_t)__builtin_amdgcn_readfirstlane(status[0]), capacity), n, k, E, align, out,
                   2 * sc64 <= kRoom};
   for (int e = threadIdx.x; e < E; e += kThreads) sh.pe[e] = psum[e];
   __syncthreads();
-  if (wid == 0) list_items(sh, p, lane);
+  if (wid == 0) list_items<kGroup>(sh, p, lane);
   __syncthreads();
   const int groups = __builtin_amdgcn_readfirstlane(sh.gp[kWide][E]);
-  // 256 columns where that makes a round of items or more.
+  // 256 columns where that makes a round of items or more, and 256 rows, too.
   const int NT256 = (n + 255) / 256, NT128 = n / 128;
-  const bool big = kGroup == 0 && (uint32_t)groups * (uint32_t)NT256 >= gridDim.x;
-  const int NTW = big ? NT256 : NT128;
-  // A last round that leaves half of the workgroups idle takes its tiles in halves of 128
-  // columns, which last 0.58 of it (8192 rows, 8 x 4096 x 7168, in 68 row groups
-  // of 16 tiles: 490 -> 467 us; 4000 rows, 8 x 2048 x 2048: 63 -> 52).
+  const int shape = __builtin_amdgcn_readfirstlane(
+      kGroup != 0 ? 0 : sh.tile == kTallRows ? 2 : (uint32_t)groups * (uint32_t)NT256 >= gridDim.x);
+  const int NTW = shape ? NT256 : NT128;
+  // A last round that leaves half of the workgroups idle takes its tiles in halves, and
+  // tall ones of a quarter of them in quarters (128-row tiles of 256 columns, 8192 rows,
+  // 8 x 4096 x 7168, 68 row groups of 16 tiles: 490 -> 467 us; 4000 rows, 8 x 2048 x 2048:
+  // 63 -> 52).
   uint32_t nwide = (uint32_t)groups * (uint32_t)NTW, whole = nwide;
-  if (big && nwide % gridDim.x * 2 <= gridDim.x) {
-    whole -= nwide % gridDim.x;
-    nwide += nwide - whole;
+  int split = 0;  // log2 of the parts
+  const uint32_t rest = nwide % gridDim.x;
+  if (shape && rest * 2 <= gridDim.x) split = shape == 2 && rest * 4 <= gridDim.x ? 2 : 1;
+  if (split) {
+    whole -= rest;
+    nwide = whole + (rest << split);
   }
   const int two = __builtin_amdgcn_readfirstlane(sh.gp[kTwo][E]);
   const int one = __builtin_amdgcn_readfirstlane(sh.gp[kOne][E]);
@@ -784,16 +987,35 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   for (;; base += gridDim.x) {
     const uint32_t item = round_item(base, nitems);
     if (item >= nwide) break;
-    const bool half = item >= whole;
-    Item t = uniform(decode(sh, p, kWide, half ? whole + (item - whole) / 2 : item, NTW,
-                            big ? 256 : 128, kTileRows));
-    if (half) t.col += (int)(item - whole) % 2 * 128;
-    if (t.col >= n) continue;
-    if (kGroup == 0 && big && !half) wide<kGroup, 4>(sh, p, t, lane, wid);
-    else wide<kGroup, 2>(sh, p, t, lane, wid);
+    const bool part = item >= whole;
+    const uint32_t of = item - whole;
+    Item t = uniform(decode(sh, p, kWide, part ? whole + (of >> split) : item, NTW,
+                            shape ? 256 : 128, shape == 2 ? kTallRows : kTileRows));
+    int now = shape;
+    if (part) {
+      // Tall ones go in halves of 128 rows or in quarters, others in halves of 128 columns.
+      const int cols = split - shape / 2, rows = shape / 2;  // log2 of parts either way
+      t.col += (int)of % (1 << cols) * 128;
+      const int down = (int)(of >> cols) % (1 << rows) * 128;
+      t.m0 += down;
+      t.live = min(t.live - down, rows ? 128 : t.live);
+      now -= cols + rows;
+      if (t.col >= n || t.live <= 0) continue;
+    }
+    int w = wid;
+    now = __builtin_amdgcn_readfirstlane(now);
+    Args q = p;
+    asm volatile("" : "+s"(w), "+s"(now), "+s"(q.n), "+s"(q.k));
+    if (now == 2) {
+      if constexpr (kGroup == 0) tall(sh, q, t, lane_now(), w);
+    } else if (now == 1) {
+      if constexpr (kGroup == 0) wide<kGroup, 4>(sh, q, t, lane_now(), w);
+    } else {
+      wide<kGroup, 2>(sh, q, t, lane_now(), w);
+    }
   }
-  narrow<kGroup, 2, kTiles2>(sh, p, nwide, end2, nitems, cs2, base, lane, wid);
-  narrow<kGroup, 1, kTiles1>(sh, p, end2, nitems, nitems, cs1, base, lane, wid);
+  narrow<kGroup, 2, kTiles2>(sh, p, nwide, end2, nitems, cs2, base, lane_now(), wid);
+  narrow<kGroup, 1, kTiles1>(sh, p, end2, nitems, nitems, cs1, base, lane_now(), wid);
 }
 
 }  // namespace

@@ -131,6 +131,16 @@ def test_a_last_round_of_few_tiles(counts, n):
     run(counts, n, 256, "mxfp4", 32, 128, whole=True, seed=n)
 
 
+@pytest.mark.parametrize("counts", [[1024] * 8, [1270, 1300, 1000, 1400, 1281, 1153, 1500, 1300],
+                                    [1600] * 7 + [1537, 33, 5, 0, 20]])
+@pytest.mark.parametrize("n,k", [(2176, 128), (2304, 256), (2176, 640)])
+def test_tiles_of_256_rows(counts, n, k):
+    """A round and a few, and some more, and most of another one: the last round's
+    tiles in quarters, in halves and whole."""
+    run(counts, n, k, "mxfp4", 32, 128, whole=True, seed=k)
+    run(counts, n, k, "mxfp4", 32, 128, whole=False, seed=k)
+
+
 @pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("int4", 128)])
 @pytest.mark.parametrize("rows", [1, 20])
 def test_more_items_than_are_listed_at_once(fmt, group, rows):

@@ -15,7 +15,7 @@
 // columns, and is scaled in fp32 once its group is complete.
 //
 // One token's eight experts, 4096 x 7168, MXFP4: 31 us, 4.0 TB/s (a plain sum over as
-// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 418 us, 1.15 PFLOP/s;
+// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 413 us, 1.17 PFLOP/s;
 // int4 772 us (a quarter to a half more MFMAs and a quarter of the tile, since the
 // scaled sums need the registers).
 #include "gemm_backward.hpp"
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(kThreads) void w4_kernel(
   const int NTW = shape ? NT256 : NT128;
   // A last round that leaves half of the workgroups idle takes its tiles in halves, and
   // tall ones of a quarter of them in quarters (128-row tiles of 256 columns, 8192 rows,
-  // 8 x 4096 x 7168, 68 row groups of 16 tiles: 490 -> 467 us; 4000 rows, 8 x 2048 x 2048:
+  // 8 x 4096 x 7168, about 68 row groups of 16 tiles: 490 -> 467 us; 4000 rows, 8 x 2048 x 2048:
   // 63 -> 52).
   uint32_t nwide = (uint32_t)groups * (uint32_t)NTW, whole = nwide;
   int split = 0;  // log2 of the parts

@@ -38,6 +38,11 @@ __device__ __forceinline__ float load_logit(const void* x, bool f32, int64_t at)
   const float v = f32 ? ((const float*)x)[at] : bf16_to_f32(((const uint16_t*)x)[at]);
   return v != v ? -INFINITY : fminf(v, FLT_MAX);
 }
+__device__ __forceinline__ float load_bias(const float* __restrict__ bias, int e) {
+  if (!bias) return 0.f;
+  const float b = bias[e];
+  return b != b ? -INFINITY : fminf(b, FLT_MAX);
+}
 __device__ __forceinline__ double wave_sum_d(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
@@ -236,6 +241,21 @@ __device__ __forceinline__ int choose_exactly(const void* __restrict__ logits, i
 __device__ __forceinline__ float key_error(float key, bool sigmoid) {
   return (sigmoid ? 0x1p-21f : 0x1p-18f) + 0x1p-22f * fabsf(key);
 }
+// fp32 key of one expert; top and inv: softmax's maximum and one over its sum.
+__device__ __forceinline__ float quick_key(float v, float b, const Sizes& z, float top,
+                                           float inv) {
+  return (z.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - top) * inv) + b;
+}
+// Does an expert of logit v and bias b come before one of v2 and b2 that was lined up
+// behind it, for certain?  The same logit and bias make the same key, and were lined up by
+// their numbers.
+__device__ __forceinline__ bool before(float v, float b, float v2, float b2, bool keys,
+                                       const Sizes& z, float top, float inv) {
+  if (v == v2 && b == b2) return true;
+  if (!keys) return v > v2;
+  const float k = quick_key(v, b, z, top, inv), k2 = quick_key(v2, b2, z, top, inv);
+  return k - k2 > key_error(k, z.sigmoid) + key_error(k2, z.sigmoid);
+}
 // fp32 as unsigned numbers of the same order; no finite number is 0.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -276,7 +296,8 @@ __device__ __forceinline__ T rank_groups(const T (&key)[kPer], const Sizes& z, i
   return sum;
 }
 
-// Can the key of a smaller number, exactly, be the larger one's or more?
+// Can the key of a smaller number, exactly, be the larger one's or more?  (By what the
+// two numbers' lost bits leave open: the smallest distance of the two.)
 template <uint32_t kIndex>
 __device__ __forceinline__ bool may_pass(uint32_t small, uint32_t large, bool keys,
                                          const Sizes& z) {
@@ -287,10 +308,10 @@ __device__ __forceinline__ bool may_pass(uint32_t small, uint32_t large, bool ke
 // The choice by fp32 keys.  A key is an ordered number whose low bits are
 // replaced by the expert, counted down, so that a maximum of 32-bit numbers finds
 // both, and equal ones by the lowest expert.  Lane l holds experts kPer l + 0 ..
-// kPer - 1.  Sets `unsure` where two neighbours of the order, down to the first
-// one left out, lie nearer than the keys' errors (cut bits included) and are not
-// equal logits with equal biases: the row is then chosen exactly.  Where the first one
-// left out equals the last one chosen, so do all that lie as near to them.
+// kPer - 1.  Sets `unsure` where two neighbours of the order, down to the first one
+// left out, may lie nearer than the keys' errors (cut bits included) and turn out so by
+// their whole keys, but for equal logits with equal biases: the row is then chosen
+// exactly.  Of those left out, all that may reach the last one chosen are looked at.
 template <int kPer>
 __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
                                               const void* __restrict__ logits, int64_t row_at,
@@ -299,10 +320,10 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
   constexpr uint32_t kIndex = 64 * kPer - 1;  // bits of an expert
   const bool scores = bias || z.groups > 1;
   float key[kPer];
+  float top = 0.f, inv = 1.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) key[i] = x[i];
   if (scores) {
-    float top = 0.f, inv = 1.f;
     if (!z.sigmoid) {
       float t = x[0];
 #pragma unroll
@@ -316,11 +337,7 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (x[i] == -INFINITY) continue;
-      key[i] = z.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : __expf(x[i] - top) * inv;
-      if (bias) {
-        const float b = bias[kPer * lane + i];
-        key[i] = b != b ? -INFINITY : key[i] + fminf(b, FLT_MAX);
-      }
+      key[i] = quick_key(x[i], load_bias(bias, kPer * lane + i), z, top, inv);
     }
   }
   unsure = false;
@@ -365,29 +382,22 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
   }
   const bool here = lane < z.topk && mine != 0;
   const int id = here ? (int)(kIndex - (mine & kIndex)) : -1;
-  if (here && next != 0) {
+  if (here && next != 0 && may_pass<kIndex>(next, mine, bias != nullptr, z)) {
     const int other = (int)(kIndex - (next & kIndex));
-    const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
-    const float error = bias ? key_error(hi, z.sigmoid) + key_error(lo, z.sigmoid) : 0.f;
-    bool near = hi - lo <= error || (mine & ~kIndex) == (next & ~kIndex);
-    // Is what was cut off nothing, or the two the same?
-    if (near) {
-      const float a = load_logit(logits, z.f32, row_at + id);
-      const float b = load_logit(logits, z.f32, row_at + other);
-      near = a != b || (bias && bias[id] != bias[other]);
-      if (!bias && near) near = (mine & ~kIndex) == (next & ~kIndex);
-    }
-    unsure |= near;
+    unsure |= !before(load_logit(logits, z.f32, row_at + id), load_bias(bias, id),
+                      load_logit(logits, z.f32, row_at + other), load_bias(bias, other),
+                      bias != nullptr, z, top, inv);
   }
   const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)mine, z.topk - 1);
   const uint32_t out = (uint32_t)__builtin_amdgcn_readlane((int)next, z.topk - 1);
   if (out != 0 && may_pass<kIndex>(out, last, bias != nullptr, z)) {
     const int at = (int)(kIndex - (last & kIndex));
-    const float v = load_logit(logits, z.f32, row_at + at), b = bias ? bias[at] : 0.f;
+    const float v = load_logit(logits, z.f32, row_at + at), b = load_bias(bias, at);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (u[i] != 0 && may_pass<kIndex>(u[i], last, bias != nullptr, z))
-        unsure |= x[i] != v || (bias && bias[kPer * lane + i] != b);
+        unsure |= !before(v, b, x[i], load_bias(bias, kPer * lane + i), bias != nullptr, z, top,
+                          inv);
   }
   unsure = __ballot(unsure) != 0;
   return id;
@@ -623,11 +633,8 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
     if (scores) {
       const float inv = __builtin_amdgcn_rcpf(total);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float s =
-            z.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : __expf(x[i] - top) * inv;
-        key[i] = x[i] > -INFINITY ? s + b[i] : -INFINITY;
-      }
+      for (int i = 0; i < kPer; ++i)
+        key[i] = x[i] > -INFINITY ? quick_key(x[i], b[i], z, top, inv) : -INFINITY;
     }
     bool unsure = false;
     if (z.groups > 1) {  // of 2^n lanes
@@ -715,14 +722,9 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
     float v = 0.f;
     if (id >= 0) v = load_logit(logits, z.f32, r * stride + id);
     bool near = false;  // the order of this one and the next is open
-    if (loose && ql < z.topk && next != 0) {
-      const float hi = unordered(mine | kIndex), lo = unordered(next & ~kIndex);
-      const float error = key_error(hi, z.sigmoid) + key_error(lo, z.sigmoid);
-      if ((mine & ~kIndex) == (next & ~kIndex) || (bias && hi - lo <= error)) {
-        const int other = (int)(kIndex - (next & kIndex));
-        near = v != load_logit(logits, z.f32, r * stride + other) ||
-               (bias && bias[id] != bias[other]);
-      }
+    if (loose && ql < z.topk && next != 0 && may_pass<kIndex>(next, mine, bias != nullptr, z)) {
+      const int other = (int)(kIndex - (next & kIndex));
+      near = v != load_logit(logits, z.f32, r * stride + other) || (bias && bias[id] != bias[other]);
     }
     // Where the first one left out equals the last one chosen, so must all that lie as
     // near to them.
@@ -732,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       const uint32_t last = (uint32_t)__shfl((int)mine, from, kWave);
       const float lv = __shfl(v, from, kWave);
       const int lid = __shfl(id, from, kWave);
-      const float lb = bias && lid >= 0 ? fminf(bias[lid], FLT_MAX) : 0.f;
+      const float lb = lid >= 0 ? load_bias(bias, lid) : 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (u[i] != 0 && u[i] < last && may_pass<kIndex>(u[i], last, bias != nullptr, z))

@@ -1,0 +1,90 @@
+"""moe_router's choice where keys are hard to tell apart, exactly, against the float64
+oracle, on every path: four rows to a wave (up to 256 experts and 14 choices), a wave
+to a row, and groups that no path in fp32 takes."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import expanded_dispatch_layout_amd as M  # noqa: E402
+from oracle import block as B  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def choice(x, topk, bias=None, score="softmax", groups=1, topk_groups=1, dtype=F32):
+    """Ids for the rows x as they are and for the same rows apart and off 16 bytes."""
+    rows, E = x.shape
+    held = torch.full((rows, E + 3), float("nan"), dtype=dtype, device="cuda")
+    b = None if bias is None else torch.from_numpy(bias).float().cuda()
+    got = []
+    for view in (held[:, 1:1 + E], torch.empty((rows, E), dtype=dtype, device="cuda")):
+        view.copy_(torch.from_numpy(x))
+        ids = torch.full((rows, topk), -9, dtype=torch.int32, device="cuda")
+        M.moe_router(view, ids, torch.empty((rows, topk), device="cuda"), b, score, groups,
+                     topk_groups)
+        got.append(ids.cpu().numpy())
+    assert np.array_equal(*got)
+    return got[0]
+
+
+def keys(x, bias, score):
+    return np.exp(B.log_scores(B.clean(x), score)) + bias.astype(np.float64)
+
+
+# ------------------------------------------------------------- near keys
+
+def pairs_on_edges(rng, rows, E, levels, score):
+    """Logits and biases (as fp32) whose 2 * levels largest keys are pairs about
+    multiples of 2^-13, a border of the numbers that are compared first for any number
+    of experts: within some 2^-25 of it, on either side."""
+    if score == "sigmoid":
+        bias, lo, hi = rng.uniform(-0.25, 0.25, E), 0.45, 1.1
+    else:                                            # scores of 0.01 to 0.04 beside biases
+        bias, lo, hi = rng.uniform(0.5, 0.505, E), 0.515, 0.54
+        bias[E - 1] = -1.0                           # takes what the others leave
+    bias = bias.astype(np.float32)
+    x = np.empty((rows, E))
+    grid = np.arange(int(lo * 2 ** 13), int(hi * 2 ** 13))
+    for r in range(rows):
+        level = np.repeat(rng.choice(grid, levels, replace=False) / 2.0 ** 13, 2)
+        at = rng.permutation(E - 1)[:2 * levels]
+        s = level - bias[at].astype(np.float64)
+        if score == "sigmoid":
+            at, s = at[(s > 0.03) & (s < 0.97)], s[(s > 0.03) & (s < 0.97)]
+            x[r] = -12.0                             # a key below 0.25 + 1e-5
+            x[r, at] = np.log(s / (1 - s))
+        else:
+            x[r] = np.log(1e-9)
+            x[r, at] = np.log(s)
+            x[r, E - 1] = np.log(1 - s.sum() - 1e-9 * (E - 1 - len(at)))
+    step = rng.integers(-1, 2, x.shape)
+    x = x.astype(np.float32)
+    return x + (step * np.spacing(np.abs(x))).astype(np.float32), bias
+
+
+@pytest.mark.parametrize("E", [64, 100, 128, 200, 256, 300, 512, 1024])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_near_keys_on_both_sides_of_a_border(E, score):
+    """The order of each pair, and which of a pair is the last one chosen.
+
+    The oracle's score, exp of a logarithm l of size below 24, is off by 2^-53 (3 * 24 + 2)
+    at most and a key near 1 by half a step more, the kernel's by less: keys that lie
+    within 2 * (2^-46 + 2^-53) of each other may come in either order."""
+    for topk in (1, 7, 8, 13, 14, 15, 16):
+        print(f"[edges {E} {score} top {topk}]", flush=True)
+        rng = np.random.default_rng(E + topk)
+        x, bias = pairs_on_edges(rng, 301, E, topk // 2 + 1, score)
+        got = choice(x, topk, bias, score)
+        want, _ = B.router(x, topk, bias, score)
+        key = keys(x, bias, score)
+        d = np.take_along_axis(key, got, 1) - np.take_along_axis(key, want, 1)
+        bad = np.nonzero((np.abs(d) > 2.0 ** -44).any(axis=1))[0]
+        assert len(bad) == 0, (len(bad), bad[:3], got[bad[:3]], want[bad[:3]])
+        assert all(len(set(row)) == topk and (row >= 0).all() for row in got)

@@ -101,6 +101,13 @@ __device__ __forceinline__ void load_row(const void* __restrict__ logits, const 
   }
 }
 
+// Logits that are compared as they are: -0 becomes +0, which it is equal to.
+template <int kPer>
+__device__ __forceinline__ void one_zero(float (&x)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] += 0.0f;
+}
+
 // Scores' common factor of a row: maximum and sum of softmax.
 template <int kPer>
 __device__ __forceinline__ void softmax_stats(const float (&x)[kPer], float& top, float& total) {
@@ -500,6 +507,7 @@ __device__ __forceinline__ void route_row(const void* __restrict__ logits, int64
                                           float* __restrict__ weights) {
   float x[kPer];
   load_row<kPer>(logits, z, r * stride, lane, x);
+  if (!bias) one_zero(x);
   int id = -1;
   bool unsure = true;
   if constexpr (kQuick) {
@@ -616,6 +624,7 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       for (int i = 0; i < kPer; ++i)
         x[i] = kPer * ql + i < z.E ? load_logit(logits, z.f32, at + i) : -INFINITY;
     }
+    if (!bias) one_zero(x);
     float top = 0.f, total = 1.f;
     if (!z.sigmoid && (scores || !z.normalize)) {
       top = x[0];

@@ -88,3 +88,25 @@ def test_near_keys_on_both_sides_of_a_border(E, score):
         bad = np.nonzero((np.abs(d) > 2.0 ** -44).any(axis=1))[0]
         assert len(bad) == 0, (len(bad), bad[:3], got[bad[:3]], want[bad[:3]])
         assert all(len(set(row)) == topk and (row >= 0).all() for row in got)
+
+
+# ---------------------------------------------------------- signed zeros
+
+@pytest.mark.parametrize("E", [5, 8, 60, 64, 100, 128, 256, 300, 512, 1024])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_zeros_of_either_sign_are_equal(E, dtype):
+    rng = np.random.default_rng(E)
+    x = np.where(rng.random((203, E)) < 0.5, -0.0, 0.0)
+    x[100:150][rng.random((50, E)) < 2 / E] = 1.0
+    x[150:][rng.random((53, E)) < 0.5] = -2.0 ** -126    # the zeros lead
+    for topk in sorted({1, 2, min(E, 8), min(E, 16), min(E, 32)}):
+        print(f"[zeros {E} {dtype} top {topk}]", flush=True)
+        for score in ("softmax", "sigmoid"):
+            want, _ = B.router(x, topk, None, score)
+            assert np.array_equal(choice(x, topk, None, score, dtype=dtype), want)
+        zero = np.where(rng.random(E) < 0.5, -0.0, 0.0)
+        assert np.array_equal(choice(x[:100], topk, zero, "sigmoid", dtype=dtype),
+                              B.router(x[:100], topk, zero, "sigmoid")[0])
+        if E % 4 == 0 and topk <= E // 2:
+            assert np.array_equal(choice(x[:150], topk, None, "softmax", 4, 2, dtype),
+                                  B.router(x[:150], topk, None, "softmax", 4, 2)[0])

@@ -26,6 +26,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -272,9 +274,17 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u ^ ((uint32_t)~((int)u >> 31) | 0x80000000u));
 }
 
+// How far a group's sum of its two largest keys may be off: by both keys' errors (of
+// which a sum that cancels shows nothing) and its own rounding, 1; 4 is taken.  The
+// errors grow more slowly than the keys, so that this holds also where other two are the
+// largest exactly.
+__device__ __forceinline__ float sum_error(float first, float second, float sum, bool sigmoid) {
+  return key_error(first, sigmoid) + (second > -INFINITY ? key_error(second, sigmoid) : 0.f) +
+         0x1p-22f * fabsf(sum);
+}
 // Groups of 2^n lanes (kPer experts to a lane): each lane's two largest keys, then
 // its group's.  Returns the sum of the group's two, -inf without any; rank: how
-// many groups come before it.
+// many groups come before it; error (fp32 keys): sum_error.
 // In fp32 a sum past the range stays finite: biases of the lowest value are still keys.
 __device__ __forceinline__ float sum_of_two(float a, float b) {
   return fminf(fmaxf(a + b, -FLT_MAX), FLT_MAX);
@@ -282,7 +292,7 @@ __device__ __forceinline__ float sum_of_two(float a, float b) {
 __device__ __forceinline__ double sum_of_two(double a, double b) { return a + b; }
 template <typename T, int kPer>
 __device__ __forceinline__ T rank_groups(const T (&key)[kPer], const Sizes& z, int lane,
-                                         int lanes, int& rank) {
+                                         int lanes, int& rank, float& error) {
   T m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -295,6 +305,7 @@ __device__ __forceinline__ T rank_groups(const T (&key)[kPer], const Sizes& z, i
     m1 = max(m1, o1);
   }
   const T sum = m2 > (T)-INFINITY ? sum_of_two(m1, m2) : m1;
+  if constexpr (std::is_same<T, float>::value) error = sum_error(m1, m2, sum, z.sigmoid);
   rank = 0;
   for (int g = 0; g < z.groups; ++g) {
     const T other = lane_value(sum, g * lanes);
@@ -351,13 +362,14 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
   if (z.groups > 1) {
     const int lanes = z.E / z.groups / kPer;
     int rank;
-    const float sum = rank_groups<float, kPer>(key, z, lane, lanes, rank);
-    // The last group chosen and the first one left out.
+    float error;
+    const float sum = rank_groups<float, kPer>(key, z, lane, lanes, rank, error);
+    // The least that a group chosen may have, and the most of one left out.
     if (z.topk_groups < z.groups) {
-      const bool group = lane < z.groups * lanes;
-      const float a = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups - 1)));
-      const float b = lane_value(sum, __builtin_ctzll(__ballot(group && rank == z.topk_groups)));
-      unsure = b > -INFINITY && a - b <= 2 * (key_error(a, z.sigmoid) + key_error(b, z.sigmoid));
+      const bool group = lane < z.groups * lanes && sum > -INFINITY;
+      const float least = -wave_max_f(group && rank < z.topk_groups ? error - sum : -INFINITY);
+      const float most = wave_max_f(group && rank >= z.topk_groups ? sum + error : -INFINITY);
+      unsure = most > -INFINITY && !(least > most);
     }
     if (rank >= z.topk_groups) {
 #pragma unroll
@@ -448,7 +460,8 @@ __device__ __forceinline__ bool choose_closely(const float (&x)[kPer],
   }
   if (z.groups > 1) {
     int rank;
-    rank_groups<double, kPer>(key, z, lane, z.E / z.groups / kPer, rank);
+    float unused;
+    rank_groups<double, kPer>(key, z, lane, z.E / z.groups / kPer, rank, unused);
     if (rank >= z.topk_groups) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) key[i] = -INFINITY;
@@ -664,16 +677,14 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       const float sum = m2 > -INFINITY ? sum_of_two(m1, m2) : m1;
       const int g = ql / lanes;
       uint32_t u = sum > -INFINITY && g < z.groups ? (ordered(sum) & ~15u) | (15u - g) : 0u;
-      uint32_t best = 0, last = 0;
-      for (int k = 0; k <= z.topk_groups; ++k) {
-        last = best;
-        best = below(k, best, row_max_u(u - best));
-      }
-      // last: the topk_groups-th, best: the first one left out (0: none is).
-      const float lo = unordered(last & ~15u), hi = unordered(best | 15u);
-      unsure = best != 0 && z.topk_groups < z.groups &&
-               lo - hi <= 2 * (key_error(lo, z.sigmoid) + key_error(hi, z.sigmoid));
+      uint32_t last = 0;  // the topk_groups-th
+      for (int k = 0; k < z.topk_groups; ++k) last = below(k, last, row_max_u(u - last));
       bool in = u != 0 && u >= last;
+      // The least that a group chosen may have, and the most of one left out.
+      const float error = sum_error(m1, m2, sum, z.sigmoid);
+      const float least = -row_max_f(in ? error - sum : -INFINITY);
+      const float most = row_max_f(u != 0 && !in ? sum + error : -INFINITY);
+      unsure = most > -INFINITY && !(least > most);
       if (exact && __ballot(unsure)) {
         // fp64 sums of the two largest, from those that may be among them.
         float cut = m2 > -INFINITY ? m2 : m1;

@@ -110,3 +110,45 @@ def test_zeros_of_either_sign_are_equal(E, dtype):
         if E % 4 == 0 and topk <= E // 2:
             assert np.array_equal(choice(x[:150], topk, None, "softmax", 4, 2, dtype),
                                   B.router(x[:150], topk, None, "softmax", 4, 2)[0])
+
+
+# ------------------------------------------------------- sums that cancel
+
+@pytest.mark.parametrize("E,groups", [(16, 4), (64, 8), (128, 4), (256, 8), (256, 4), (60, 5),
+                                      (512, 8), (1024, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(E, groups, score):
+    """Two keys of a group near +B and -B, the others below: their sum is known to
+    their own errors, not to its own.  B is another one for each group, so that the
+    keys are far apart.  fp64 holds one near 2^28 to 2^-25, two of two groups 2^-23
+    together, and the sums here, of scores drawn at random, lie 2^-20 apart and more
+    (looked at)."""
+    rng = np.random.default_rng(E + groups)
+    per = E // groups
+    for size in (20.0, 1000.0, 2.0 ** 14, 2.0 ** 20, 2.0 ** 24):
+        low = -4 * size * groups
+        bias = np.full((groups, per), low)
+        for g in range(groups):
+            at = rng.permutation(per)[:2]
+            bias[g, at] = size * (g + 1), -size * (g + 1)
+        if size == 1000.0:
+            bias[0] = low                            # one that does not cancel, and is last
+        bias = bias.reshape(-1).astype(np.float32)
+        x = np.round(rng.normal(0, 1.5, (151, E)) * 256) / 256
+        if score == "softmax":
+            x[:, bias < low / 2] -= 6              # leaves the pairs scores worth telling
+        topk_groups = groups // 2
+        s = np.exp(B.log_scores(x, score)).reshape(151, groups, per)
+        two = np.where(bias.reshape(groups, per) > low / 2, s, 0).sum(axis=2)
+        two[:, (bias.reshape(groups, per) < low / 2).all(axis=1)] = -1
+        order = np.sort(two, axis=1)[:, ::-1]
+        told = order[:, topk_groups - 1] - order[:, topk_groups] > 2.0 ** -20
+        assert told.sum() > 120
+        x = x[told]
+        for topk in (topk_groups, min(2 * topk_groups, 32)):
+            print(f"[cancel {E} {groups} {score} {size} top {topk}]", flush=True)
+            got = choice(x, topk, bias, score, groups, topk_groups)
+            want, _ = B.router(x, topk, bias, score, groups, topk_groups)
+            of = lambda ids: np.sort(np.unique(ids // per))  # noqa: E731
+            bad = [r for r in range(len(x)) if not np.array_equal(of(got[r]), of(want[r]))]
+            assert not bad, (len(bad), got[bad[:3]], want[bad[:3]])

@@ -323,6 +323,22 @@ __device__ __forceinline__ bool may_pass(uint32_t small, uint32_t large, bool ke
   return hi - lo <= (keys ? key_error(hi, z.sigmoid) + key_error(lo, z.sigmoid) : 0.f);
 }
 
+// Without a bias but with groups the fp64 scores are in the order of the logits, unless
+// fp64 holds two of them as one number: near 1 (sigmoid), below its range, or next to each
+// other.  Is that possible for the logit of `mine` and that of `next`, or, where these are
+// the same, another one below it?  (Scores that are told apart here differ by 2^-34 of
+// themselves, of 1 for the sigmoid: 2^18 steps of fp64.)
+template <uint32_t kIndex>
+__device__ __forceinline__ bool one_score(uint32_t mine, uint32_t next, const Sizes& z,
+                                          float top) {
+  const uint32_t at = mine & ~kIndex;
+  const float hi = unordered(at);
+  const float lo = at != (next & ~kIndex) ? unordered(next | kIndex)
+                                          : unordered(at - (z.f32 ? 1u : 0x10000u));
+  const float slope = z.sigmoid ? __expf(-fmaxf(hi, 0.f)) : 1.f;
+  return !((hi - lo) * slope > 0x1p-32f && lo - (z.sigmoid ? 0.f : top) > -600.f);
+}
+
 // The choice by fp32 keys.  A key is an ordered number whose low bits are
 // replaced by the expert, counted down, so that a maximum of 32-bit numbers finds
 // both, and equal ones by the lowest expert.  Lane l holds experts kPer l + 0 ..
@@ -376,8 +392,10 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
       for (int i = 0; i < kPer; ++i) key[i] = -INFINITY;
     }
   }
-  // Without a bias the order is the logits', also between the groups chosen.
-  if (!bias && z.groups > 1) {
+  // Without a bias the order is the logits', also between the groups chosen, if no two
+  // have one score.
+  const bool by_logits = !bias && z.groups > 1;
+  if (by_logits) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) key[i] = key[i] > -INFINITY ? x[i] : -INFINITY;
   }
@@ -407,6 +425,7 @@ __device__ __forceinline__ int choose_quickly(const float (&x)[kPer],
                       load_logit(logits, z.f32, row_at + other), load_bias(bias, other),
                       bias != nullptr, z, top, inv);
   }
+  if (by_logits && here && next != 0) unsure |= one_score<kIndex>(mine, next, z, top);
   const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)mine, z.topk - 1);
   const uint32_t out = (uint32_t)__builtin_amdgcn_readlane((int)next, z.topk - 1);
   if (out != 0 && may_pass<kIndex>(out, last, bias != nullptr, z)) {
@@ -717,7 +736,7 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
           rank += other > both || (other == both && j < g);
         }
         in = u != 0 && rank < z.topk_groups;
-        unsure = false;
+        unsure = unsure && !z.sigmoid && least < 0x1p-100f;  // (with softmax's sum, then)
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) key[i] = in && key[i] > -INFINITY ? (bias ? key[i] : x[i])
@@ -746,6 +765,8 @@ __global__ __launch_bounds__(kThreads) void router_quad_kernel(
       const int other = (int)(kIndex - (next & kIndex));
       near = v != load_logit(logits, z.f32, r * stride + other) || (bias && bias[id] != bias[other]);
     }
+    if (!bias && z.groups > 1 && ql < z.topk && next != 0)
+      unsure |= one_score<kIndex>(mine, next, z, top);
     // Where the first one left out equals the last one chosen, so must all that lie as
     // near to them.
     if (loose && __ballot(ql == z.topk - 1 && next != 0 && !near &&

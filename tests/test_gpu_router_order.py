@@ -152,3 +152,33 @@ def test_group_sums_that_cancel(E, groups, score):
             of = lambda ids: np.sort(np.unique(ids // per))  # noqa: E731
             bad = [r for r in range(len(x)) if not np.array_equal(of(got[r]), of(want[r]))]
             assert not bad, (len(bad), got[bad[:3]], want[bad[:3]])
+
+
+# ---------------------------------------------- scores that are one number
+
+@pytest.mark.parametrize("E,groups", [(16, 4), (64, 4), (128, 8), (256, 8), (256, 2), (60, 4),
+                                      (160, 8), (512, 8), (1024, 2), (7, 7)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_equal_scores_of_different_logits(E, groups, dtype):
+    """With groups it is the scores that are compared: sigmoids of 40, 50 and 60 are 1,
+    those of -800 and -900 are 0, and so are softmax's beside a 0; the lowest expert
+    comes first.  Without groups and bias the logits are."""
+    rng = np.random.default_rng(E)
+    for score, some in (("sigmoid", [40.0, 50.0, 60.0, 2.0, 1.0, -1.0]),
+                        ("sigmoid", [-800.0, -900.0, -1000.0, -2.0]),
+                        ("softmax", [0.0, -800.0, -900.0, -1000.0]),
+                        ("softmax", [1000.0, 20.0, 10.0, float("inf"), -float("inf")])):
+        x = rng.choice(some, (101, E))
+        x[:, 0] = some[0]
+        if len(some) == 4 and score == "softmax":
+            x[50:, 1:] = rng.choice(some[1:], (51, E - 1))
+        for topk_groups in sorted({1, groups // 2, groups}):
+            for topk in sorted({1, min(8, E // groups * topk_groups),
+                                min(20, E // groups * topk_groups)}):
+                print(f"[equal scores {E} {groups} {topk_groups} {score} {dtype} top {topk}]",
+                      flush=True)
+                got = choice(x, topk, None, score, groups, topk_groups, dtype)
+                want, _ = B.router(x, topk, None, score, groups, topk_groups)
+                assert np.array_equal(got, want)
+        got = choice(x, min(8, E), None, score, dtype=dtype)
+        assert np.array_equal(got, B.router(x, min(8, E), None, score)[0])

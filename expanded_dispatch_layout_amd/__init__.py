@@ -518,7 +518,7 @@ def _need_rows(fn, name, t, dtypes, shape, gpu):
     if t.get_device() != gpu:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
     if rows <= 1:
-        return max(row, cols)    # the distance to a row that is not there
+        return cols              # there is no second row to be away from
     if row < cols:
         raise ValueError(f"{fn}: {name} has rows that overlap")
     return row

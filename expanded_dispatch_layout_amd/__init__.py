@@ -941,7 +941,8 @@ class StandardW4MoE(StandardBf16MoE):
     """The standard path with 4-bit weights: as StandardBf16MoE, the products
     from w13 [E, 2I, H/2] and w2 [E, H, I/2] uint8 (two codes a byte) with
     w13_scale [E, 2I, H/group] and w2_scale [E, H, I/group].  fmt 'int4' (bf16
-    scales, group 32, 64 or 128) or 'mxfp4' (UE8M0 bytes, group 32)."""
+    scales, group 32, 64 or 128) or 'mxfp4' (UE8M0 bytes, group 32).  H and I are
+    multiples of 128 (StandardBf16MoE: of 64)."""
 
     def __init__(self, rows, topk, w13, w13_scale, w2, w2_scale, fmt, align=128,
                  routed_scaling_factor=1.0, device="cuda"):
@@ -949,6 +950,9 @@ class StandardW4MoE(StandardBf16MoE):
         if E2 != E or H != 2 * half or two_i != 4 * half_i:
             raise ValueError(f"StandardW4MoE: w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} "
                              "are not [E, 2I, H/2] and [E, H, I/2]")
+        if H % 128 or two_i % 256:
+            raise ValueError(f"StandardW4MoE: H {H} and I {two_i // 2} must be multiples of 128 "
+                             "(moe_grouped_gemm_w4's)")
         W4[fmt]
         # The buffers are the bf16 path's, sized by w13's shape alone.
         sizes = w13[:, :, :1].expand(E, two_i, H)

@@ -25,3 +25,21 @@ def test_rows_apart_keep_their_distance():
     for bad in (held[:, ::2][:, :100], held.t(), held[:1].expand(5, 272)):
         with pytest.raises(ValueError):
             M._need_rows("f", "x", bad, (torch.bfloat16,), bad.shape, CPU)
+
+
+@pytest.mark.parametrize("H,inter", [(256, 64), (256, 192), (192, 128), (64, 256)])
+def test_w4_layer_refuses_sizes_that_its_products_refuse(H, inter):
+    """When it is built, not at the first call."""
+    w13 = torch.zeros((2, 2 * inter, H // 2), dtype=torch.uint8)
+    w2 = torch.zeros((2, H, inter // 2), dtype=torch.uint8)
+    s13, s2 = (torch.zeros((2, w.shape[1], w.shape[2] // 16), dtype=torch.uint8) for w in (w13, w2))
+    with pytest.raises(ValueError, match="multiples of 128"):
+        M.StandardW4MoE(8, 2, w13, s13, w2, s2, "mxfp4", device="cpu")
+
+
+def test_w4_layer_takes_multiples_of_128():
+    w13 = torch.zeros((2, 768, 64), dtype=torch.uint8)
+    w2 = torch.zeros((2, 128, 192), dtype=torch.uint8)
+    s13, s2 = (torch.zeros((2, w.shape[1], w.shape[2] // 16), dtype=torch.uint8) for w in (w13, w2))
+    moe = M.StandardW4MoE(8, 2, w13, s13, w2, s2, "mxfp4", device="cpu")
+    assert (moe.H, moe.I, moe.E) == (128, 384, 2)

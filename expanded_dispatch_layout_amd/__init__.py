@@ -1032,7 +1032,8 @@ class MoEBlock:
         """Returns (the experts' output [rows, H] bf16, the residual stream: x, or
         x + branch in self.sum).  A next block takes the stream as its x and the
         output as its branch."""
-        self.h = x if branch is None else self.sum
+        self.h = None    # until the buffers are all of this call
+        h = x if branch is None else self.sum
         y, logits = self.y[:self.rows], self.logits[:self.rows, :self.E]
         moe_layer_norm(x, self.weight, y, self.bias, branch, None if branch is None else self.sum,
                        self.mean, self.rstd, self.kind, self.eps, psum_recv_per_rank, stream)
@@ -1041,14 +1042,16 @@ class MoEBlock:
         moe_router(logits, self.topk_ids, self.topk_weights, self.select_bias,
                    psum_recv_per_rank=psum_recv_per_rank, stream=stream, **self.route,
                    **self.groups)
-        return self.moe(y, self.topk_ids, self.topk_weights, psum_recv_per_rank, out,
-                        stream), self.h
+        out = self.moe(y, self.topk_ids, self.topk_weights, psum_recv_per_rank, out, stream)
+        self.h = h
+        return out, h
 
     def backward(self, dout, dsum=None, psum_recv_per_rank=None, dx=None, accumulate=False,
                  stream=None):
         """Gradient of the last forward call with respect to its residual stream (x,
         and the branch, if it had one), from the output's (dout) and the stream's
-        own (dsum, or None).  Returns dx [rows, H] of the stream's type."""
+        own (dsum, or None).  Returns dx [rows, H] of the stream's type.  After a
+        forward call that was refused there is none (RuntimeError)."""
         if not isinstance(self.moe, TrainableBf16MoE):
             raise TypeError("MoEBlock: backward() needs a TrainableBf16MoE")
         if self.h is None:

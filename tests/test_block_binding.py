@@ -43,3 +43,55 @@ def test_w4_layer_takes_multiples_of_128():
     s13, s2 = (torch.zeros((2, w.shape[1], w.shape[2] // 16), dtype=torch.uint8) for w in (w13, w2))
     moe = M.StandardW4MoE(8, 2, w13, s13, w2, s2, "mxfp4", device="cpu")
     assert (moe.H, moe.I, moe.E) == (128, 384, 2)
+
+
+CALLS = ["moe_layer_norm", "moe_grouped_gemm_bf16", "moe_router", "moe_router_backward",
+         "moe_grouped_wgrad_bf16", "moe_grouped_dgrad_bf16", "moe_layer_norm_backward"]
+
+
+class Experts(M.TrainableBf16MoE):
+    """Stands in for the experts: hands on what it gets."""
+
+    def __init__(self, rows, topk, E, H):
+        self.rows, self.topk, self.E, self.H = rows, topk, E, H
+
+    def __call__(self, y, ids, weights, psum, out, stream):
+        if getattr(self, "refuses", False):
+            raise ValueError("refused")
+        return y
+
+    def backward(self, dout, weights, psum, accumulate, stream):
+        return dout, weights
+
+
+@pytest.mark.parametrize("refused", ["moe_layer_norm", "moe_grouped_gemm_bf16", "moe_router", None])
+def test_no_gradient_of_a_forward_call_that_was_refused(monkeypatch, refused):
+    """The buffers are then of two calls."""
+    for name in CALLS:
+        monkeypatch.setattr(M, name, lambda *a, **k: None)
+    rows, E, H = 5, 6, 128
+    x, branch = torch.zeros((rows, H), dtype=torch.bfloat16), torch.ones(1)
+    block = M.MoEBlock(Experts(rows, 2, E, H), torch.zeros((E, H), dtype=torch.bfloat16),
+                       torch.ones(H))
+    with pytest.raises(RuntimeError):
+        block.backward(x)
+    for b, stream in ((None, x), (branch, block.sum)):
+        out, h = block(x, b)
+        assert h is stream and block.h is stream
+        block.backward(x, dx=torch.empty_like(x))
+
+    def no(*a, **k):
+        raise ValueError("refused")
+
+    with monkeypatch.context() as m:
+        if refused:
+            m.setattr(M, refused, no)
+        else:
+            block.moe.refuses = True
+        with pytest.raises(ValueError, match="refused"):
+            block(x)
+        block.moe.refuses = False
+    with pytest.raises(RuntimeError):
+        block.backward(x, dx=torch.empty_like(x))
+    block(x)
+    block.backward(x, dx=torch.empty_like(x))

@@ -887,8 +887,14 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(
     if (z.sigmoid) own = w * (1.0f / (1.0f + expf(v))) * (z.normalize ? g - dot : g);
     else own = w * (z.normalize ? g - dot : g);
     if (dense) {
+      const float f = -inv * dot;
+      if (fabsf(f) < INFINITY) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) d[i] *= -inv * dot;
+        for (int i = 0; i < kPer; ++i) d[i] *= f;
+      } else {  // experts that are not available get 0 all the same
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) d[i] = d[i] > 0.f ? d[i] * f : 0.f;
+      }
     }
     for (int k = 0; k < z.topk; ++k) {
       const int e = __builtin_amdgcn_readlane(id, k);

@@ -67,19 +67,11 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8])
   }
 }
 
-// The same, past the caches.
-template <bool kF32>
+// The same in bf16, past the caches.
 __device__ __forceinline__ void store8_once(void* p, int64_t at, const float (&v)[8]) {
-  if constexpr (kF32) {
-    __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]},
-                                reinterpret_cast<v4f*>((float*)p + at));
-    __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]},
-                                reinterpret_cast<v4f*>((float*)p + at + 4));
-  } else {
-    __builtin_nontemporal_store(u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]),
-                                      pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])},
-                                reinterpret_cast<u32x4*>((uint16_t*)p + at));
-  }
+  __builtin_nontemporal_store(
+      u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])},
+      reinterpret_cast<u32x4*>((uint16_t*)p + at));
 }
 
 // A gain or bias vector, bf16 or fp32 (the same for every row: from the caches).
@@ -192,8 +184,10 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(
 // ------------------------------------------------------------ backward
 
 constexpr int kBackThreads = 512, kBackWaves = kBackThreads / kWave;
-// dx beyond this goes past the caches: nothing of it would be left for its reader
-// (16384 rows of 7168: 227 us with plain stores, 211 so).
+// bf16 dx beyond this goes past the caches: nothing of it would be left for its reader
+// (16384 rows of 7168, two gradients and the stream's: 227 us with plain stores, 210 so;
+// 12288 rows, one gradient: 106 and 98).  fp32 gains nothing for sure (16384 rows of 7168:
+// 347 and 344; of 6144, one gradient: 194 and 201; 32768 of 2048: 204 and 197).
 constexpr int64_t kCached = 128 << 20;
 constexpr int kParts = 256;  // workgroups, and partial sums of the weight's gradient
 
@@ -316,8 +310,14 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(
           if constexpr (kSum) o[i] += s.ds[u][c].get(i);
         }
         if (ok[c]) {
-          if (once) store8_once<kF32>(dx, r * hidden + at[c], o);
-          else store8<kF32>(dx, r * hidden + at[c], o);
+          if (!kF32 && once) {
+            // (Set apart: the compiler joins the two branches otherwise, as plain stores.)
+            asm volatile("; past the caches");
+            store8_once(dx, r * hidden + at[c], o);
+            asm volatile("; past the caches");
+          } else {
+            store8<kF32>(dx, r * hidden + at[c], o);
+          }
         }
       }
     }

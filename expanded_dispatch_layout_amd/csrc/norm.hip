@@ -14,7 +14,7 @@
 // Forward: a wave or a workgroup per row, by its length.  16384 rows of 6144, fp32
 // stream with a branch: 245 us, 4.9 TB/s, the rate of a plain copy (accesses past the
 // caches: 254 to 262).  Backward: 16384 rows of 7168 in bf16, two gradients and the
-// stream's: 211 us, 5.6 TB/s, of which 7.5 join the weight's gradient.
+// stream's: 211 us, 5.6 TB/s, of which 7.4 join the weight's gradient.
 #include <initializer_list>
 
 #include "lds_dma.hpp"
@@ -193,9 +193,9 @@ constexpr int kParts = 256;  // workgroups, and partial sums of the weight's gra
 
 // kTeam waves share a row, kU rows at a time; a thread holds kCh chunks of 8
 // columns, and over all its rows the sums of its columns' dw and db.  The next rows
-// are asked for before the present ones are worked on (16384 rows of 7168: 246 us
-// without, 227 so; two rows at a time spill at this width: 519).  The workgroup's sums go to
-// its own place in the workspace (512 workgroups in place of 256: 247).
+// are asked for before the present ones are worked on (16384 rows of 7168, plain stores:
+// 246 us without, 227 so; two rows at a time spill at this width: 519).  The workgroup's
+// sums go to its own place in the workspace (512 workgroups in place of 256: 247).
 // Loads are not conditional, so that the compiler can count them: columns and rows past
 // the end repeat the last ones, with a gradient of 0.  (Where those hold a NaN, the sums
 // have one already.)

@@ -15,9 +15,9 @@
 // columns, and is scaled in fp32 once its group is complete.
 //
 // One token's eight experts, 4096 x 7168, MXFP4: 31 us, 4.0 TB/s (a plain sum over as
-// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 413 us, 1.17 PFLOP/s;
-// int4 772 us (a quarter to a half more MFMAs and a quarter of the tile, since the
-// scaled sums need the registers).
+// many bytes takes longer).  8192 rows, 8 x 4096 x 7168: MXFP4 413 to 435 us, 1.11 to 1.17
+// PFLOP/s; int4 of 128 797 us (half more MFMAs, 8 beside 16, and a quarter of the tile,
+// since the scaled sums need the registers).
 #include "gemm_backward.hpp"
 
 namespace moe {
@@ -143,7 +143,10 @@ __device__ __forceinline__ int rows_of(const Shared& sh, const Args& p, int e, i
   return en > st ? (int)(en - st) : 0;
 }
 
-// The row groups of every kind.  Experts of up to 32 rows are narrow.  The others
+// The row groups of every kind.  Experts of up to 32 rows are narrow, if the scales of
+// their items fit (p.fits: K up to 4736 for int4 of 32, 9472 for MXFP4 and int4 of 64,
+// 18944 for int4 of 128; one token's 8 products of 4096 x 9472 and x 9600 in MXFP4: 38 and
+// 98 us).  The others
 // are all narrow or all wide, by the rounds that the workgroups make of their
 // 128-column tiles of 32 or 128 rows, which take about 0.55 and 1.3 us for 128 of the
 // reduction (weights of 8 x 4096 x 7168 in MXFP4, narrow / wide: 40 rows each 68 / 82 us,

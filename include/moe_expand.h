@@ -747,8 +747,9 @@ moe_status moe_layer_norm_backward(
  * never chosen, and a NaN or -inf logit has score 0.  +inf counts as the
  * largest finite fp32 value.  Slots for which no expert is left (all of them
  * in a row without any) get id -1 and weight 0.  Without a bias and groups
- * the experts are compared by their logits, otherwise by fp64 scores (and sums of
- * scores), which are told apart down to fp64's own rounding.  A bias of the lowest
+ * the experts are compared by their logits (-0 and +0 are equal), otherwise by fp64
+ * scores (and sums of scores), which are told apart down to fp64's own rounding: logits
+ * whose scores fp64 holds as one number are equal then.  A bias of the lowest
  * fp32 value is a key like others; only -inf and NaN exclude an expert.  Rows >= R_v
  * are neither read nor written.
  * Sizes: 1 <= topk <= min(num_experts, MOE_MAX_TOPK), num_experts <=
